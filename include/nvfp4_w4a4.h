@@ -61,7 +61,8 @@ typedef enum {
 
 typedef enum {
     NVFP4_DTYPE_F32 = 0,
-    NVFP4_DTYPE_BF16 = 1
+    NVFP4_DTYPE_BF16 = 1,
+    NVFP4_DTYPE_E4M3 = 2      /* caches only: one code byte per element   */
 } nvfp4_dtype;
 
 typedef enum {
@@ -299,12 +300,169 @@ int fp8_kv_scale_from_amax(const float* amax, float* scale, void* stream);
 int fp8_kv_cast(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx,
                 const float* scale, uint8_t* out, int64_t ldo, void* stream);
 
+/*
+ * Paged KV cache.  K and V live in two arrays of n_pages pages of page_size
+ * tokens; element i of head h, token t of page p is at
+ *   p * page_stride + h * head_stride + t * token_stride + i
+ * (elements, unit stride along d) in either array: [page][head][token][d],
+ * [page][token][head][d] or views of a larger pool.  A cache is BF16, or
+ * E4M3 codes under static per-tensor decode scales as fp8_kv_cast makes
+ * them.  A token's slot is page * page_size + place in the page; a block
+ * table [n_requests][ld_table] lists the pages of each request in order.
+ * page_size is a multiple of 16 (a power of two or not).
+ *
+ * kv_page_tables -- block tables, positions and slots of one serving step
+ *   from the request lengths, in one launch without reading anything back.
+ *
+ *   new_lens, cached_lens  device, [n_requests]: tokens that the step adds to
+ *                each request and tokens that it holds (values below 0 count
+ *                as 0).  n_requests >= 1.
+ *   block_table  device, in/out, [n_requests][ld_table], the first max_blocks
+ *                columns of each row used.  Request r holds its first
+ *                ceil(cached / page_size) entries; the entries that it needs
+ *                more, up to column max_blocks, are written.
+ *   free_pages   device, [n_free] page ids, taken from the front in request
+ *                order (NULL allowed if n_free == 0).
+ *   n_tokens     tokens of the step, >= 0; at least the sum of new_lens
+ *                (entries past the sum are padding; tokens past n_tokens get
+ *                neither slot nor page entry).
+ *   cu_new       device, out, [n_requests + 1]: exclusive prefix sums of
+ *                new_lens.
+ *   kv_lens      device, out, [n_requests]: cached + new.
+ *   positions    device, out, [n_tokens]: position in its request of each
+ *                token, requests one after another; -1 for padding.
+ *   slots        device, out, [n_tokens]: its slot; -1 for padding, past
+ *                max_blocks and where no page is left.
+ *   pages_used   device, out, one int32: pages that the step needs.  More
+ *                than n_free: the entries past the list are -1.
+ * Calling it again with the same lengths writes the same values.
+ */
+int kv_page_tables(const int32_t* new_lens, const int32_t* cached_lens,
+                   int64_t n_requests, int32_t* block_table, int64_t max_blocks,
+                   int64_t ld_table, const int32_t* free_pages, int64_t n_free,
+                   int64_t page_size, int64_t n_tokens, int32_t* cu_new,
+                   int32_t* kv_lens, int32_t* positions, int64_t* slots,
+                   int32_t* pages_used, void* stream);
+
+/*
+ * kv_page_write -- write new keys and values into their slots.
+ *
+ *   k, v         device, [n_tokens][n_heads][d] of x_dtype (F32 or BF16) with
+ *                token and head strides in elements (columns of a fused
+ *                projection's output, say); 16-byte aligned, strides * size
+ *                multiples of 16.
+ *   k_cache, v_cache, cache_dtype  BF16 or E4M3, layout above; 16-byte
+ *                aligned, strides * size multiples of 16 bytes.
+ *   n_heads, d   key/value heads; d % 16 == 0, d <= 1024; n_tokens * n_heads
+ *                * d < 2^35.
+ *   k_scale, v_scale  device floats (finite, >= 0) for E4M3, else ignored.
+ *   slots        device, [n_tokens]; a slot outside [0, n_pages * page_size)
+ *                is skipped.  Equal slots: one of the tokens is kept.
+ * BF16 rounds to nearest even; E4M3 codes are those of fp8_kv_cast.
+ * n_tokens >= 0 (0 does nothing).
+ */
+int kv_page_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                  const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                  int x_dtype, int64_t n_tokens, void* k_cache, void* v_cache,
+                  int cache_dtype, int64_t n_pages, int64_t page_size,
+                  int64_t n_heads, int64_t d, int64_t page_stride,
+                  int64_t head_stride, int64_t token_stride, const float* k_scale,
+                  const float* v_scale, const int64_t* slots, void* stream);
+
+/*
+ * kv_paged_attention -- attention of a chunk of new tokens of each request
+ * over its keys and values in the paged cache (theirs written before); a
+ * decode step is a chunk of one token each, and chunks and decodes mix.
+ *
+ *   q            device, BF16 [n_tokens][n_heads][d] with token and head
+ *                strides in elements, 16-byte aligned, strides multiples of 8.
+ *                Request r's rows are [cu_new[r], cu_new[r + 1]); the last of
+ *                them stands at position kv_lens[r] - 1.
+ *   n_heads      a multiple of n_kv_heads; head h reads key/value head
+ *                h / (n_heads / n_kv_heads).  n_heads <= 65536, n_tokens *
+ *                n_heads <= 2^30, n_requests * n_kv_heads <= 2^26.
+ *   d            64, 128 or 256 (else UNSUPPORTED).
+ *   k_cache ... token_stride, scales   the cache as for kv_page_write; a token
+ *                stride below 2^26 bytes.
+ *   block_table, max_blocks, ld_table   page ids; one outside [0, n_pages)
+ *                reads as keys and values of zero.
+ *   cu_new, kv_lens  device, as kv_page_tables makes them (non-decreasing,
+ *                cu_new[n_requests] <= n_tokens, kv_lens <= max_blocks *
+ *                page_size).
+ *   max_new, max_kv  host: upper bounds of the new lengths and of kv_lens.
+ *   scale        factor of the scores, finite and > 0 (1 / sqrt(d)).
+ *   causal       nonzero: a token at position p sees the keys at <= p; zero:
+ *                every key of its request.
+ *   window       0, or the token sees only keys at positions > p - window.
+ *   out          device, out, BF16 [n_tokens][n_heads][d] with its own strides,
+ *                multiples of 4, 8-byte aligned; no overlap with an input.
+ *                Rows of no request are not written.  A row that sees no key
+ *                gives zeros.
+ *   workspace    device, 16-byte aligned, of the bytes that
+ *                kv_paged_attention_workspace returns for the same sizes
+ *                (NULL if 0); calls in flight together need one each.
+ *
+ * out = sum_j softmax_j(scale q.k_j) v_j with scores, softmax statistics and
+ * sums in binary32 and one final rounding; the weights enter the second
+ * matrix product rounded to bf16 (BF16 cache) or fp16 (E4M3 cache).  Only
+ * keys that some row of the call sees are used: what pages hold past a
+ * request's end, or before its window, is never used.
+ */
+int kv_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       int64_t n_tokens, int64_t n_heads, const void* k_cache,
+                       const void* v_cache, int cache_dtype, int64_t n_pages,
+                       int64_t page_size, int64_t n_kv_heads, int64_t d,
+                       int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                       const float* k_scale, const float* v_scale,
+                       const int32_t* block_table, int64_t max_blocks, int64_t ld_table,
+                       const int32_t* cu_new, const int32_t* kv_lens,
+                       int64_t n_requests, int64_t max_new, int64_t max_kv, float scale,
+                       int causal, int64_t window, void* out, int64_t out_token_stride,
+                       int64_t out_head_stride, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/* Bytes of workspace of kv_paged_attention for these sizes; -1 if one of
+   them is out of range.  Host only. */
+int64_t kv_paged_attention_workspace(int64_t n_tokens, int64_t n_heads,
+                                     int64_t n_kv_heads, int64_t d,
+                                     int64_t n_requests, int64_t max_new,
+                                     int64_t max_kv, int64_t window);
+
+/*
+ * prompt_attention -- attention over whole prompts packed one after another,
+ * keys and values taken from the packed rows themselves (no cache).
+ *
+ *   q            BF16 [n_tokens][n_heads][d]; k, v BF16 [n_tokens][n_kv_heads]
+ *                [d]; each with its token and head strides in elements
+ *                (16-byte aligned, multiples of 8, the token strides of k and
+ *                v below 2^25).
+ *   cu_lens      device, [n_prompts + 1] offsets: prompt r is rows
+ *                [cu_lens[r], cu_lens[r + 1]).
+ *   max_len      host: upper bound of the prompt lengths.
+ * d, heads, scale, causal, window, out, workspace and arithmetic as for
+ * kv_paged_attention (BF16 form).
+ */
+int prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                     const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                     const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                     int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads, int64_t d,
+                     const int32_t* cu_lens, int64_t n_prompts, int64_t max_len,
+                     float scale, int causal, int64_t window, void* out,
+                     int64_t out_token_stride, int64_t out_head_stride,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of prompt_attention; -1 if a size is out of range. */
+int64_t prompt_attention_workspace(int64_t n_tokens, int64_t n_heads,
+                                   int64_t n_kv_heads, int64_t d, int64_t n_prompts,
+                                   int64_t max_len, int64_t window);
+
 /* Static text for a status code (never NULL). */
 const char* nvfp4_status_string(int status);
 
 /* ABI version of this header: 3 (1 plus w4a4_gemm_gdn_gates, nvfp4_dequantize,
    nvfp4_error_stats and the fp8_kv_* calls in 2, plus w4a4_gemm_quantize_a
-   in 3). */
+   in 3).  The paged-cache and attention calls were added to 3 without a
+   change to any earlier call; look their symbols up to find them. */
 int nvfp4_abi_version(void);
 
 #ifdef __cplusplus

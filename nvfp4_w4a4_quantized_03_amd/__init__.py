@@ -10,8 +10,16 @@ and a GPU, and fails loudly otherwise.
     q = quantize(x, global_scale=g)        # calibrated static global
     g_star = harmonize_group(scales, k, row_offsets, module_globals)
     y = gemm(a, b, out_dtype=torch.bfloat16, epilogue="none")
+
+    step = kv_page_tables(new_lens, cached_lens, block_table, free_pages,
+                          page_size, n_tokens)
+    kv_page_write(k, v, k_cache, v_cache, step.slots, k_scale, v_scale)
+    o = paged_attention(q, k_cache, v_cache, block_table, step.cu_new,
+                        step.kv_lens, max_new, max_kv, k_scale=k_scale,
+                        v_scale=v_scale)
 """
 import ctypes
+import functools
 import os
 from collections import namedtuple
 
@@ -20,14 +28,16 @@ import torch
 __all__ = ["NVFP4", "quantize", "harmonize_group", "gemm", "gemm_quantize_a",
            "gdn_gates",
            "dequantize", "fp8_kv_calibrate", "fp8_kv_cast",
-           "fake_quantize", "error_stats", "library",
+           "fake_quantize", "error_stats",
+           "KVPages", "kv_page_tables", "kv_page_write", "paged_attention",
+           "prompt_attention", "library",
            "LIB_PATH", "NVFP4Error"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                         "libnvfp4_w4a4.so")
 
 # Enumerations of the C ABI.
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 GLOBAL_COMPUTE, GLOBAL_GIVEN = 0, 1
 EPILOGUES = {"none": 0, "alpha": 1, "beta": 2}
 
@@ -35,6 +45,13 @@ NVFP4 = namedtuple("NVFP4", ["codes", "scales", "global_scale"])
 NVFP4.__doc__ = """A packed NVFP4 tensor: codes uint8 [rows, k/2] (element 2j
 in the low nibble of byte j), scales uint8 [rows, k/16] (OCP E4M3), and
 global_scale float32 [1] (decode scale: value = e2m1 * e4m3 * g)."""
+
+
+KVPages = namedtuple("KVPages", ["cu_new", "kv_lens", "positions", "slots",
+                                 "pages_used"])
+KVPages.__doc__ = """A serving step's bookkeeping: cu_new int32
+[n_requests + 1], kv_lens int32 [n_requests], positions int32 [n_tokens] and
+slots int64 [n_tokens] (-1: none), pages_used int32 [1]."""
 
 
 class NVFP4Error(RuntimeError):
@@ -81,6 +98,23 @@ def library():
     L.nvfp4_error_stats.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp,
                                     vp]
     L.nvfp4_error_stats.restype = i32
+    L.kv_page_tables.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, i64, i64,
+                                 vp, vp, vp, vp, vp, vp]
+    L.kv_page_tables.restype = i32
+    L.kv_page_write.argtypes = [vp, i64, i64, vp, i64, i64, i32, i64, vp, vp,
+                                i32] + [i64] * 7 + [vp] * 4
+    L.kv_page_write.restype = i32
+    L.kv_paged_attention.argtypes = [vp, i64, i64, i64, i64, vp, vp, i32] + \
+        [i64] * 7 + [vp, vp, vp, i64, i64, vp, vp, i64, i64, i64,
+                     ctypes.c_float, i32, i64, vp, i64, i64, vp, i64, vp]
+    L.kv_paged_attention.restype = i32
+    L.kv_paged_attention_workspace.argtypes = [i64] * 8
+    L.kv_paged_attention_workspace.restype = i64
+    L.prompt_attention.argtypes = [vp, i64, i64] * 3 + [i64] * 4 + \
+        [vp, i64, i64, ctypes.c_float, i32, i64, vp, i64, i64, vp, i64, vp]
+    L.prompt_attention.restype = i32
+    L.prompt_attention_workspace.argtypes = [i64] * 7
+    L.prompt_attention_workspace.restype = i64
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_abi_version.argtypes = []
@@ -435,4 +469,226 @@ def fp8_kv_cast(x, scale, out=None):
     _check(library().fp8_kv_cast(_ptr(x), dt, rows, k, ldx, _ptr(scale), _ptr(out),
                                  ldo, _stream(x)),
            "fp8_kv_cast rows=%d k=%d ldx=%d ldo=%d" % (rows, k, ldx, ldo))
+    return out
+
+
+def _ints(t, name, dtype, device, numel=None):
+    """A contiguous 1-D integer GPU tensor."""
+    _device_tensor(t, name, dtype, numel, device)
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous 1-D tensor" % name)
+    return t.data_ptr()
+
+
+def _table_args(t, device, rows=None):
+    """Pointer, columns and row stride of an int32 block table."""
+    _device_tensor(t, "block_table", torch.int32, device=device)
+    if t.dim() != 2 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1) \
+            or (rows is not None and t.shape[0] != rows):
+        raise ValueError("block_table must be int32 [n_requests, max_blocks] "
+                         "with unit column stride")
+    rows, cols = t.shape
+    return t.data_ptr(), cols, t.stride(0) if rows > 1 else cols
+
+
+def _head_rows(t, name, device=None, dtype=torch.bfloat16, shape=None):
+    """Pointer, token stride and head stride of [tokens, heads, d] rows."""
+    _device_tensor(t, name, dtype, device=device)
+    if t.dim() != 3 or t.stride(2) != 1 or (shape is not None and
+                                            t.shape != shape):
+        raise ValueError("%s must be [tokens, heads, d] with unit stride along "
+                         "d, and agree with the other operands" % name)
+    tokens, heads, d = t.shape
+    # strides of axes of length one are arbitrary
+    ts, hs = t.stride(0), t.stride(1)
+    if heads == 1:
+        hs = d
+    return t.data_ptr(), ts if tokens > 1 else max(d, hs * heads), hs
+
+
+def _pool_args(k_cache, v_cache, k_scale, v_scale, device):
+    """Arguments of the paged caches, in the C ABI's order without scales:
+    pointers, dtype, sizes and strides; and the scales' pointers."""
+    _device_tensor(k_cache, "k_cache", device=device)
+    _device_tensor(v_cache, "v_cache", k_cache.dtype, device=device)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
+            k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache must be [n_pages, n_kv_heads, "
+                         "page_size, d] with the same strides, unit along d")
+    if k_cache.dtype == torch.uint8:
+        dt = DTYPE_E4M3
+        _global_tensor(k_scale, "k_scale", device)
+        _global_tensor(v_scale, "v_scale", device)
+        scales = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_cache.dtype == torch.bfloat16:
+        dt = DTYPE_BF16
+        scales = None, None
+    else:
+        raise ValueError("caches must be bfloat16 or uint8 (E4M3 codes)")
+    pages, heads, page, d = k_cache.shape
+    ps, hs, ts, _ = k_cache.stride()
+    if pages == 1:
+        ps = max(ps, d)
+    if heads == 1:
+        hs = max(hs, d)
+    return (k_cache.data_ptr(), v_cache.data_ptr(), dt, pages, page, heads, d,
+            ps, hs, ts), scales
+
+
+def kv_page_tables(new_lens, cached_lens, block_table, free_pages, page_size,
+                   n_tokens, out=None):
+    """Block tables, positions and slots of one serving step, on the device.
+
+    new_lens, cached_lens: int32 GPU tensors [n_requests], the tokens that the
+    step adds to each request and those it holds; block_table: int32
+    [n_requests, max_blocks], whose new entries are written in place;
+    free_pages: int32 [n_free], used from the front; n_tokens: host int, the
+    sum of new_lens or more (a captured graph's capacity).  Returns KVPages
+    (out supplies one to fill); pages_used above n_free means that pages ran
+    out: those entries and slots are -1."""
+    _device_tensor(new_lens, "new_lens")
+    dev = new_lens.device
+    n = new_lens.numel()
+    news = _ints(new_lens, "new_lens", torch.int32, dev)
+    held = _ints(cached_lens, "cached_lens", torch.int32, dev, n)
+    table, cols, ld = _table_args(block_table, dev, n)
+    free = _ints(free_pages, "free_pages", torch.int32, dev)
+    n_tokens = int(n_tokens)
+    if n_tokens < 0:
+        raise ValueError("n_tokens must not be negative")
+    if out is None:
+        # one allocation: the int64 slots, then the int32 arrays
+        buf = torch.empty(3 * n_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
+        at = 2 * n_tokens
+        out = KVPages(buf[at:at + n + 1], buf[at + n + 1:at + 2 * n + 1],
+                      buf[at + 2 * n + 2:], buf[:at].view(torch.int64),
+                      buf[at + 2 * n + 1:at + 2 * n + 2])
+    p = [_ints(t, nm, dt, dev, num) for t, nm, dt, num in
+         zip(out, KVPages._fields,
+             (torch.int32, torch.int32, torch.int32, torch.int64, torch.int32),
+             (n + 1, n, n_tokens, n_tokens, 1))]
+    _check(library().kv_page_tables(news, held, n, table, cols, ld, free,
+                                    free_pages.numel(), int(page_size),
+                                    n_tokens, *p, _stream(new_lens)),
+           "kv_page_tables")
+    return out
+
+
+def kv_page_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None):
+    """Write new keys and values into their slots of the paged caches.
+
+    k, v: float32 or bfloat16 GPU tensors [n_tokens, n_kv_heads, d] (strided
+    views of a fused projection's output are fine); k_cache, v_cache:
+    [n_pages, n_kv_heads, page_size, d], bfloat16, or uint8 E4M3 codes under
+    the static scales (float32 [1], fp8_kv_calibrate); any order of the first
+    three axes in memory.  slots: int64 [n_tokens]; one outside the cache is
+    skipped."""
+    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}.get(
+        getattr(k, "dtype", None))
+    if dt is None:
+        raise ValueError("k must be a float32 or bfloat16 tensor")
+    kp = _head_rows(k, "k", None, k.dtype)
+    dev = k.device
+    vp = _head_rows(v, "v", dev, k.dtype, k.shape)
+    pool, scales = _pool_args(k_cache, v_cache, k_scale, v_scale, dev)
+    if (k.shape[1], k.shape[2]) != (pool[5], pool[6]):
+        raise ValueError("k and the caches disagree in heads or d")
+    tokens = k.shape[0]
+    sl = _ints(slots, "slots", torch.int64, dev, tokens)
+    _check(library().kv_page_write(*kp, *vp, dt, tokens, *pool, *scales, sl,
+                                   _stream(k)),
+           "kv_page_write tokens=%d" % tokens)
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(paged, *sizes):
+    L = library()
+    fn = L.kv_paged_attention_workspace if paged else L.prompt_attention_workspace
+    return fn(*sizes)
+
+
+def _workspace(q, paged, *sizes):
+    """A buffer of the bytes that the call asks for (none: a null pointer).
+    It is allocated on the current stream and used there only."""
+    n = _attention_workspace(paged, *sizes)
+    if n <= 0:
+        return None, None, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    return ws, ws.data_ptr(), n
+
+
+def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new,
+                    max_kv, scale=None, causal=True, window=0, k_scale=None,
+                    v_scale=None, out=None):
+    """Attention of each request's new tokens over its paged keys and values
+    (already written, see kv_page_write); decode steps and chunks of prompts
+    mix in one call.
+
+    q: bfloat16 GPU tensor [n_tokens, n_heads, d] (d 64, 128 or 256; n_heads a
+    multiple of the caches' heads), packed by request; block_table int32
+    [n_requests, max_blocks], cu_new int32 [n_requests + 1] and kv_lens int32
+    [n_requests] as kv_page_tables makes them; max_new, max_kv: host upper
+    bounds of the new lengths and of kv_lens.  scale defaults to
+    1 / sqrt(d).  window > 0: a token sees the last `window` positions only,
+    itself included.  Returns [n_tokens, n_heads, d] bfloat16 (or fills
+    out)."""
+    qp = _head_rows(q, "q")
+    dev = q.device
+    tokens, heads, d = q.shape
+    pool, scales = _pool_args(k_cache, v_cache, k_scale, v_scale, dev)
+    if d != pool[6] or heads % pool[5] != 0:
+        raise ValueError("q and the caches disagree in d, or the heads are no "
+                         "multiple of the caches'")
+    n = kv_lens.numel()
+    kv = _ints(kv_lens, "kv_lens", torch.int32, dev)
+    cu = _ints(cu_new, "cu_new", torch.int32, dev, n + 1)
+    table, cols, ld = _table_args(block_table, dev, n)
+    if out is None:
+        out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
+    op = _head_rows(out, "out", dev, shape=q.shape)
+    max_new, max_kv, window = int(max_new), int(max_kv), int(window)
+    ws, wp, wn = _workspace(q, True, tokens, heads, pool[5], d, n, max_new,
+                            max_kv, window)
+    _check(library().kv_paged_attention(
+        *qp, tokens, heads, *pool, *scales, table, cols, ld, cu, kv, n,
+        max_new, max_kv, d ** -0.5 if scale is None else scale,
+        1 if causal else 0, window, *op, wp, wn, _stream(q)),
+        "paged_attention tokens=%d heads=%d d=%d requests=%d"
+        % (tokens, heads, d, n))
+    return out
+
+
+def prompt_attention(q, k, v, cu_lens, max_len, scale=None, causal=True,
+                     window=0, out=None):
+    """Attention over whole prompts packed one after another.
+
+    q: bfloat16 GPU tensor [n_tokens, n_heads, d] (d 64, 128 or 256); k, v:
+    [n_tokens, n_kv_heads, d]; each may be a strided view of a fused
+    projection's output.  cu_lens: int32 [n_prompts + 1] offsets; max_len:
+    host upper bound of the lengths.  scale, causal, window, out as for
+    paged_attention."""
+    qp = _head_rows(q, "q")
+    dev = q.device
+    tokens, heads, d = q.shape
+    kp = _head_rows(k, "k", dev)
+    vp = _head_rows(v, "v", dev, shape=k.shape)
+    kv_heads = k.shape[1]
+    if k.shape[0] != tokens or k.shape[2] != d or kv_heads < 1 or \
+            heads % kv_heads != 0:
+        raise ValueError("q and k disagree in tokens or d, or the heads are no "
+                         "multiple of k's")
+    n = cu_lens.numel() - 1
+    cu = _ints(cu_lens, "cu_lens", torch.int32, dev)
+    if out is None:
+        out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
+    op = _head_rows(out, "out", dev, shape=q.shape)
+    max_len, window = int(max_len), int(window)
+    ws, wp, wn = _workspace(q, False, tokens, heads, kv_heads, d, n, max_len,
+                            window)
+    _check(library().prompt_attention(
+        *qp, *kp, *vp, tokens, heads, kv_heads, d, cu, n, max_len,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+        *op, wp, wn, _stream(q)),
+        "prompt_attention tokens=%d heads=%d d=%d prompts=%d"
+        % (tokens, heads, d, n))
     return out

@@ -26,7 +26,8 @@ DEVICE = ["-x", "hip", "--offload-arch=" + ARCH,
           "-fno-gpu-flush-denormals-to-zero",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = ["quantize.hip", "harmonize.hip", "gemm.hip", "gemm_stream.hip",
-           "dequantize.hip", "fp8kv.hip", "api.cpp"]
+           "dequantize.hip", "fp8kv.hip", "kvpage.hip", "attention.hip",
+           "api.cpp"]
 
 
 def _compile(src):

@@ -1,6 +1,7 @@
 // C ABI front end: argument validation on the host, then kernel dispatch.
 // Every check runs before any HIP call, so a rejected call touches no
 // device state (and can be exercised on a machine without a GPU).
+#include <math.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime_api.h>
@@ -44,6 +45,93 @@ int check_x(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx) {
   return NVFP4_OK;
 }
 
+// Extent in bytes of [token][head][d] rows.
+int64_t rows_bytes(int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t d, int64_t es) {
+  return tokens < 1 ? 0 : ((tokens - 1) * ts + (heads - 1) * hs + d) * es;
+}
+
+// [token][head][d] rows of a caller's tensor: strides that keep rows apart,
+// `align` bytes of alignment.
+int check_rows(const void* p, int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t d,
+               int64_t es, int64_t align) {
+  if (!p) return NVFP4_ERR_INVALID_VALUE;
+  if (ts < d || hs < d || ts > kMaxDim || hs > kMaxDim || tokens > kMaxDim / ts ||
+      heads > kMaxDim / hs)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(p, align) || (ts * es) % align != 0 || (hs * es) % align != 0)
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+// A paged cache as kv_page_write and kv_paged_attention take it.
+int check_pool(const nvfp4::KvPool& p, int dtype) {
+  if (!p.k || !p.v) return NVFP4_ERR_INVALID_VALUE;
+  if (p.n_pages < 1 || p.page_size < 1 || p.n_heads < 1 || p.d < 16 || p.n_pages > 0x7FFFFFFF ||
+      p.page_size > (1 << 24) || p.n_heads > (1 << 16))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (dtype != NVFP4_DTYPE_BF16 && dtype != NVFP4_DTYPE_E4M3) return NVFP4_ERR_UNSUPPORTED;
+  if (p.page_size % 16 != 0) return NVFP4_ERR_UNSUPPORTED;
+  if (p.page_stride < p.d || p.head_stride < p.d || p.token_stride < p.d ||
+      p.page_stride > kMaxDim || p.head_stride > kMaxDim || p.token_stride > kMaxDim ||
+      p.n_pages > kMaxDim / p.page_stride || p.n_heads > kMaxDim / p.head_stride ||
+      p.page_size > kMaxDim / p.token_stride)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (p.fp8 && (!p.k_scale || !p.v_scale)) return NVFP4_ERR_INVALID_VALUE;
+  const int64_t es = p.fp8 ? 1 : 2;
+  if (!aligned(p.k, 16) || !aligned(p.v, 16) || (p.page_stride * es) % 16 != 0 ||
+      (p.head_stride * es) % 16 != 0 || (p.token_stride * es) % 16 != 0 ||
+      (p.fp8 && (!aligned(p.k_scale, 4) || !aligned(p.v_scale, 4))))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+int64_t pool_bytes(const nvfp4::KvPool& p) {
+  return ((p.n_pages - 1) * p.page_stride + (p.n_heads - 1) * p.head_stride +
+          (p.page_size - 1) * p.token_stride + p.d) * (p.fp8 ? 1 : 2);
+}
+
+// Sizes and options that both attention calls share.
+int check_attention(const nvfp4::AttnCall& c) {
+  constexpr int64_t kInt = 0x7FFFFFFF;
+  if (c.n_tokens < 0 || c.n_heads < 1 || c.n_kv_heads < 1 || c.n_heads % c.n_kv_heads != 0 ||
+      c.n_heads > (1 << 16) || c.n_requests < 1 || c.n_requests > (1 << 24) || c.max_new < 0 ||
+      c.max_kv < 0 || c.max_kv > kInt - 65536 || c.max_new > kInt - 65536 || c.window < 0 ||
+      c.window > kInt - 65536)
+    return NVFP4_ERR_INVALID_VALUE;
+  // rows, tiles and workgroups are counted in 32 bits
+  if (c.n_tokens > (int64_t(1) << 30) / c.n_heads ||
+      c.n_requests > (int64_t(1) << 26) / c.n_kv_heads)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!(c.scale > 0.0f) || isinf(c.scale)) return NVFP4_ERR_INVALID_VALUE;
+  if (c.d != 64 && c.d != 128 && c.d != 256) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+// Workspace and output of an attention call, then the launch.
+int run_attention(const nvfp4::AttnCall& c, int64_t workspace_bytes, void* stream) {
+  const int64_t need = nvfp4::attention_workspace(c);
+  if (need < 0 || workspace_bytes < need || (need > 0 && !c.workspace))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (need > 0 && !aligned(c.workspace, 16)) return NVFP4_ERR_MISALIGNED;
+  const int64_t obytes = rows_bytes(c.n_tokens, c.out_token, c.n_heads, c.out_head, c.d, 2);
+  const bool paged = c.table != nullptr;
+  struct Range { const void* p; int64_t len; };
+  const Range in[] = {
+      {c.q.p, rows_bytes(c.n_tokens, c.q.token, c.n_heads, c.q.head, c.d, 2)},
+      {paged ? c.pool.k : c.k.p, paged ? pool_bytes(c.pool) : rows_bytes(c.n_tokens, c.k.token, c.n_kv_heads, c.k.head, c.d, 2)},
+      {paged ? c.pool.v : c.v.p, paged ? pool_bytes(c.pool) : rows_bytes(c.n_tokens, c.v.token, c.n_kv_heads, c.v.head, c.d, 2)},
+      {c.cu, 4 * (c.n_requests + 1)},
+      {c.kv_lens, paged ? 4 * c.n_requests : 0},
+      {c.table, paged ? ((c.n_requests - 1) * c.ld_table + c.cols) * 4 : 0}};
+  for (const Range& r : in) {
+    if (r.len < 1) continue;
+    if (overlap(c.out, obytes, r.p, r.len)) return NVFP4_ERR_INVALID_VALUE;
+    if (need > 0 && overlap(c.workspace, need, r.p, r.len)) return NVFP4_ERR_INVALID_VALUE;
+  }
+  if (need > 0 && overlap(c.workspace, need, c.out, obytes)) return NVFP4_ERR_INVALID_VALUE;
+  return status_of(nvfp4::launch_attention(c, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -60,7 +148,8 @@ const char* nvfp4_status_string(int status) {
       return "NVFP4_ERR_UNSUPPORTED: unknown dtype, global mode or epilogue, "
              "or a shape outside the call's kernels (gate pair: more than 256 "
              "columns or k not a multiple of 128; fused quantise + GEMM: more "
-             "than 64 rows or k not a multiple of 128)";
+             "than 64 rows or k not a multiple of 128; paged cache: page size "
+             "not a multiple of 16; attention: d not 64, 128 or 256)";
     case NVFP4_ERR_MISALIGNED:
       return "NVFP4_ERR_MISALIGNED: a pointer or row stride breaks the "
              "required alignment";
@@ -326,6 +415,173 @@ int fp8_kv_cast(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx
     return NVFP4_ERR_INVALID_VALUE;
   return status_of(nvfp4::launch_kv_cast(x, x_dtype, rows, k, ldx, scale, out, ldo,
                                          static_cast<hipStream_t>(stream)));
+}
+
+int kv_page_tables(const int32_t* new_lens, const int32_t* cached_lens, int64_t n_requests,
+                   int32_t* block_table, int64_t max_blocks, int64_t ld_table,
+                   const int32_t* free_pages, int64_t n_free, int64_t page_size,
+                   int64_t n_tokens, int32_t* cu_new, int32_t* kv_lens, int32_t* positions,
+                   int64_t* slots, int32_t* pages_used, void* stream) {
+  if (!new_lens || !cached_lens || !block_table || !cu_new || !kv_lens || !pages_used ||
+      (n_free > 0 && !free_pages) || (n_tokens > 0 && (!positions || !slots)))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (n_requests < 1 || n_requests > (1 << 24) || max_blocks < 1 || ld_table < max_blocks ||
+      ld_table > 0x7FFFFFFF || n_free < 0 || n_free > 0x7FFFFFFF || page_size < 1 ||
+      page_size > (1 << 24) || n_tokens < 0 || n_tokens > 0x7FFFFFFF)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (page_size % 16 != 0) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(new_lens, 4) || !aligned(cached_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(cu_new, 4) || !aligned(kv_lens, 4) ||
+      !aligned(positions, 4) || !aligned(slots, 8) || !aligned(pages_used, 4))
+    return NVFP4_ERR_MISALIGNED;
+  struct Range { const void* p; int64_t len; };
+  const Range in[] = {{new_lens, 4 * n_requests}, {cached_lens, 4 * n_requests},
+                      {free_pages, 4 * n_free}};
+  const Range outs[] = {{block_table, ((n_requests - 1) * ld_table + max_blocks) * 4},
+                        {cu_new, 4 * (n_requests + 1)}, {kv_lens, 4 * n_requests},
+                        {positions, 4 * n_tokens}, {slots, 8 * n_tokens}, {pages_used, 4}};
+  for (int i = 0; i < 6; ++i) {
+    if (outs[i].len < 1) continue;
+    for (const Range& r : in)
+      if (r.len > 0 && overlap(outs[i].p, outs[i].len, r.p, r.len)) return NVFP4_ERR_INVALID_VALUE;
+    for (int j = i + 1; j < 6; ++j)
+      if (outs[j].len > 0 && overlap(outs[i].p, outs[i].len, outs[j].p, outs[j].len))
+        return NVFP4_ERR_INVALID_VALUE;
+  }
+  return status_of(nvfp4::launch_page_tables(new_lens, cached_lens, n_requests, block_table,
+                                             max_blocks, ld_table, free_pages, n_free, page_size,
+                                             n_tokens, cu_new, kv_lens, positions, slots,
+                                             pages_used, static_cast<hipStream_t>(stream)));
+}
+
+int kv_page_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_token_stride, int64_t v_head_stride, int x_dtype, int64_t n_tokens,
+                  void* k_cache, void* v_cache, int cache_dtype, int64_t n_pages,
+                  int64_t page_size, int64_t n_heads, int64_t d, int64_t page_stride,
+                  int64_t head_stride, int64_t token_stride, const float* k_scale,
+                  const float* v_scale, const int64_t* slots, void* stream) {
+  const nvfp4::KvPool pool = {k_cache, v_cache, cache_dtype == NVFP4_DTYPE_E4M3, n_pages,
+                              page_size, n_heads, d, page_stride, head_stride, token_stride,
+                              k_scale, v_scale};
+  const int cp = check_pool(pool, cache_dtype);
+  if (cp != NVFP4_OK) return cp;
+  if (n_tokens < 0) return NVFP4_ERR_INVALID_VALUE;
+  if (d % 16 != 0 || d > 1024) return NVFP4_ERR_UNSUPPORTED;
+  if (x_dtype != NVFP4_DTYPE_F32 && x_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return NVFP4_OK;
+  const int64_t es = x_dtype == NVFP4_DTYPE_F32 ? 4 : 2;
+  int st = check_rows(k, n_tokens, k_token_stride, n_heads, k_head_stride, d, es, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(v, n_tokens, v_token_stride, n_heads, v_head_stride, d, es, 16);
+  if (st != NVFP4_OK) return st;
+  if (!slots || n_tokens >= (int64_t(1) << 31) / (n_heads * (d / 16)))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(slots, 8)) return NVFP4_ERR_MISALIGNED;
+  struct Range { const void* p; int64_t len; };
+  const Range in[] = {{k, rows_bytes(n_tokens, k_token_stride, n_heads, k_head_stride, d, es)},
+                      {v, rows_bytes(n_tokens, v_token_stride, n_heads, v_head_stride, d, es)},
+                      {slots, 8 * n_tokens}, {k_scale, pool.fp8 ? 4 : 0},
+                      {v_scale, pool.fp8 ? 4 : 0}};
+  for (const Range& r : in)
+    if (r.len > 0 && (overlap(k_cache, pool_bytes(pool), r.p, r.len) ||
+                      overlap(v_cache, pool_bytes(pool), r.p, r.len)))
+      return NVFP4_ERR_INVALID_VALUE;
+  return status_of(nvfp4::launch_page_write({k, k_token_stride, k_head_stride},
+                                            {v, v_token_stride, v_head_stride}, x_dtype, n_tokens,
+                                            pool, slots, static_cast<hipStream_t>(stream)));
+}
+
+int64_t kv_paged_attention_workspace(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
+                                     int64_t d, int64_t n_requests, int64_t max_new,
+                                     int64_t max_kv, int64_t window) {
+  nvfp4::AttnCall c = {};
+  static const int32_t paged = 0;      // any non-null table: only its presence counts
+  c.table = &paged;
+  c.n_tokens = n_tokens; c.n_heads = n_heads; c.n_kv_heads = n_kv_heads; c.d = d;
+  c.n_requests = n_requests; c.max_new = max_new; c.max_kv = max_kv; c.window = window;
+  c.scale = 1.0f;
+  return check_attention(c) == NVFP4_OK ? nvfp4::attention_workspace(c) : -1;
+}
+
+int kv_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                       int64_t n_tokens, int64_t n_heads, const void* k_cache,
+                       const void* v_cache, int cache_dtype, int64_t n_pages, int64_t page_size,
+                       int64_t n_kv_heads, int64_t d, int64_t page_stride, int64_t head_stride,
+                       int64_t token_stride, const float* k_scale, const float* v_scale,
+                       const int32_t* block_table, int64_t max_blocks, int64_t ld_table,
+                       const int32_t* cu_new, const int32_t* kv_lens, int64_t n_requests,
+                       int64_t max_new, int64_t max_kv, float scale, int causal, int64_t window,
+                       void* out, int64_t out_token_stride, int64_t out_head_stride,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  nvfp4::AttnCall c = {};
+  c.q = {q, q_token_stride, q_head_stride};
+  c.out = out; c.out_token = out_token_stride; c.out_head = out_head_stride;
+  c.n_tokens = n_tokens; c.n_heads = n_heads; c.n_kv_heads = n_kv_heads; c.d = d;
+  c.pool = {const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+            cache_dtype == NVFP4_DTYPE_E4M3, n_pages, page_size, n_kv_heads, d, page_stride,
+            head_stride, token_stride, k_scale, v_scale};
+  c.table = block_table; c.cols = max_blocks; c.ld_table = ld_table;
+  c.cu = cu_new; c.kv_lens = kv_lens;
+  c.n_requests = n_requests; c.max_new = max_new; c.max_kv = max_kv;
+  c.scale = scale; c.causal = causal != 0; c.window = window; c.workspace = workspace;
+  if (!block_table || !cu_new || !kv_lens) return NVFP4_ERR_INVALID_VALUE;
+  int st = check_attention(c);
+  if (st != NVFP4_OK) return st;
+  st = check_pool(c.pool, cache_dtype);
+  if (st != NVFP4_OK) return st;
+  if (max_blocks < 1 || ld_table < max_blocks || ld_table > 0x7FFFFFFF ||
+      token_stride * (c.pool.fp8 ? 1 : 2) >= (1 << 26))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (n_tokens == 0) return NVFP4_OK;
+  st = check_rows(q, n_tokens, q_token_stride, n_heads, q_head_stride, d, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(out, n_tokens, out_token_stride, n_heads, out_head_stride, d, 2, 8);
+  if (st != NVFP4_OK) return st;
+  if (!aligned(block_table, 4) || !aligned(cu_new, 4) || !aligned(kv_lens, 4))
+    return NVFP4_ERR_MISALIGNED;
+  return run_attention(c, workspace_bytes, stream);
+}
+
+int64_t prompt_attention_workspace(int64_t n_tokens, int64_t n_heads, int64_t n_kv_heads,
+                                   int64_t d, int64_t n_prompts, int64_t max_len,
+                                   int64_t window) {
+  nvfp4::AttnCall c = {};
+  c.n_tokens = n_tokens; c.n_heads = n_heads; c.n_kv_heads = n_kv_heads; c.d = d;
+  c.n_requests = n_prompts; c.max_new = c.max_kv = max_len; c.window = window;
+  c.scale = 1.0f;
+  return check_attention(c) == NVFP4_OK ? nvfp4::attention_workspace(c) : -1;
+}
+
+int prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                     int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                     int64_t v_token_stride, int64_t v_head_stride, int64_t n_tokens,
+                     int64_t n_heads, int64_t n_kv_heads, int64_t d, const int32_t* cu_lens,
+                     int64_t n_prompts, int64_t max_len, float scale, int causal, int64_t window,
+                     void* out, int64_t out_token_stride, int64_t out_head_stride,
+                     void* workspace, int64_t workspace_bytes, void* stream) {
+  nvfp4::AttnCall c = {};
+  c.q = {q, q_token_stride, q_head_stride};
+  c.k = {k, k_token_stride, k_head_stride};
+  c.v = {v, v_token_stride, v_head_stride};
+  c.out = out; c.out_token = out_token_stride; c.out_head = out_head_stride;
+  c.n_tokens = n_tokens; c.n_heads = n_heads; c.n_kv_heads = n_kv_heads; c.d = d;
+  c.cu = cu_lens; c.n_requests = n_prompts; c.max_new = c.max_kv = max_len;
+  c.scale = scale; c.causal = causal != 0; c.window = window; c.workspace = workspace;
+  if (!cu_lens) return NVFP4_ERR_INVALID_VALUE;
+  int st = check_attention(c);
+  if (st != NVFP4_OK) return st;
+  if (n_tokens == 0) return NVFP4_OK;
+  st = check_rows(q, n_tokens, q_token_stride, n_heads, q_head_stride, d, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(k, n_tokens, k_token_stride, n_kv_heads, k_head_stride, d, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(v, n_tokens, v_token_stride, n_kv_heads, v_head_stride, d, 2, 16);
+  if (st != NVFP4_OK) return st;
+  if (k_token_stride >= (1 << 25) || v_token_stride >= (1 << 25)) return NVFP4_ERR_INVALID_VALUE;
+  st = check_rows(out, n_tokens, out_token_stride, n_heads, out_head_stride, d, 2, 8);
+  if (st != NVFP4_OK) return st;
+  if (!aligned(cu_lens, 4)) return NVFP4_ERR_MISALIGNED;
+  return run_attention(c, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -99,4 +99,60 @@ hipError_t launch_kv_cast(const void* x, int x_dtype, int64_t rows, int64_t k,
                           int64_t ldx, const float* scale, uint8_t* out,
                           int64_t ldo, hipStream_t stream);
 
+// Rows [token][head][d] of a caller's tensor; strides in elements, unit
+// stride along d.
+struct KvRows {
+  const void* p;
+  int64_t token, head;
+};
+
+// A paged K and V cache: element (page, head, token in page, i) at page *
+// page_stride + head * head_stride + token * token_stride + i of either
+// array; bf16, or E4M3 codes under the device scales.
+struct KvPool {
+  void* k;
+  void* v;
+  bool fp8;
+  int64_t n_pages, page_size, n_heads, d;
+  int64_t page_stride, head_stride, token_stride;
+  const float* k_scale;
+  const float* v_scale;
+};
+
+// Block tables, positions and slots of a step; the write of its keys and
+// values (kvpage.hip).
+hipError_t launch_page_tables(const int32_t* new_lens, const int32_t* cached_lens,
+                              int64_t n_requests, int32_t* block_table, int64_t cols, int64_t ld,
+                              const int32_t* free_pages, int64_t n_free, int64_t page_size,
+                              int64_t n_tokens, int32_t* cu_new, int32_t* kv_lens,
+                              int32_t* positions, int64_t* slots, int32_t* pages_used,
+                              hipStream_t stream);
+hipError_t launch_page_write(const KvRows& k, const KvRows& v, int x_dtype, int64_t n_tokens,
+                             const KvPool& pool, const int64_t* slots, hipStream_t stream);
+
+// Attention (attention.hip).  Queries and outputs are bf16 [token][head][d]
+// rows; request r's queries are rows [cu[r], cu[r + 1]) and the last of them
+// stands at position kv_lens[r] - 1 (kv_lens == nullptr: as many keys as
+// queries, the prompt form).  The keys are pages of `pool` under `table`, or
+// (table == nullptr) rows of k and v.
+struct AttnCall {
+  KvRows q, k, v;
+  void* out;
+  int64_t out_token, out_head;
+  int64_t n_tokens, n_heads, n_kv_heads, d;
+  KvPool pool;
+  const int32_t* table;
+  int64_t cols, ld_table;
+  const int32_t* cu;
+  const int32_t* kv_lens;
+  int64_t n_requests, max_new, max_kv;
+  float scale;
+  int causal;
+  int64_t window;
+  void* workspace;
+};
+// Bytes of workspace that the call needs (the pointers are not read).
+int64_t attention_workspace(const AttnCall& c);
+hipError_t launch_attention(const AttnCall& c, hipStream_t stream);
+
 }  // namespace nvfp4

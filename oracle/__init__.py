@@ -34,6 +34,7 @@ from .quantize import (quantize, quantize_exact, dequantize, global_scale,
 from .harmonize import harmonize, harmonize_exact
 from .fp8kv import (kv_amax, kv_scale, kv_cast, kv_decode, kv_cast_exact,
                     kv_scale_exact)
+from .attention import attention, page_tables
 from .gemm import (gemm_exact_int, gemm_f64, gemm_f64_rows_cols,
                    gemm_f64_row_blocks, gate_alpha, gate_beta, decoded_units,
                    gdn_gates)
@@ -48,6 +49,7 @@ __all__ = [
     "harmonize", "harmonize_exact",
     "kv_amax", "kv_scale", "kv_cast", "kv_decode", "kv_cast_exact",
     "kv_scale_exact",
+    "attention", "page_tables",
     "gemm_exact_int", "gemm_f64", "gemm_f64_rows_cols", "gemm_f64_row_blocks",
     "gate_alpha",
     "gate_beta", "decoded_units", "gdn_gates",
