@@ -57,6 +57,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileRows = 128;         // rows of a workgroup, 32 a wave
+constexpr int kFewRows = 16;           // rows of a request that few_rows_kernel takes
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -74,13 +75,16 @@ struct Args {
   const int32_t* kv_lens;
   const float* k_scale;
   const float* v_scale;
-  float* part;                                    // [split][token * head][d]
-  float* part_ml;                                 // [split][token * head][2]
+  // sums of chunks of keys, [slot][d] and [slot][2] (bound, sum of weights)
+  float* part;
+  float* part_ml;
   float scale_log2;
   int n_requests, n_tokens, n_heads, n_kv_heads, n_pages;
   FastDiv group, page;
   int64_t cols_len;                               // columns * page size
-  int max_kv, causal, window, tiles, splits, chunk;
+  int max_kv, causal, window, tiles;
+  // chunks of keys: of tiles of many rows, of requests of few
+  int splits, chunk, few_splits, few_chunk;
 };
 
 __device__ __forceinline__ int clampi(int64_t x, int64_t lo, int64_t hi) {
@@ -147,9 +151,18 @@ __device__ __forceinline__ Span span_of(const Args& a, int r, int row0, int rows
 }
 
 // Chunks that the keys of a tile are cut into.
-__device__ __forceinline__ int splits_of(const Args& a, const Span& s) {
-  const int n = (s.hi - s.start + a.chunk - 1) / a.chunk;
-  return n < 1 ? 1 : n > a.splits ? a.splits : n;
+__device__ __forceinline__ int splits_of(const Span& s, int chunk, int most) {
+  const int n = (s.hi - s.start + chunk - 1) / chunk;
+  return n < 1 ? 1 : n > most ? most : n;
+}
+
+// Places of a chunk's sums: of a row of a tile, of a row of a few-row request.
+__device__ __forceinline__ int64_t tile_slot(const Args& a, int split, int64_t token, int head) {
+  return (static_cast<int64_t>(split) * a.n_tokens + token) * a.n_heads + head;
+}
+__device__ __forceinline__ int64_t few_slot(const Args& a, int split, int r, int kvh, int row) {
+  const int64_t before = a.splits > 1 ? tile_slot(a, a.splits, 0, 0) : 0;
+  return before + ((static_cast<int64_t>(split) * a.n_requests + r) * a.n_kv_heads + kvh) * kFewRows + row;
 }
 
 // ---------------------------------------------------------------- staging
@@ -315,9 +328,9 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   const int group = static_cast<int>(a.group.d);
   const int64_t n_rows = static_cast<int64_t>(clampi(a.cu[r + 1], 0, a.n_tokens) -
                                               clampi(a.cu[r], 0, a.n_tokens)) * group;
-  if (row0 < 0 || row0 >= n_rows) return;
+  if (row0 < 0 || row0 >= n_rows || (a.few_splits > 0 && n_rows <= kFewRows)) return;
   const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
-  const int splits = splits_of(a, s);
+  const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
   const int begin = s.start + split * a.chunk;
   const int end = split == splits - 1 ? s.hi : begin + a.chunk;
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
         *reinterpret_cast<u32x2*>(op + (32 * b + 8 * i + 4 * half) * 2) = w;
       }
   } else {
-    const int64_t at = (static_cast<int64_t>(split) * a.n_tokens + out_row) * a.n_heads + head;
+    const int64_t at = tile_slot(a, split, out_row, head);
     float* pp = a.part + at * D;
 #pragma unroll
     for (int b = 0; b < kDb; ++b)
@@ -470,6 +483,302 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
             f32x4{acc[b][4 * i], acc[b][4 * i + 1], acc[b][4 * i + 2], acc[b][4 * i + 3]};
     if (half == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m, l};
   }
+}
+
+// ------------------------------------------------- requests of few rows
+
+// value over the four lanes that share a column of a 16x16 product
+__device__ __forceinline__ float quad_max(float x) {
+  unsigned u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  unsigned u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// Keys and values of 32 keys of one wave, in flight.  K goes straight to the
+// layout of the A operand (lane: key lane & 15, 16 bytes at chunk 4 i + lane
+// / 16; of E4M3 codes the two halves of a chunk belong to two steps, and Q
+// is read in the same order); V is read row by row for the transposing LDS.
+template <int D, bool FP8>
+struct Stream {
+  static constexpr int kKeys = 32;
+  static constexpr int kChunks = D * (FP8 ? 1 : 2) / 16;
+  static constexpr int kK = kChunks / 4;                    // loads of 16 keys
+  static constexpr int kV = kKeys * kChunks / 64;           // loads of the tile
+  u32x4 k[2][kK], v[kV];
+  const uint8_t* kb[2];
+  const uint8_t* vb[2];
+  int kt, vt, first[2], end[2];
+
+  // Bases of the two groups of 16 keys at key0, as for Stage: rows outside
+  // [lo, hi) read the nearest one inside.
+  __device__ __forceinline__ void locate(const Args& a, const Span& s, int64_t head_k,
+                                         int64_t head_v, int key0, const int* ids) {
+    const int last = (s.hi - 1) & ~15;
+    kt = static_cast<int>(a.k_token);
+    vt = static_cast<int>(a.v_token);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      int g = key0 + 16 * p;
+      g = g < last ? g : last;
+      first[p] = s.lo - g;
+      end[p] = s.hi - 1 - g;
+      if (a.table) {
+        const int off = g - static_cast<int>(a.page.div(static_cast<unsigned>(g)) * a.page.d);
+        const bool in = ids[p] >= 0 && ids[p] < a.n_pages;
+        const int64_t page = in ? ids[p] * a.page_stride : 0;
+        kb[p] = a.k + page + head_k + off * a.k_token;
+        vb[p] = a.v + page + head_v + off * a.v_token;
+        if (!in) {
+          kb[p] = vb[p] = reinterpret_cast<const uint8_t*>(kZeros);
+          first[p] = end[p] = 0;           // every row at the one of zeros
+        }
+      } else {
+        kb[p] = a.k + (static_cast<int64_t>(s.token0) + g) * a.k_token + head_k;
+        vb[p] = a.v + (static_cast<int64_t>(s.token0) + g) * a.v_token + head_v;
+      }
+    }
+  }
+  __device__ __forceinline__ static int inside(int r, int first, int end) {
+    r = r < first ? first : r;
+    return r > end ? end : r;
+  }
+  __device__ __forceinline__ void load_k() {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint8_t* row = kb[p] + inside(lane & 15, first[p], end[p]) * kt + (lane >> 4) * 16;
+#pragma unroll
+      for (int i = 0; i < kK; ++i) k[p][i] = *reinterpret_cast<const u32x4*>(row + i * 64);
+    }
+  }
+  __device__ __forceinline__ void load_v() {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int p = i * 64 / kChunks / 16;                  // a load lies in one group
+      const int r = (i * 64 + lane) / kChunks - 16 * p, c = (i * 64 + lane) % kChunks;
+      v[i] = *reinterpret_cast<const u32x4*>(vb[p] + inside(r, first[p], end[p]) * vt + c * 16);
+    }
+  }
+  // The 8 rows that 32 lanes of a transposing read touch differ by 32 bytes.
+  static __device__ __forceinline__ int v_at(int r, int c) {
+    return r * (D * 2) + ((c ^ (D == 64 ? ((r >> 1) & 3) << 1 : (r & 7) << 1)) << 4);
+  }
+  __device__ __forceinline__ void store_v(uint8_t* lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const int r = (i * 64 + lane) / kChunks, c = (i * 64 + lane) % kChunks;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const u32x2 v0 = widen4<true>(v[i][2 * p]), v1 = widen4<true>(v[i][2 * p + 1]);
+          *reinterpret_cast<u32x4*>(lds + v_at(r, 2 * c + p)) = u32x4{v0[0], v0[1], v1[0], v1[1]};
+        }
+      } else {
+        *reinterpret_cast<u32x4*>(lds + v_at(r, c)) = v[i];
+      }
+    }
+  }
+  // A operand of step i of the first product, key group p.
+  __device__ __forceinline__ bf16x8 k_operand(int p, int i) const {
+    if constexpr (FP8) {
+      const u32x4 w = k[p][i >> 1];
+      const u32x2 a = widen4<false>(w[2 * (i & 1)]), b = widen4<false>(w[2 * (i & 1) + 1]);
+      return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+    } else {
+      return __builtin_bit_cast(bf16x8, k[p][i]);
+    }
+  }
+};
+
+// A request whose rows fit one 16-column operand: a decode token with its
+// group of heads, a few speculated ones.  Its keys are streamed once, each
+// wave taking 32 at a time straight from memory (no barrier: V passes
+// through an LDS area of the wave's own); the four waves are joined at the
+// end.  Bound by the read of the keys and values.
+template <int D, bool FP8>
+__global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(Args a) {
+  using S = Stream<D, FP8>;
+  constexpr int kSteps = D / 32;
+  constexpr int kDb = D / 16;
+  constexpr int kWave = S::kKeys * D * 2;      // LDS bytes of a wave: V, later its sums
+  constexpr float kSlack = 8.0f;
+  constexpr float kLift = FP8 ? 6.0f : 0.0f;
+  static_assert(kWave == 16 * D * 4, "the sums take the place of V");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kWave];
+  __shared__ float lds_m[4][16], lds_l[4][16];
+
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int kvh = blockIdx.x % a.n_kv_heads;
+  const int rest = blockIdx.x / a.n_kv_heads;
+  const int split = rest % a.few_splits, r = rest / a.few_splits;
+  const int group = static_cast<int>(a.group.d);
+  const Span s = span_of(a, r, 0, kFewRows);
+  const int64_t n_rows = static_cast<int64_t>(s.n_new) * group;
+  if (n_rows < 1 || n_rows > kFewRows) return;
+  const int splits = splits_of(s, a.few_chunk, a.few_splits);
+  if (split >= splits) return;
+  const int begin = s.start + split * a.few_chunk;
+  const int end = split == splits - 1 ? s.hi : begin + a.few_chunk;
+
+  const bool real = col < n_rows;
+  const int token = static_cast<int>(a.group.div(real ? col : 0));
+  const int head = kvh * group + (real ? col - token * group : 0);
+  int see_lo = 0, see_hi = 0;
+  if (real) sees(a, s, token, &see_lo, &see_hi);
+
+  bf16x8 qf[kSteps];
+  {
+    const uint8_t* qp = a.q + (static_cast<int64_t>(s.token0) + token) * a.q_token + head * a.q_head;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      // the chunk order of k_operand
+      const int at = FP8 ? (i >> 1) * 128 + quad * 32 + (i & 1) * 16 : i * 64 + quad * 16;
+      qf[i] = *reinterpret_cast<const bf16x8*>(qp + at);
+    }
+  }
+  const float c = FP8 ? fmaxf(a.scale_log2 * *a.k_scale, 0x1p-120f) : a.scale_log2;
+
+  f32x4 acc[kDb];
+#pragma unroll
+  for (int b = 0; b < kDb; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kNegInf, l = 0.0f;
+
+  const int32_t* table = a.table ? a.table + r * a.ld_table : nullptr;
+  const int64_t head_k = kvh * a.k_head, head_v = kvh * a.v_head;
+  const int last_group = (s.hi - 1) & ~15;
+  uint8_t* lv = lds + wave * kWave;
+  S st;
+  int ids[2] = {0, 0};                 // pages of the next tile's two groups
+  auto look_up = [&](int key0) {
+    if (!table) return;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int g = key0 + 16 * p < last_group ? key0 + 16 * p : last_group;
+      ids[p] = table[a.page.div(static_cast<unsigned>(g))];
+    }
+  };
+  int key0 = begin + wave * S::kKeys;
+  constexpr int kStride = 4 * S::kKeys;
+  if (key0 < end) {
+    look_up(key0);
+    st.locate(a, s, head_k, head_v, key0, ids);
+    st.load_k();
+    st.load_v();
+    if (key0 + kStride < end) look_up(key0 + kStride);
+  }
+  for (; key0 < end; key0 += kStride) {
+    const bool more = key0 + kStride < end;
+    f32x4 sc[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      sc[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i)
+        sc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(st.k_operand(p, i), qf[i], sc[p], 0, 0, 0);
+    }
+    st.store_v(lv);
+    if (more) {
+      st.locate(a, s, head_k, head_v, key0 + kStride, ids);
+      st.load_k();
+      st.load_v();
+      if (key0 + 2 * kStride < end) look_up(key0 + 2 * kStride);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = key0 + 16 * p + 4 * quad + i;
+        if (j < see_lo || j >= see_hi) sc[p][i] = kNegInf;
+      }
+    float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                      fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+    top = quad_max(top) * c;
+    if (__any(top > m + kSlack)) {
+      const float m2 = fmaxf(m, top);
+      const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
+      m = m2;
+      l *= f;
+#pragma unroll
+      for (int b = 0; b < kDb; ++b) acc[b] *= f;
+    }
+    const float shift = (m == kNegInf ? 0.0f : m) - kLift;
+    u32x4 pf;
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[p][i], c, -shift));
+        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[p][i + 1], c, -shift));
+        l += p0 + p1;
+        pf[2 * p + (i >> 1)] = pack2<FP8>(p0, p1);
+      }
+    const int vr = 4 * quad + (col >> 2);
+#pragma unroll
+    for (int b = 0; b < kDb; ++b) {
+      const int vc = 2 * b + ((lane & 3) >> 1);
+      const s16x4 v0 = read_tr(lv + S::v_at(vr, vc) + 8 * (lane & 1));
+      const s16x4 v1 = read_tr(lv + S::v_at(vr + 16, vc) + 8 * (lane & 1));
+      const s16x8 vf = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+      if constexpr (FP8)
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, vf),
+                                                        __builtin_bit_cast(half8_t, pf), acc[b], 0, 0, 0);
+      else
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf),
+                                                         __builtin_bit_cast(bf16x8, pf), acc[b], 0, 0, 0);
+    }
+  }
+  // join the waves: rows of sums in LDS, 16-byte pieces exchanged by row
+  l = quad_sum(l);
+  if (quad == 0) {
+    lds_m[wave][col] = m;
+    lds_l[wave][col] = l;
+  }
+#pragma unroll
+  for (int b = 0; b < kDb; ++b)
+    *reinterpret_cast<f32x4*>(lv + col * (D * 4) + (((4 * b + quad) ^ col) << 4)) = acc[b];
+  __syncthreads();
+  const int row = threadIdx.x >> 4, piece = threadIdx.x & 15;
+  if (row >= n_rows) return;
+  float w[4], mm = kNegInf, ll = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (lds_l[i][row] > 0.0f) mm = fmaxf(mm, lds_m[i][row]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = lds_l[i][row] > 0.0f ? __builtin_amdgcn_exp2f(lds_m[i][row] - mm) : 0.0f;
+    ll = __builtin_fmaf(lds_l[i][row], w[i], ll);
+  }
+  const int out_token = static_cast<int>(a.group.div(row));
+  const int out_head = kvh * group + row - out_token * group;
+  const int64_t at = few_slot(a, split, r, kvh, row);
+  const float inv = ll > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / ll : 0.0f;
+  uint8_t* op = a.out + (static_cast<int64_t>(s.token0) + out_token) * a.out_token + out_head * a.out_head;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    const int ch = piece + 16 * e;
+    f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 p = *reinterpret_cast<const f32x4*>(lds + i * kWave + row * (D * 4) + ((ch ^ row) << 4));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(p[x], w[i], o[x]);
+    }
+    if (splits == 1) {
+      const u32x2 packed = {pack2<false>(o[0] * inv, o[1] * inv), pack2<false>(o[2] * inv, o[3] * inv)};
+      *reinterpret_cast<u32x2*>(op + ch * 8) = packed;
+    } else {
+      *reinterpret_cast<f32x4*>(a.part + at * D + ch * 4) = o;
+    }
+  }
+  if (splits > 1 && piece == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{mm, ll};
 }
 
 // Joins the chunks of each row: one wave a row.
@@ -483,23 +792,28 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   const int r = find_request<true>(a, t);
   const int group = static_cast<int>(a.group.d);
   const int token0 = clampi(a.cu[r], 0, a.n_tokens);
-  if (t >= a.cu[r + 1] || t < token0) return;        // rows of no request
-  const int tile_row = ((t - token0) * group + head % group) / kTileRows * kTileRows;
-  const Span s = span_of(a, r, tile_row, kTileRows);
-  const int splits = splits_of(a, s);
+  const int token1 = clampi(a.cu[r + 1], token0, a.n_tokens);
+  if (t < token0 || t >= token1) return;             // a row of no request
+  const int kvh = static_cast<int>(a.group.div(static_cast<unsigned>(head)));
+  const int in_request = (t - token0) * group + head - kvh * group;
+  const bool few = a.few_splits > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
+  const Span s = few ? span_of(a, r, 0, kFewRows)
+                     : span_of(a, r, in_request / kTileRows * kTileRows, kTileRows);
+  const int splits = few ? splits_of(s, a.few_chunk, a.few_splits) : splits_of(s, a.chunk, a.splits);
   if (splits == 1) return;
-  const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
+  const int64_t at = few ? few_slot(a, 0, r, kvh, in_request) : tile_slot(a, 0, t, head);
+  const int64_t step = few ? few_slot(a, 1, r, kvh, in_request) - at : tile_slot(a, 1, t, head) - at;
   float m = kNegInf;
   for (int i = 0; i < splits; ++i) {
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (i * rows + row) * 2);
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + i * step) * 2);
     if (ml[1] > 0.0f) m = fmaxf(m, ml[0]);
   }
   float l = 0.0f, o[kEach] = {};
   for (int i = 0; i < splits; ++i) {
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (i * rows + row) * 2);
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + i * step) * 2);
     const float f = ml[1] > 0.0f ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
     l = __builtin_fmaf(ml[1], f, l);
-    const float* p = a.part + (i * rows + row) * D + lane * kEach;
+    const float* p = a.part + (at + i * step) * D + lane * kEach;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) o[e] = __builtin_fmaf(p[e], f, o[e]);
   }
@@ -512,35 +826,70 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kLongest = 2048;
 
 struct Plan {
-  int64_t tiles, splits, chunk;
+  int64_t tiles, splits, chunk;           // tiles == 0: no request of many rows
+  int64_t few_splits, few_chunk;          // few_splits == 0: none of few
+  int64_t slots;                          // places of chunks' sums
 };
 
-Plan plan_of(const AttnCall& c) {
-  Plan p;
-  const int64_t group = c.n_heads / c.n_kv_heads;
-  p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
-  // keys of the longest tile, its first group rounded down included
-  int64_t keys = c.table ? c.max_kv : c.max_new;
-  const int64_t tokens = kTileRows / group + 2;
-  if (c.window && keys > c.window + tokens) keys = c.window + tokens;
-  keys += 15;
-  const int64_t wgs = p.tiles * c.n_kv_heads;
-  // fill the CUs twice over, with chunks of at least 256 keys
-  int64_t want = (2 * kCus + wgs - 1) / wgs;
-  const int64_t most = (keys + 255) / 256;
+// Chunks that fill `fill` workgroups when `items` take one each: whole
+// multiples of `unit` keys, at least `least`.
+void cut(int64_t keys, int64_t items, int64_t fill, int64_t unit, int64_t least, int64_t* splits,
+         int64_t* chunk) {
+  int64_t want = (fill + items - 1) / items;
+  const int64_t most = (keys + least - 1) / least;
   want = want < most ? want : most;
-  p.chunk = ((keys + want - 1) / want + 127) / 128 * 128;
-  p.splits = (keys + p.chunk - 1) / p.chunk;
+  want = want > 1 ? want : 1;
+  *chunk = ((keys + want - 1) / want + unit - 1) / unit * unit;
+  if (*chunk < unit) *chunk = unit;
+  *splits = (keys + *chunk - 1) / *chunk;
+  if (*splits < 1) *splits = 1;
+}
+
+// Keys that the first and last of `tokens` neighbours see together, the
+// first 16-key group rounded down included.
+int64_t span_keys(const AttnCall& c, int64_t tokens) {
+  const int64_t keys = c.table ? c.max_kv : c.max_new;
+  const int64_t seen = c.window + tokens - 1;
+  return (c.window && c.causal && keys > seen ? seen : keys) + 15;
+}
+
+Plan plan_of(const AttnCall& c) {
+  Plan p = {};
+  const int64_t group = c.n_heads / c.n_kv_heads;
+  // a prompt of few rows has few keys too: its tile costs no more
+  const bool few = c.table && group <= kFewRows;
+  const bool many = !c.table || c.max_new * group > kFewRows;
+  if (many) {
+    p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
+    cut(span_keys(c, kTileRows / group + 2), p.tiles * c.n_kv_heads, 2 * kCus, 128, 256, &p.splits,
+        &p.chunk);
+  }
+  if (few)
+  {
+    const int64_t keys = span_keys(c, kFewRows), items = c.n_requests * c.n_kv_heads;
+    // lengths differ: no workgroup takes more than kLongest keys while
+    // another has none (but for so many requests that they balance anyway)
+    const int64_t by_length = items < (1 << 16) ? items * ((keys + kLongest - 1) / kLongest) : 0;
+    cut(keys, items, by_length > 4 * kCus ? by_length : 4 * kCus, 128, 256, &p.few_splits,
+        &p.few_chunk);
+  }
+  if (p.splits > 1) p.slots += p.splits * c.n_tokens * c.n_heads;
+  if (p.few_splits > 1) p.slots += p.few_splits * c.n_requests * c.n_kv_heads * kFewRows;
   return p;
 }
 
 template <int D, bool FP8>
 void launch(const Args& a, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.tiles) * a.splits * a.n_kv_heads);
-  attn_tile_kernel<D, FP8><<<grid, 256, 0, stream>>>(a);
-  if (a.splits > 1) {
+  if (a.tiles > 0)
+    attn_tile_kernel<D, FP8><<<static_cast<unsigned>(static_cast<int64_t>(a.tiles) * a.splits * a.n_kv_heads),
+                               256, 0, stream>>>(a);
+  if (a.few_splits > 0)
+    few_rows_kernel<D, FP8><<<static_cast<unsigned>(static_cast<int64_t>(a.n_requests) * a.few_splits * a.n_kv_heads),
+                              256, 0, stream>>>(a);
+  if (a.splits > 1 || a.few_splits > 1) {
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
     combine_kernel<D, FP8><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
   }
@@ -549,9 +898,7 @@ void launch(const Args& a, hipStream_t stream) {
 }  // namespace
 
 int64_t attention_workspace(const AttnCall& c) {
-  const Plan p = plan_of(c);
-  if (p.splits <= 1) return 0;
-  return p.splits * c.n_tokens * c.n_heads * (c.d + 2) * 4;
+  return plan_of(c).slots * (c.d + 2) * 4;
 }
 
 hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
@@ -579,7 +926,7 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.k_scale = c.pool.k_scale;
   a.v_scale = c.pool.v_scale;
   a.part = static_cast<float*>(c.workspace);
-  a.part_ml = a.part + p.splits * c.n_tokens * c.n_heads * c.d;
+  a.part_ml = a.part + p.slots * c.d;
   a.scale_log2 = c.scale * kLog2e;
   a.n_requests = static_cast<int>(c.n_requests);
   a.n_tokens = static_cast<int>(c.n_tokens);
@@ -595,6 +942,8 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.tiles = static_cast<int>(p.tiles);
   a.splits = static_cast<int>(p.splits);
   a.chunk = static_cast<int>(p.chunk);
+  a.few_splits = static_cast<int>(p.few_splits);
+  a.few_chunk = static_cast<int>(p.few_chunk);
   const bool fp8 = paged && c.pool.fp8;
   if (c.d == 64) fp8 ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
   else if (c.d == 128) fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
