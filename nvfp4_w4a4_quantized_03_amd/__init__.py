@@ -129,8 +129,14 @@ def _check(rc, what=""):
                          (" [%s]" % what if what else ""))
 
 
+# The current stream's handle without the Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ptr(t):
@@ -480,53 +486,52 @@ def _ints(t, name, dtype, device, numel=None):
     return t.data_ptr()
 
 
-def _table_args(t, device, rows=None):
+def _table_args(t, device, rows):
     """Pointer, columns and row stride of an int32 block table."""
     _device_tensor(t, "block_table", torch.int32, device=device)
-    if t.dim() != 2 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1) \
-            or (rows is not None and t.shape[0] != rows):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] < 1 or \
+            (shape[1] > 1 and stride[1] != 1):
         raise ValueError("block_table must be int32 [n_requests, max_blocks] "
                          "with unit column stride")
-    rows, cols = t.shape
-    return t.data_ptr(), cols, t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), shape[1], stride[0] if rows > 1 else shape[1]
 
 
 def _head_rows(t, name, device=None, dtype=torch.bfloat16, shape=None):
     """Pointer, token stride and head stride of [tokens, heads, d] rows."""
     _device_tensor(t, name, dtype, device=device)
-    if t.dim() != 3 or t.stride(2) != 1 or (shape is not None and
-                                            t.shape != shape):
+    got, stride = t.shape, t.stride()
+    if len(got) != 3 or stride[2] != 1 or (shape is not None and got != shape):
         raise ValueError("%s must be [tokens, heads, d] with unit stride along "
                          "d, and agree with the other operands" % name)
-    tokens, heads, d = t.shape
+    tokens, heads, d = got
     # strides of axes of length one are arbitrary
-    ts, hs = t.stride(0), t.stride(1)
-    if heads == 1:
-        hs = d
-    return t.data_ptr(), ts if tokens > 1 else max(d, hs * heads), hs
+    hs = stride[1] if heads > 1 else d
+    return t.data_ptr(), stride[0] if tokens > 1 else max(d, hs * heads), hs
 
 
 def _pool_args(k_cache, v_cache, k_scale, v_scale, device):
     """Arguments of the paged caches, in the C ABI's order without scales:
     pointers, dtype, sizes and strides; and the scales' pointers."""
     _device_tensor(k_cache, "k_cache", device=device)
-    _device_tensor(v_cache, "v_cache", k_cache.dtype, device=device)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or \
-            k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+    dtype, shape, stride = k_cache.dtype, k_cache.shape, k_cache.stride()
+    _device_tensor(v_cache, "v_cache", dtype, device=device)
+    if len(shape) != 4 or v_cache.shape != shape or \
+            v_cache.stride() != stride or stride[3] != 1:
         raise ValueError("k_cache and v_cache must be [n_pages, n_kv_heads, "
                          "page_size, d] with the same strides, unit along d")
-    if k_cache.dtype == torch.uint8:
+    if dtype == torch.uint8:
         dt = DTYPE_E4M3
         _global_tensor(k_scale, "k_scale", device)
         _global_tensor(v_scale, "v_scale", device)
         scales = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_cache.dtype == torch.bfloat16:
+    elif dtype == torch.bfloat16:
         dt = DTYPE_BF16
         scales = None, None
     else:
         raise ValueError("caches must be bfloat16 or uint8 (E4M3 codes)")
-    pages, heads, page, d = k_cache.shape
-    ps, hs, ts, _ = k_cache.stride()
+    pages, heads, page, d = shape
+    ps, hs, ts, _ = stride
     if pages == 1:
         ps = max(ps, d)
     if heads == 1:
@@ -553,23 +558,25 @@ def kv_page_tables(new_lens, cached_lens, block_table, free_pages, page_size,
     held = _ints(cached_lens, "cached_lens", torch.int32, dev, n)
     table, cols, ld = _table_args(block_table, dev, n)
     free = _ints(free_pages, "free_pages", torch.int32, dev)
-    n_tokens = int(n_tokens)
-    if n_tokens < 0:
+    t = int(n_tokens)
+    if t < 0:
         raise ValueError("n_tokens must not be negative")
     if out is None:
-        # one allocation: the int64 slots, then the int32 arrays
-        buf = torch.empty(3 * n_tokens + 2 * n + 2, dtype=torch.int32, device=dev)
-        at = 2 * n_tokens
-        out = KVPages(buf[at:at + n + 1], buf[at + n + 1:at + 2 * n + 1],
-                      buf[at + 2 * n + 2:], buf[:at].view(torch.int64),
-                      buf[at + 2 * n + 1:at + 2 * n + 2])
-    p = [_ints(t, nm, dt, dev, num) for t, nm, dt, num in
-         zip(out, KVPages._fields,
-             (torch.int32, torch.int32, torch.int32, torch.int64, torch.int32),
-             (n + 1, n, n_tokens, n_tokens, 1))]
+        slots = new_lens.new_empty(t, dtype=torch.int64)
+        buf = new_lens.new_empty(t + 2 * n + 2)
+        cu, kv, positions, used = buf.split_with_sizes((n + 1, n, t, 1))
+        out = KVPages(cu, kv, positions, slots, used)
+        at = buf.data_ptr()
+        p = (at, at + 4 * n + 4, at + 8 * n + 4, slots.data_ptr(),
+             at + 8 * n + 4 + 4 * t)
+    else:
+        p = [_ints(b, nm, dt, dev, num) for b, nm, dt, num in
+             zip(out, KVPages._fields,
+                 (torch.int32, torch.int32, torch.int32, torch.int64, torch.int32),
+                 (n + 1, n, t, t, 1))]
     _check(library().kv_page_tables(news, held, n, table, cols, ld, free,
-                                    free_pages.numel(), int(page_size),
-                                    n_tokens, *p, _stream(new_lens)),
+                                    free_pages.numel(), int(page_size), t, *p,
+                                    _stream(new_lens)),
            "kv_page_tables")
     return out
 
@@ -583,21 +590,23 @@ def kv_page_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None):
     the static scales (float32 [1], fp8_kv_calibrate); any order of the first
     three axes in memory.  slots: int64 [n_tokens]; one outside the cache is
     skipped."""
-    dt = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}.get(
-        getattr(k, "dtype", None))
-    if dt is None:
+    dtype = getattr(k, "dtype", None)
+    if dtype == torch.bfloat16:
+        dt = DTYPE_BF16
+    elif dtype == torch.float32:
+        dt = DTYPE_F32
+    else:
         raise ValueError("k must be a float32 or bfloat16 tensor")
-    kp = _head_rows(k, "k", None, k.dtype)
-    dev = k.device
-    vp = _head_rows(v, "v", dev, k.dtype, k.shape)
+    kp = _head_rows(k, "k", None, dtype)
+    dev, shape = k.device, k.shape
+    vp = _head_rows(v, "v", dev, dtype, shape)
     pool, scales = _pool_args(k_cache, v_cache, k_scale, v_scale, dev)
-    if (k.shape[1], k.shape[2]) != (pool[5], pool[6]):
+    tokens, heads, d = shape
+    if heads != pool[5] or d != pool[6]:
         raise ValueError("k and the caches disagree in heads or d")
-    tokens = k.shape[0]
     sl = _ints(slots, "slots", torch.int64, dev, tokens)
     _check(library().kv_page_write(*kp, *vp, dt, tokens, *pool, *scales, sl,
-                                   _stream(k)),
-           "kv_page_write tokens=%d" % tokens)
+                                   _stream(k)), "kv_page_write")
 
 
 @functools.lru_cache(maxsize=4096)
@@ -607,14 +616,13 @@ def _attention_workspace(paged, *sizes):
     return fn(*sizes)
 
 
-def _workspace(q, paged, *sizes):
-    """A buffer of the bytes that the call asks for (none: a null pointer).
-    It is allocated on the current stream and used there only."""
-    n = _attention_workspace(paged, *sizes)
-    if n <= 0:
-        return None, None, 0
-    ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-    return ws, ws.data_ptr(), n
+def _out_rows(out, q):
+    """The output, a new one if none is given, and its arguments."""
+    if out is not None:
+        return out, _head_rows(out, "out", q.device, shape=q.shape)
+    _, heads, d = q.shape
+    out = q.new_empty(q.shape)
+    return out, (out.data_ptr(), heads * d, d)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new,
@@ -636,25 +644,25 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new,
     dev = q.device
     tokens, heads, d = q.shape
     pool, scales = _pool_args(k_cache, v_cache, k_scale, v_scale, dev)
-    if d != pool[6] or heads % pool[5] != 0:
+    kv_heads = pool[5]
+    if d != pool[6] or heads % kv_heads != 0:
         raise ValueError("q and the caches disagree in d, or the heads are no "
                          "multiple of the caches'")
-    n = kv_lens.numel()
     kv = _ints(kv_lens, "kv_lens", torch.int32, dev)
+    n = kv_lens.numel()
     cu = _ints(cu_new, "cu_new", torch.int32, dev, n + 1)
-    table, cols, ld = _table_args(block_table, dev, n)
-    if out is None:
-        out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
-    op = _head_rows(out, "out", dev, shape=q.shape)
+    table = _table_args(block_table, dev, n)
+    out, op = _out_rows(out, q)
     max_new, max_kv, window = int(max_new), int(max_kv), int(window)
-    ws, wp, wn = _workspace(q, True, tokens, heads, pool[5], d, n, max_new,
-                            max_kv, window)
+    # the workspace is allocated on the current stream and used there only
+    size = _attention_workspace(True, tokens, heads, kv_heads, d, n, max_new,
+                                max_kv, window)
+    work = q.new_empty(size, dtype=torch.uint8) if size > 0 else None
     _check(library().kv_paged_attention(
-        *qp, tokens, heads, *pool, *scales, table, cols, ld, cu, kv, n,
-        max_new, max_kv, d ** -0.5 if scale is None else scale,
-        1 if causal else 0, window, *op, wp, wn, _stream(q)),
-        "paged_attention tokens=%d heads=%d d=%d requests=%d"
-        % (tokens, heads, d, n))
+        *qp, tokens, heads, *pool, *scales, *table, cu, kv, n, max_new, max_kv,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, window, *op,
+        work.data_ptr() if size > 0 else None, size, _stream(q)),
+        "paged_attention")
     return out
 
 
@@ -671,24 +679,23 @@ def prompt_attention(q, k, v, cu_lens, max_len, scale=None, causal=True,
     dev = q.device
     tokens, heads, d = q.shape
     kp = _head_rows(k, "k", dev)
-    vp = _head_rows(v, "v", dev, shape=k.shape)
-    kv_heads = k.shape[1]
-    if k.shape[0] != tokens or k.shape[2] != d or kv_heads < 1 or \
+    shape = k.shape
+    vp = _head_rows(v, "v", dev, shape=shape)
+    kv_heads = shape[1]
+    if shape[0] != tokens or shape[2] != d or kv_heads < 1 or \
             heads % kv_heads != 0:
         raise ValueError("q and k disagree in tokens or d, or the heads are no "
                          "multiple of k's")
-    n = cu_lens.numel() - 1
     cu = _ints(cu_lens, "cu_lens", torch.int32, dev)
-    if out is None:
-        out = torch.empty((tokens, heads, d), dtype=torch.bfloat16, device=dev)
-    op = _head_rows(out, "out", dev, shape=q.shape)
+    n = cu_lens.numel() - 1
+    out, op = _out_rows(out, q)
     max_len, window = int(max_len), int(window)
-    ws, wp, wn = _workspace(q, False, tokens, heads, kv_heads, d, n, max_len,
-                            window)
+    size = _attention_workspace(False, tokens, heads, kv_heads, d, n, max_len,
+                                window)
+    work = q.new_empty(size, dtype=torch.uint8) if size > 0 else None
     _check(library().prompt_attention(
         *qp, *kp, *vp, tokens, heads, kv_heads, d, cu, n, max_len,
-        d ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-        *op, wp, wn, _stream(q)),
-        "prompt_attention tokens=%d heads=%d d=%d prompts=%d"
-        % (tokens, heads, d, n))
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, window, *op,
+        work.data_ptr() if size > 0 else None, size, _stream(q)),
+        "prompt_attention")
     return out

@@ -167,6 +167,14 @@ __device__ __forceinline__ int64_t few_slot(const Args& a, int split, int r, int
 
 // ---------------------------------------------------------------- staging
 
+// 16 bytes from global memory: said so, since a load that might be of LDS
+// counts with the LDS reads and makes each of their waits wait for it.
+__device__ __forceinline__ u32x4 load16b(const uint8_t* base, unsigned off) {
+  typedef const __attribute__((address_space(1))) uint8_t* gptr;
+  typedef const __attribute__((address_space(1))) u32x4* gvec;
+  return *(gvec)((gptr)base + off);
+}
+
 __device__ const u32x4 kZeros[64] = {};           // a row for pages out of range
 
 template <int D, bool FP8>
@@ -216,34 +224,34 @@ struct Stage {
     int g = key0 + wave * T::kRows;               // uniform; 16 keys share a page
     const int last = (s.hi - 1) & ~(T::kRows - 1);
     g = g < last ? g : last;
-    const uint8_t* kb;
-    const uint8_t* vb;
-    int64_t kt = a.k_token, vt = a.v_token;
+    int kt = static_cast<int>(a.k_token), vt = static_cast<int>(a.v_token);
+    const uint8_t* kb = a.k + head_k;
+    const uint8_t* vb = a.v + head_v;
+    int first = s.lo - g, end = s.hi - 1 - g;
     if (row_of_table) {
       const int blk = static_cast<int>(a.page.div(static_cast<unsigned>(g)));
       const int id = row_of_table[blk];
       const int off = g - blk * static_cast<int>(a.page.d);
       if (id >= 0 && id < a.n_pages) {
-        kb = a.k + id * a.page_stride + head_k + off * kt;
-        vb = a.v + id * a.page_stride + head_v + off * vt;
+        kb += id * a.page_stride + static_cast<int64_t>(off) * kt;
+        vb += id * a.page_stride + static_cast<int64_t>(off) * vt;
       } else {
         kb = vb = reinterpret_cast<const uint8_t*>(kZeros);
-        kt = vt = 0;
+        first = end = 0;                          // every row at the one of zeros
       }
     } else {
-      kb = a.k + (static_cast<int64_t>(s.token0) + g) * kt + head_k;
-      vb = a.v + (static_cast<int64_t>(s.token0) + g) * vt + head_v;
+      kb += (static_cast<int64_t>(s.token0) + g) * a.k_token;
+      vb += (static_cast<int64_t>(s.token0) + g) * a.v_token;
     }
-    const int first = s.lo - g, end = s.hi - 1 - g;
+    const int r = lane / T::kChunks, c = (lane % T::kChunks) * 16;
+    constexpr int kStep = 64 / T::kChunks;        // rows from one load to the next
+    // the clamp on byte offsets: no multiplication per load
+    const int ko = r * kt, k_first = first * kt, k_end = end * kt;
+    const int vo = r * vt, v_first = first * vt, v_end = end * vt;
 #pragma unroll
     for (int i = 0; i < T::kLoads; ++i) {
-      const int at = i * 64 + lane;
-      int r = at / T::kChunks;
-      const int c = at % T::kChunks;
-      r = r < first ? first : r;
-      r = r > end ? end : r;
-      k[i] = *reinterpret_cast<const u32x4*>(kb + r * static_cast<int>(kt) + c * 16);
-      v[i] = *reinterpret_cast<const u32x4*>(vb + r * static_cast<int>(vt) + c * 16);
+      k[i] = load16b(kb, min(max(ko + i * kStep * kt, k_first), k_end) + c);
+      v[i] = load16b(vb, min(max(vo + i * kStep * vt, v_first), v_end) + c);
     }
   }
 
@@ -551,9 +559,9 @@ struct Stream {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const uint8_t* row = kb[p] + inside(lane & 15, first[p], end[p]) * kt + (lane >> 4) * 16;
+      const int row = inside(lane & 15, first[p], end[p]) * kt + (lane >> 4) * 16;
 #pragma unroll
-      for (int i = 0; i < kK; ++i) k[p][i] = *reinterpret_cast<const u32x4*>(row + i * 64);
+      for (int i = 0; i < kK; ++i) k[p][i] = load16b(kb[p], row + i * 64);
     }
   }
   __device__ __forceinline__ void load_v() {
@@ -562,7 +570,7 @@ struct Stream {
     for (int i = 0; i < kV; ++i) {
       const int p = i * 64 / kChunks / 16;                  // a load lies in one group
       const int r = (i * 64 + lane) / kChunks - 16 * p, c = (i * 64 + lane) % kChunks;
-      v[i] = *reinterpret_cast<const u32x4*>(vb[p] + inside(r, first[p], end[p]) * vt + c * 16);
+      v[i] = load16b(vb[p], inside(r, first[p], end[p]) * vt + c * 16);
     }
   }
   // The 8 rows that 32 lanes of a transposing read touch differ by 32 bytes.
