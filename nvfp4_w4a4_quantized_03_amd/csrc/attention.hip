@@ -56,7 +56,9 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTileRows = 128;         // rows of a workgroup, 32 a wave
+// Rows of a workgroup's tile: 4 waves of one or two 32-column blocks.
+constexpr int tile_blocks(int d) { return 1; }
+constexpr int tile_rows(int d) { return 128 * tile_blocks(d); }
 constexpr int kFewRows = 16;           // rows of a request that few_rows_kernel takes
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNegInf = -__builtin_inff();
@@ -82,7 +84,7 @@ struct Args {
   int n_requests, n_tokens, n_heads, n_kv_heads, n_pages;
   FastDiv group, page;
   int64_t cols_len;                               // columns * page size
-  int max_kv, causal, window, tiles;
+  int max_kv, causal, window, tiles, tile_rows;
   // chunks of keys: of tiles of many rows, of requests of few
   int splits, chunk, few_splits, few_chunk;
 };
@@ -91,11 +93,11 @@ __device__ __forceinline__ int clampi(int64_t x, int64_t lo, int64_t hi) {
   return static_cast<int>(x < lo ? lo : x > hi ? hi : x);
 }
 
-// First tile of request i: floor(rows before / kTileRows) + i leaves every
+// First tile of request i: floor(rows before / tile_rows) + i leaves every
 // request at least the tiles it fills, without a prefix sum of its own.
 __device__ __forceinline__ int64_t first_tile(const Args& a, int i) {
   const int64_t rows = static_cast<int64_t>(clampi(a.cu[i], 0, a.n_tokens)) * a.group.d;
-  return rows / kTileRows + i;
+  return (rows >> (a.tile_rows == 256 ? 8 : 7)) + i;
 }
 
 // The request of tile t: the last i with first_tile(i) <= t (or, BY_TOKEN,
@@ -177,6 +179,22 @@ __device__ __forceinline__ u32x4 load16b(const uint8_t* base, unsigned off) {
 
 __device__ const u32x4 kZeros[64] = {};           // a row for pages out of range
 
+// A resource over the bytes from base on (32-bit offsets), and 16 bytes per
+// lane from it straight to LDS at lds + 16 * lane.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  const unsigned lo = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p));
+  const unsigned hi = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, 0x7FFFFFFF, 0x00020000);
+}
+__device__ __forceinline__ void lds_load16(__amdgpu_buffer_rsrc_t rsrc, uint8_t* lds, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 16,
+                                           off, 0, 0, 0);
+#endif
+}
+
 template <int D, bool FP8>
 struct Tile {
   static constexpr int kKeys = D > 128 ? 32 : 64;       // keys of a tile
@@ -187,11 +205,15 @@ struct Tile {
   // LDS bytes of 16-byte chunk c of row r.  K: the 16 rows that a fragment
   // read touches at once differ in their place; V: the 4 rows of a
   // transposing read do, by whole 64-byte pieces.
+  static __device__ __forceinline__ int k_swap(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
+  static __device__ __forceinline__ int v_swap(int r) {
+    return D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+  }
   static __device__ __forceinline__ int k_at(int r, int c) {
-    return r * (D * 2) + ((c ^ (D == 64 ? (r >> 1) & 7 : r & 15)) << 4);
+    return r * (D * 2) + ((c ^ k_swap(r)) << 4);
   }
   static __device__ __forceinline__ int v_at(int r, int c) {
-    return r * (D * 2) + ((c ^ (D == 64 ? ((r >> 1) & 1) << 2 : (r & 3) << 2)) << 4);
+    return r * (D * 2) + ((c ^ v_swap(r)) << 4);
   }
 };
 
@@ -209,79 +231,107 @@ __device__ __forceinline__ u32x2 widen4(unsigned w) {
   return r;
 }
 
-template <int D, bool FP8>
+// Page of a 16-key group: a scalar load, whatever the stores around it (the
+// table does not change during a launch).
+__device__ __forceinline__ int page_of(const Args& a, const int32_t* row_of_table, int key) {
+  typedef const __attribute__((address_space(4))) int32_t* cptr;
+  return ((cptr)row_of_table)[a.page.div(static_cast<unsigned>(key))];
+}
+
+// Where `rows` keys from `key` on (of one 16-key group) are, and which of them
+// may be read: rows outside [lo, hi) are read at the nearest one inside, so
+// that whatever a cache holds past a request's end is never used.  A page
+// out of range reads as zeros.
+struct Place {
+  const uint8_t* k;
+  const uint8_t* v;
+  int first, end;
+};
+template <int ROWS>
+__device__ __forceinline__ int group_at(const Span& s, int key) {
+  const int last = (s.hi - 1) & ~(ROWS - 1);
+  return key < last ? key : last;
+}
+template <int ROWS>
+__device__ __forceinline__ Place place_of(const Args& a, const Span& s, int64_t head_k,
+                                          int64_t head_v, int key, int id) {
+  const int g = group_at<ROWS>(s, key);
+  Place p = {a.k + head_k, a.v + head_v, s.lo - g, s.hi - 1 - g};
+  if (a.table) {
+    const int off = g - static_cast<int>(a.page.div(static_cast<unsigned>(g)) * a.page.d);
+    if (id >= 0 && id < a.n_pages) {
+      const int64_t at = id * a.page_stride + off * a.k_token;    // K and V alike
+      p.k += at;
+      p.v += at;
+    } else {
+      p.k = p.v = reinterpret_cast<const uint8_t*>(kZeros);
+      p.first = p.end = 0;               // every row at the one of zeros
+    }
+  } else {
+    p.k += (static_cast<int64_t>(s.token0) + g) * a.k_token;
+    p.v += (static_cast<int64_t>(s.token0) + g) * a.v_token;
+  }
+  return p;
+}
+
+// A wave's rows of K or V of one tile on their way to LDS: bf16 straight
+// from memory (no registers), E4M3 codes through registers, widened there.
+template <int D, bool FP8, bool IS_V>
 struct Stage {
   using T = Tile<D, FP8>;
-  u32x4 k[T::kLoads], v[T::kLoads];
+  u32x4 x[FP8 ? T::kLoads : 1];
 
-  // Keys [key0, key0 + kKeys) of the request: this wave's rows.  Rows
-  // outside [lo, hi) are read at the nearest one inside, so that whatever
-  // a cache holds past a request's end is never used; pages out of range
-  // read as zeros.
-  __device__ __forceinline__ void load(const Args& a, const Span& s, const int32_t* row_of_table,
-                                       int64_t head_k, int64_t head_v, int key0, int wave) {
+  __device__ __forceinline__ void load(const Place& p, int stride, int wave, uint8_t* lds) {
     const int lane = threadIdx.x & 63;
-    int g = key0 + wave * T::kRows;               // uniform; 16 keys share a page
-    const int last = (s.hi - 1) & ~(T::kRows - 1);
-    g = g < last ? g : last;
-    int kt = static_cast<int>(a.k_token), vt = static_cast<int>(a.v_token);
-    const uint8_t* kb = a.k + head_k;
-    const uint8_t* vb = a.v + head_v;
-    int first = s.lo - g, end = s.hi - 1 - g;
-    if (row_of_table) {
-      const int blk = static_cast<int>(a.page.div(static_cast<unsigned>(g)));
-      const int id = row_of_table[blk];
-      const int off = g - blk * static_cast<int>(a.page.d);
-      if (id >= 0 && id < a.n_pages) {
-        kb += id * a.page_stride + static_cast<int64_t>(off) * kt;
-        vb += id * a.page_stride + static_cast<int64_t>(off) * vt;
-      } else {
-        kb = vb = reinterpret_cast<const uint8_t*>(kZeros);
-        first = end = 0;                          // every row at the one of zeros
-      }
-    } else {
-      kb += (static_cast<int64_t>(s.token0) + g) * a.k_token;
-      vb += (static_cast<int64_t>(s.token0) + g) * a.v_token;
-    }
-    const int r = lane / T::kChunks, c = (lane % T::kChunks) * 16;
+    const uint8_t* base = IS_V ? p.v : p.k;
+    const int r0 = lane / T::kChunks, c0 = lane % T::kChunks;
     constexpr int kStep = 64 / T::kChunks;        // rows from one load to the next
     // the clamp on byte offsets: no multiplication per load
-    const int ko = r * kt, k_first = first * kt, k_end = end * kt;
-    const int vo = r * vt, v_first = first * vt, v_end = end * vt;
+    const int first = p.first * stride, end = p.end * stride;
+    if constexpr (FP8) {
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-      k[i] = load16b(kb, min(max(ko + i * kStep * kt, k_first), k_end) + c);
-      v[i] = load16b(vb, min(max(vo + i * kStep * vt, v_first), v_end) + c);
+      for (int i = 0; i < T::kLoads; ++i)
+        x[i] = load16b(base, min(max(r0 * stride + i * kStep * stride, first), end) + c0 * 16);
+    } else {
+      // LDS takes consecutive lanes' pieces one after another; which chunk of
+      // the row a lane brings makes the exchange
+      const auto rsrc = resource(base);
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) {
+        const int r = wave * T::kRows % 16 + r0 + i * kStep;
+        const int c = c0 ^ (IS_V ? T::v_swap(r) : T::k_swap(r));
+        lds_load16(rsrc, lds + (wave * T::kLoads + i) * 1024,
+                   min(max(r0 * stride + i * kStep * stride, first), end) + c * 16);
+      }
     }
   }
 
-  __device__ __forceinline__ void store(uint8_t* lds_k, uint8_t* lds_v, int wave) const {
-    const int lane = threadIdx.x & 63;
+  // E4M3: the widened values to LDS.
+  __device__ __forceinline__ void store(uint8_t* lds, int wave) const {
+    if constexpr (FP8) {
+      const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) {
-      const int at = i * 64 + lane;
-      const int r = wave * T::kRows + at / T::kChunks, c = at % T::kChunks;
-      if constexpr (FP8) {
+      for (int i = 0; i < T::kLoads; ++i) {
+        const int at = i * 64 + lane;
+        const int r = wave * T::kRows + at / T::kChunks, c = at % T::kChunks;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const u32x2 k0 = widen4<false>(k[i][2 * p]), k1 = widen4<false>(k[i][2 * p + 1]);
-          const u32x2 v0 = widen4<true>(v[i][2 * p]), v1 = widen4<true>(v[i][2 * p + 1]);
-          *reinterpret_cast<u32x4*>(lds_k + T::k_at(r, 2 * c + p)) = u32x4{k0[0], k0[1], k1[0], k1[1]};
-          *reinterpret_cast<u32x4*>(lds_v + T::v_at(r, 2 * c + p)) = u32x4{v0[0], v0[1], v1[0], v1[1]};
+          const u32x2 w0 = widen4<IS_V>(x[i][2 * p]), w1 = widen4<IS_V>(x[i][2 * p + 1]);
+          *reinterpret_cast<u32x4*>(lds + (IS_V ? T::v_at(r, 2 * c + p) : T::k_at(r, 2 * c + p))) =
+              u32x4{w0[0], w0[1], w1[0], w1[1]};
         }
-      } else {
-        *reinterpret_cast<u32x4*>(lds_k + T::k_at(r, c)) = k[i];
-        *reinterpret_cast<u32x4*>(lds_v + T::v_at(r, c)) = v[i];
       }
     }
   }
 };
 
-// Barrier for LDS alone: global loads stay in flight across it.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+// Every wave's part of the next tile is in LDS (loads to LDS count as vector
+// memory) and its reads of this one are done.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);      // vmcnt(0) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  asm volatile("" ::: "memory");
 }
 
 __device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
@@ -301,6 +351,13 @@ __device__ __forceinline__ float half_sum(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// N instructions of a kind (0x008 MFMA, 0x100 LDS reads) next, in the order of
+// these calls.
+template <int KIND, int N>
+__device__ __forceinline__ void order() {
+  __builtin_amdgcn_sched_group_barrier(KIND, N, 0);
+}
+
 template <bool HALF>
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   const f32x2 p = {x, y};
@@ -314,6 +371,8 @@ __device__ __forceinline__ unsigned pack2(float x, float y) {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a) {
   using T = Tile<D, FP8>;
+  constexpr int kNb = tile_blocks(D);
+  constexpr int kRows = tile_rows(D);
   constexpr int kSteps = D / 16;          // of the first product
   constexpr int kBlocks = T::kKeys / 32;  // key blocks of a tile
   constexpr int kDb = D / 32;             // d blocks of the output
@@ -322,7 +381,11 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   // subnormals; 2^14 is still in range)
   constexpr float kSlack = 8.0f;
   constexpr float kLift = FP8 ? 6.0f : 0.0f;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * T::kBytes];
+  constexpr int kReach = 4;
+  // arrays of their own, so that reads of one need not wait for loads into
+  // the other
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k0[T::kBytes], lds_k1[T::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_v0[T::kBytes], lds_v1[T::kBytes];
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
@@ -332,26 +395,36 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   const int tile = a.tiles - 1 - rest / a.splits;    // the longest rows of a prompt first
 
   const int r = __builtin_amdgcn_readfirstlane(find_request<false>(a, tile));
-  const int64_t row0 = (tile - first_tile(a, r)) * kTileRows;
+  const int64_t row0 = (tile - first_tile(a, r)) * kRows;
   const int group = static_cast<int>(a.group.d);
   const int64_t n_rows = static_cast<int64_t>(clampi(a.cu[r + 1], 0, a.n_tokens) -
                                               clampi(a.cu[r], 0, a.n_tokens)) * group;
   if (row0 < 0 || row0 >= n_rows || (a.few_splits > 0 && n_rows <= kFewRows)) return;
-  const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
+  const Span s = span_of(a, r, static_cast<int>(row0), kRows);
   const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
   const int begin = s.start + split * a.chunk;
   const int end = split == splits - 1 ? s.hi : begin + a.chunk;
 
-  // this lane's row
-  const int row = s.row0 + wave * 32 + col;
-  const bool real = row < n_rows;
-  const int token = static_cast<int>(a.group.div(real ? row : 0));
-  const int head = kvh * group + (real ? row - token * group : 0);
-  int see_lo = 0, see_hi = 0;
-  if (real) sees(a, s, token, &see_lo, &see_hi);
-  // what all rows of the wave see, for tiles that need no mask
-  int all_lo = see_lo, all_hi = see_hi, any_lo = real ? see_lo : 0x7FFFFFFF, any_hi = see_hi;
+  // this lane's rows, and what all and any rows of the wave see
+  bool real[kNb];
+  int token[kNb], head[kNb], see_lo[kNb], see_hi[kNb];
+  int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
+#pragma unroll
+  for (int n = 0; n < kNb; ++n) {
+    const int row = s.row0 + (wave * kNb + n) * 32 + col;
+    real[n] = row < n_rows;
+    token[n] = static_cast<int>(a.group.div(real[n] ? row : 0));
+    head[n] = kvh * group + (real[n] ? row - token[n] * group : 0);
+    see_lo[n] = see_hi[n] = 0;
+    if (real[n]) {
+      sees(a, s, token[n], &see_lo[n], &see_hi[n]);
+      any_lo = min(any_lo, see_lo[n]);
+    }
+    all_lo = max(all_lo, see_lo[n]);
+    all_hi = min(all_hi, see_hi[n]);
+    any_hi = max(any_hi, see_hi[n]);
+  }
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     all_lo = max(all_lo, __shfl_xor(all_lo, off));
@@ -364,132 +437,205 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   any_lo = __builtin_amdgcn_readfirstlane(any_lo);
   any_hi = __builtin_amdgcn_readfirstlane(any_hi);
 
-  bf16x8 qf[kSteps];
-  {
-    const uint8_t* qp = a.q + (static_cast<int64_t>(s.token0) + token) * a.q_token + head * a.q_head;
+  bf16x8 qf[kNb][kSteps];
+#pragma unroll
+  for (int n = 0; n < kNb; ++n) {
+    const uint8_t* qp = a.q + (static_cast<int64_t>(s.token0) + token[n]) * a.q_token + head[n] * a.q_head;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      qf[i] = *reinterpret_cast<const bf16x8*>(qp + i * 32 + half * 16);
+      qf[n][i] = *reinterpret_cast<const bf16x8*>(qp + i * 32 + half * 16);
   }
   // a scale of zero makes every score 0; it must not make -inf * 0 of a
   // masked one
   const float c = FP8 ? fmaxf(a.scale_log2 * *a.k_scale, 0x1p-120f) : a.scale_log2;
 
-  f32x16 acc[kDb];
+  f32x16 acc[kNb][kDb];
+  float m[kNb], l[kNb];
 #pragma unroll
-  for (int b = 0; b < kDb; ++b)
+  for (int n = 0; n < kNb; ++n) {
+    m[n] = kNegInf;
+    l[n] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[b][i] = 0.0f;
-  float m = kNegInf, l = 0.0f;
+    for (int b = 0; b < kDb; ++b) acc[n][b] = f32x16{};
+  }
 
   const int32_t* table = a.table ? a.table + r * a.ld_table : nullptr;
   const int64_t head_k = kvh * a.k_head, head_v = kvh * a.v_head;
-  Stage<D, FP8> st;
-  if (begin < end) st.load(a, s, table, head_k, head_v, begin, wave);
-  int buf = 0;
-  for (int key0 = begin; key0 < end; key0 += T::kKeys, buf ^= 1) {
-    uint8_t* lk = lds + buf * 2 * T::kBytes;
-    uint8_t* lv = lk + T::kBytes;
-    // the waves still at the tile before last have passed the last barrier
-    st.store(lk, lv, wave);
-    if (key0 + T::kKeys < end) st.load(a, s, table, head_k, head_v, key0 + T::kKeys, wave);
-    lds_barrier();
-    if (key0 >= any_hi || key0 + T::kKeys <= any_lo) continue;    // no row sees the tile
+  // this lane's reads of a tile: chunk 2 i + half of K row col at ka ^ 32 i,
+  // 4-key piece of V d block b at va ^ 64 b (the exchange by the row's
+  // number is the same in all the rows that are a multiple of 8 further)
+  const int ka = T::k_at(col, half);
+  const int va = T::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) +
+                 8 * (lane & 1);
 
-    f32x16 sc[kBlocks];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sc[b][i] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(lk + T::k_at(32 * b + col, 2 * i + half));
-        sc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], sc[b], 0, 0, 0);
-      }
-    }
-    if (key0 < all_lo || key0 + T::kKeys > all_hi) {
+  Stage<D, FP8, false> xk;
+  Stage<D, FP8, true> xv;
+  int id = 0;                             // page of this wave's rows of the next tile
+  auto look_up = [&](int key0) {
+    if (table) id = page_of(a, table, group_at<T::kRows>(s, key0 + wave * T::kRows));
+  };
+  auto fetch = [&](uint8_t* nk, uint8_t* nv, int key0) {
+    const Place p = place_of<T::kRows>(a, s, head_k, head_v, key0 + wave * T::kRows, id);
+    xk.load(p, static_cast<int>(a.k_token), wave, nk);
+    xv.load(p, static_cast<int>(a.v_token), wave, nv);
+  };
+  // One tile, its keys in (lk, lv); the next one's go to (nk, nv).
+  auto step = [&](const uint8_t* lk, const uint8_t* lv, uint8_t* nk, uint8_t* nv, int key0) {
+    const bool more = key0 + T::kKeys < end;
+    if (more) fetch(nk, nv, key0 + T::kKeys);
+    const bool seen = key0 < any_hi && key0 + T::kKeys > any_lo;      // by some row of the wave
+    if (!seen) look_up(key0 + 2 * T::kKeys);
+    if (seen) {
+      f32x16 sc[kNb][kBlocks];
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = key0 + 32 * b + 8 * (i >> 2) + 4 * half + (i & 3);
-          if (j < see_lo || j >= see_hi) sc[b][i] = kNegInf;
+        for (int i = 0; i < kSteps; ++i) {
+          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(lk + (ka ^ (32 * i)) + 32 * b * D * 2);
+#pragma unroll
+          for (int n = 0; n < kNb; ++n)
+            sc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n][i], i ? sc[n][b] : f32x16{}, 0, 0, 0);
         }
+      // reads kReach products ahead: an LDS read takes several products' time
+      order<0x100, kReach>();
+#pragma unroll
+      for (int i = 0; i < kBlocks * kSteps - kReach; ++i) {
+        order<0x008, kNb>();
+        order<0x100, 1>();
+      }
+      order<0x008, kNb * kReach>();
+      // a scalar load in flight makes LDS waits full ones: here no reads are
+      look_up(key0 + 2 * T::kKeys);
+      if (key0 < all_lo || key0 + T::kKeys > all_hi) {
+#pragma unroll
+        for (int n = 0; n < kNb; ++n)
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              // see_lo <= j < see_hi in one comparison
+              const unsigned j = key0 + 4 * half - see_lo[n] + (32 * b + 8 * (i >> 2) + (i & 3));
+              if (j >= static_cast<unsigned>(see_hi[n] - see_lo[n])) sc[n][b][i] = kNegInf;
+            }
+      }
+      float top[kNb], shift[kNb];
+      bool move = false;
+#pragma unroll
+      for (int n = 0; n < kNb; ++n) {
+        float t = sc[n][0][0];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t = fmaxf(t, sc[n][b][i]);
+        top[n] = half_max(t) * c;
+        move |= top[n] > m[n] + kSlack;
+      }
+      if (__any(move)) {
+#pragma unroll
+        for (int n = 0; n < kNb; ++n) {
+          const float m2 = fmaxf(m[n], top[n]);
+          const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - m2);
+          m[n] = m2;
+          l[n] *= f;
+#pragma unroll
+          for (int b = 0; b < kDb; ++b) acc[n][b] *= f;
+        }
+      }
+      unsigned pw[kNb][kBlocks][8];
+#pragma unroll
+      for (int n = 0; n < kNb; ++n) {
+        shift[n] = (m[n] == kNegInf ? 0.0f : m[n]) - kLift;
+        float sum = 0.0f;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][b][i], c, -shift[n]));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][b][i + 1], c, -shift[n]));
+            sum += p0 + p1;
+            pw[n][b][i >> 1] = pack2<FP8>(p0, p1);
+          }
+        l[n] += sum;
+      }
+      // O^T += V^T P^T, 16 keys a step
+#pragma unroll
+      for (int t = 0; t < T::kKeys / 16; ++t)
+#pragma unroll
+        for (int b = 0; b < kDb; ++b) {
+          const uint8_t* vp = lv + (va ^ (64 * b)) + 16 * t * D * 2;
+          const s16x4 v0 = read_tr(vp);
+          const s16x4 v1 = read_tr(vp + 8 * D * 2);
+          const s16x8 vf = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+          for (int n = 0; n < kNb; ++n) {
+            const u32x4 pf = {pw[n][t >> 1][4 * (t & 1)], pw[n][t >> 1][4 * (t & 1) + 1],
+                              pw[n][t >> 1][4 * (t & 1) + 2], pw[n][t >> 1][4 * (t & 1) + 3]};
+            if constexpr (FP8)
+              acc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  __builtin_bit_cast(half8_t, vf), __builtin_bit_cast(half8_t, pf), acc[n][b], 0, 0, 0);
+            else
+              acc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  __builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf), acc[n][b], 0, 0, 0);
+          }
+        }
+      constexpr int kProducts = T::kKeys / 16 * kDb;
+      order<0x100, 2 * kReach>();
+#pragma unroll
+      for (int i = 0; i < kProducts - kReach; ++i) {
+        order<0x008, kNb>();
+        order<0x100, 2>();
+      }
+      order<0x008, kNb * kReach>();
     }
-    float top = sc[0][0];
+    if (more) {
+      xk.store(nk, wave);
+      xv.store(nv, wave);
+    }
+    tile_barrier();
+  };
+
+  if (begin < end) {
+    look_up(begin);
+    fetch(lds_k0, lds_v0, begin);
+    look_up(begin + T::kKeys);
+    xk.store(lds_k0, wave);
+    xv.store(lds_v0, wave);
+    tile_barrier();
+    for (int key0 = begin; key0 < end; key0 += 2 * T::kKeys) {
+      step(lds_k0, lds_v0, lds_k1, lds_v1, key0);
+      if (key0 + T::kKeys < end) step(lds_k1, lds_v1, lds_k0, lds_v0, key0 + T::kKeys);
+    }
+  }
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[b][i]);
-    top = half_max(top) * c;
-    if (__any(top > m + kSlack)) {
-      const float m2 = fmaxf(m, top);
-      const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
-      m = m2;
-      l *= f;
+  for (int n = 0; n < kNb; ++n) {
+    const float sum = half_sum(l[n]);
+    if (!real[n]) continue;
+    const int64_t out_row = static_cast<int64_t>(s.token0) + token[n];
+    if (splits == 1) {
+      const float inv = sum > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / sum : 0.0f;
+      uint8_t* op = a.out + out_row * a.out_token + head[n] * a.out_head;
 #pragma unroll
       for (int b = 0; b < kDb; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[b][i] *= f;
+        for (int i = 0; i < 4; ++i) {
+          const f32x16& o = acc[n][b];
+          const u32x2 w = {pack2<false>(o[4 * i] * inv, o[4 * i + 1] * inv),
+                           pack2<false>(o[4 * i + 2] * inv, o[4 * i + 3] * inv)};
+          *reinterpret_cast<u32x2*>(op + (32 * b + 8 * i + 4 * half) * 2) = w;
+        }
+    } else {
+      const int64_t at = tile_slot(a, split, out_row, head[n]);
+      float* pp = a.part + at * D;
+#pragma unroll
+      for (int b = 0; b < kDb; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x16& o = acc[n][b];
+          *reinterpret_cast<f32x4*>(pp + 32 * b + 8 * i + 4 * half) =
+              f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+        }
+      if (half == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m[n], sum};
     }
-    const float shift = (m == kNegInf ? 0.0f : m) - kLift;
-    unsigned pw[kBlocks][8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], c, -shift));
-        const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i + 1], c, -shift));
-        sum += p0 + p1;
-        pw[b][i >> 1] = pack2<FP8>(p0, p1);
-      }
-    l += sum;
-    // O^T += V^T P^T, 16 keys a step
-#pragma unroll
-    for (int t = 0; t < T::kKeys / 16; ++t) {
-      const u32x4 pf = {pw[t >> 1][4 * (t & 1)], pw[t >> 1][4 * (t & 1) + 1],
-                        pw[t >> 1][4 * (t & 1) + 2], pw[t >> 1][4 * (t & 1) + 3]};
-      const int vr = 16 * t + 4 * half + ((lane & 15) >> 2);
-#pragma unroll
-      for (int b = 0; b < kDb; ++b) {
-        const int vc = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        const s16x4 v0 = read_tr(lv + T::v_at(vr, vc) + 8 * (lane & 1));
-        const s16x4 v1 = read_tr(lv + T::v_at(vr + 8, vc) + 8 * (lane & 1));
-        const s16x8 vf = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-        if constexpr (FP8)
-          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, vf),
-                                                          __builtin_bit_cast(half8_t, pf), acc[b], 0, 0, 0);
-        else
-          acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf),
-                                                           __builtin_bit_cast(bf16x8, pf), acc[b], 0, 0, 0);
-      }
-    }
-  }
-  l = half_sum(l);
-  if (!real) return;
-  const int64_t out_row = static_cast<int64_t>(s.token0) + token;
-  if (splits == 1) {
-    const float inv = l > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / l : 0.0f;
-    uint8_t* op = a.out + out_row * a.out_token + head * a.out_head;
-#pragma unroll
-    for (int b = 0; b < kDb; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const u32x2 w = {pack2<false>(acc[b][4 * i] * inv, acc[b][4 * i + 1] * inv),
-                         pack2<false>(acc[b][4 * i + 2] * inv, acc[b][4 * i + 3] * inv)};
-        *reinterpret_cast<u32x2*>(op + (32 * b + 8 * i + 4 * half) * 2) = w;
-      }
-  } else {
-    const int64_t at = tile_slot(a, split, out_row, head);
-    float* pp = a.part + at * D;
-#pragma unroll
-    for (int b = 0; b < kDb; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(pp + 32 * b + 8 * i + 4 * half) =
-            f32x4{acc[b][4 * i], acc[b][4 * i + 1], acc[b][4 * i + 2], acc[b][4 * i + 3]};
-    if (half == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m, l};
   }
 }
 
@@ -518,38 +664,16 @@ struct Stream {
   static constexpr int kK = kChunks / 4;                    // loads of 16 keys
   static constexpr int kV = kKeys * kChunks / 64;           // loads of the tile
   u32x4 k[2][kK], v[kV];
-  const uint8_t* kb[2];
-  const uint8_t* vb[2];
-  int kt, vt, first[2], end[2];
+  Place at[2];
+  int kt, vt;
 
-  // Bases of the two groups of 16 keys at key0, as for Stage: rows outside
-  // [lo, hi) read the nearest one inside.
+  // The two groups of 16 keys at key0.
   __device__ __forceinline__ void locate(const Args& a, const Span& s, int64_t head_k,
                                          int64_t head_v, int key0, const int* ids) {
-    const int last = (s.hi - 1) & ~15;
     kt = static_cast<int>(a.k_token);
     vt = static_cast<int>(a.v_token);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      int g = key0 + 16 * p;
-      g = g < last ? g : last;
-      first[p] = s.lo - g;
-      end[p] = s.hi - 1 - g;
-      if (a.table) {
-        const int off = g - static_cast<int>(a.page.div(static_cast<unsigned>(g)) * a.page.d);
-        const bool in = ids[p] >= 0 && ids[p] < a.n_pages;
-        const int64_t page = in ? ids[p] * a.page_stride : 0;
-        kb[p] = a.k + page + head_k + off * a.k_token;
-        vb[p] = a.v + page + head_v + off * a.v_token;
-        if (!in) {
-          kb[p] = vb[p] = reinterpret_cast<const uint8_t*>(kZeros);
-          first[p] = end[p] = 0;           // every row at the one of zeros
-        }
-      } else {
-        kb[p] = a.k + (static_cast<int64_t>(s.token0) + g) * a.k_token + head_k;
-        vb[p] = a.v + (static_cast<int64_t>(s.token0) + g) * a.v_token + head_v;
-      }
-    }
+    for (int p = 0; p < 2; ++p) at[p] = place_of<16>(a, s, head_k, head_v, key0 + 16 * p, ids[p]);
   }
   __device__ __forceinline__ static int inside(int r, int first, int end) {
     r = r < first ? first : r;
@@ -559,9 +683,9 @@ struct Stream {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const int row = inside(lane & 15, first[p], end[p]) * kt + (lane >> 4) * 16;
+      const int row = inside(lane & 15, at[p].first, at[p].end) * kt + (lane >> 4) * 16;
 #pragma unroll
-      for (int i = 0; i < kK; ++i) k[p][i] = load16b(kb[p], row + i * 64);
+      for (int i = 0; i < kK; ++i) k[p][i] = load16b(at[p].k, row + i * 64);
     }
   }
   __device__ __forceinline__ void load_v() {
@@ -570,7 +694,7 @@ struct Stream {
     for (int i = 0; i < kV; ++i) {
       const int p = i * 64 / kChunks / 16;                  // a load lies in one group
       const int r = (i * 64 + lane) / kChunks - 16 * p, c = (i * 64 + lane) % kChunks;
-      v[i] = load16b(vb[p], inside(r, first[p], end[p]) * vt + c * 16);
+      v[i] = load16b(at[p].v, inside(r, at[p].first, at[p].end) * vt + c * 16);
     }
   }
   // The 8 rows that 32 lanes of a transposing read touch differ by 32 bytes.
@@ -661,17 +785,13 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
 
   const int32_t* table = a.table ? a.table + r * a.ld_table : nullptr;
   const int64_t head_k = kvh * a.k_head, head_v = kvh * a.v_head;
-  const int last_group = (s.hi - 1) & ~15;
   uint8_t* lv = lds + wave * kWave;
   S st;
   int ids[2] = {0, 0};                 // pages of the next tile's two groups
   auto look_up = [&](int key0) {
     if (!table) return;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int g = key0 + 16 * p < last_group ? key0 + 16 * p : last_group;
-      ids[p] = table[a.page.div(static_cast<unsigned>(g))];
-    }
+    for (int p = 0; p < 2; ++p) ids[p] = page_of(a, table, group_at<16>(s, key0 + 16 * p));
   };
   int key0 = begin + wave * S::kKeys;
   constexpr int kStride = 4 * S::kKeys;
@@ -806,7 +926,7 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   const int in_request = (t - token0) * group + head - kvh * group;
   const bool few = a.few_splits > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
   const Span s = few ? span_of(a, r, 0, kFewRows)
-                     : span_of(a, r, in_request / kTileRows * kTileRows, kTileRows);
+                     : span_of(a, r, in_request & -a.tile_rows, a.tile_rows);
   const int splits = few ? splits_of(s, a.few_chunk, a.few_splits) : splits_of(s, a.chunk, a.splits);
   if (splits == 1) return;
   const int64_t at = few ? few_slot(a, 0, r, kvh, in_request) : tile_slot(a, 0, t, head);
@@ -871,8 +991,9 @@ Plan plan_of(const AttnCall& c) {
   const bool few = c.table && group <= kFewRows;
   const bool many = !c.table || c.max_new * group > kFewRows;
   if (many) {
-    p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
-    cut(span_keys(c, kTileRows / group + 2), p.tiles * c.n_kv_heads, 2 * kCus, 128, 256, &p.splits,
+    const int64_t rows = tile_rows(static_cast<int>(c.d));
+    p.tiles = c.n_tokens * group / rows + c.n_requests;
+    cut(span_keys(c, rows / group + 2), p.tiles * c.n_kv_heads, kCus, 128, 256, &p.splits,
         &p.chunk);
   }
   if (few)
@@ -948,6 +1069,7 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.causal = c.causal;
   a.window = static_cast<int>(c.window);
   a.tiles = static_cast<int>(p.tiles);
+  a.tile_rows = tile_rows(static_cast<int>(c.d));
   a.splits = static_cast<int>(p.splits);
   a.chunk = static_cast<int>(p.chunk);
   a.few_splits = static_cast<int>(p.few_splits);
