@@ -36,6 +36,7 @@
 // output's own.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
 #include <stdint.h>
 
 #include "internal.h"
@@ -56,9 +57,7 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-// Rows of a workgroup's tile: 4 waves of one or two 32-column blocks.
-constexpr int tile_blocks(int d) { return 1; }
-constexpr int tile_rows(int d) { return 128 * tile_blocks(d); }
+constexpr int kTileRows = 128;         // rows of a workgroup, 32 a wave
 constexpr int kFewRows = 16;           // rows of a request that few_rows_kernel takes
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNegInf = -__builtin_inff();
@@ -84,7 +83,8 @@ struct Args {
   int n_requests, n_tokens, n_heads, n_kv_heads, n_pages;
   FastDiv group, page;
   int64_t cols_len;                               // columns * page size
-  int max_kv, causal, window, tiles, tile_rows;
+  int max_kv, causal, window, tiles;
+  int tile_blocks;                                // workgroups of the tiles
   // chunks of keys: of tiles of many rows, of requests of few
   int splits, chunk, few_splits, few_chunk;
 };
@@ -93,11 +93,11 @@ __device__ __forceinline__ int clampi(int64_t x, int64_t lo, int64_t hi) {
   return static_cast<int>(x < lo ? lo : x > hi ? hi : x);
 }
 
-// First tile of request i: floor(rows before / tile_rows) + i leaves every
+// First tile of request i: floor(rows before / kTileRows) + i leaves every
 // request at least the tiles it fills, without a prefix sum of its own.
 __device__ __forceinline__ int64_t first_tile(const Args& a, int i) {
   const int64_t rows = static_cast<int64_t>(clampi(a.cu[i], 0, a.n_tokens)) * a.group.d;
-  return (rows >> (a.tile_rows == 256 ? 8 : 7)) + i;
+  return rows / kTileRows + i;
 }
 
 // The request of tile t: the last i with first_tile(i) <= t (or, BY_TOKEN,
@@ -358,6 +358,34 @@ __device__ __forceinline__ void order() {
   __builtin_amdgcn_sched_group_barrier(KIND, N, 0);
 }
 
+// The weights are 2^(c s - m + kLift) with a bound m that may be up to kSlack
+// below the largest score: it is moved, and the sums with it, only when a
+// score passes it by more.  fp16 weights (next to E4M3 values) are lifted
+// away from fp16's subnormals; 2^14 is still in its range.
+constexpr float kSlack = 8.0f;
+template <bool FP8>
+__device__ __forceinline__ float shift_of(float m) {
+  return (m == kNegInf ? 0.0f : m) - (FP8 ? 6.0f : 0.0f);
+}
+// Raises m to top; returns the factor of the sums so far.
+__device__ __forceinline__ float moved(float* m, float top) {
+  const float m2 = fmaxf(*m, top);
+  const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(*m - m2);
+  *m = m2;
+  return f;
+}
+// c.  A K scale of zero makes every score 0; it must not make -inf * 0 of a
+// masked one.
+template <bool FP8>
+__device__ __forceinline__ float score_factor(const Args& a) {
+  return FP8 ? fmaxf(a.scale_log2 * *a.k_scale, 0x1p-120f) : a.scale_log2;
+}
+// Factor of a row's sums for its output; a row that saw no key gives zeros.
+template <bool FP8>
+__device__ __forceinline__ float output_factor(const Args& a, float l) {
+  return l > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / l : 0.0f;
+}
+
 template <bool HALF>
 __device__ __forceinline__ unsigned pack2(float x, float y) {
   const f32x2 p = {x, y};
@@ -367,64 +395,56 @@ __device__ __forceinline__ unsigned pack2(float x, float y) {
 
 // ---------------------------------------------------------------- kernel
 
-// One tile of 128 rows; 4 waves, 32 rows each.
+// LDS of a workgroup: two tiles of K and V, in arrays of their own so that
+// reads of one need not wait for loads into another.
+template <int D>
+struct Lds {
+  uint8_t* k0;
+  uint8_t* k1;
+  uint8_t* v0;
+  uint8_t* v1;
+};
+
+// Workgroup `block` of the tiles: 128 rows, 4 waves of 32.  Two waves a SIMD
+// at every D, so that one's exponentials run under another's products; D =
+// 256 (128 registers of sums, 64 of queries) affords that with tiles of 32
+// keys.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a) {
+__device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>& lds) {
   using T = Tile<D, FP8>;
-  constexpr int kNb = tile_blocks(D);
-  constexpr int kRows = tile_rows(D);
   constexpr int kSteps = D / 16;          // of the first product
   constexpr int kBlocks = T::kKeys / 32;  // key blocks of a tile
   constexpr int kDb = D / 32;             // d blocks of the output
-  // weights are at most 2^kSlack: the bound is moved only when a score
-  // passes it by more (fp16 weights are kept 2^6 higher, away from its
-  // subnormals; 2^14 is still in range)
-  constexpr float kSlack = 8.0f;
-  constexpr float kLift = FP8 ? 6.0f : 0.0f;
-  constexpr int kReach = 4;
-  // arrays of their own, so that reads of one need not wait for loads into
-  // the other
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_k0[T::kBytes], lds_k1[T::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_v0[T::kBytes], lds_v1[T::kBytes];
+  // LDS reads are issued this many products ahead
+  constexpr int kReach = D > 128 ? 2 : 4;
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int kvh = blockIdx.x % a.n_kv_heads;
-  const int rest = blockIdx.x / a.n_kv_heads;
+  const int kvh = block % a.n_kv_heads;
+  const int rest = block / a.n_kv_heads;
   const int split = rest % a.splits;
   const int tile = a.tiles - 1 - rest / a.splits;    // the longest rows of a prompt first
 
   const int r = __builtin_amdgcn_readfirstlane(find_request<false>(a, tile));
-  const int64_t row0 = (tile - first_tile(a, r)) * kRows;
+  const int64_t row0 = (tile - first_tile(a, r)) * kTileRows;
   const int group = static_cast<int>(a.group.d);
   const int64_t n_rows = static_cast<int64_t>(clampi(a.cu[r + 1], 0, a.n_tokens) -
                                               clampi(a.cu[r], 0, a.n_tokens)) * group;
   if (row0 < 0 || row0 >= n_rows || (a.few_splits > 0 && n_rows <= kFewRows)) return;
-  const Span s = span_of(a, r, static_cast<int>(row0), kRows);
+  const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
   const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
   const int begin = s.start + split * a.chunk;
   const int end = split == splits - 1 ? s.hi : begin + a.chunk;
 
-  // this lane's rows, and what all and any rows of the wave see
-  bool real[kNb];
-  int token[kNb], head[kNb], see_lo[kNb], see_hi[kNb];
-  int all_lo = 0, all_hi = 0x7FFFFFFF, any_lo = 0x7FFFFFFF, any_hi = 0;
-#pragma unroll
-  for (int n = 0; n < kNb; ++n) {
-    const int row = s.row0 + (wave * kNb + n) * 32 + col;
-    real[n] = row < n_rows;
-    token[n] = static_cast<int>(a.group.div(real[n] ? row : 0));
-    head[n] = kvh * group + (real[n] ? row - token[n] * group : 0);
-    see_lo[n] = see_hi[n] = 0;
-    if (real[n]) {
-      sees(a, s, token[n], &see_lo[n], &see_hi[n]);
-      any_lo = min(any_lo, see_lo[n]);
-    }
-    all_lo = max(all_lo, see_lo[n]);
-    all_hi = min(all_hi, see_hi[n]);
-    any_hi = max(any_hi, see_hi[n]);
-  }
+  // this lane's row, and what all and any rows of the wave see
+  const int row = s.row0 + wave * 32 + col;
+  const bool real = row < n_rows;
+  const int token = static_cast<int>(a.group.div(real ? row : 0));
+  const int head = kvh * group + (real ? row - token * group : 0);
+  int see_lo = 0, see_hi = 0;
+  if (real) sees(a, s, token, &see_lo, &see_hi);
+  int all_lo = see_lo, all_hi = see_hi, any_lo = real ? see_lo : 0x7FFFFFFF, any_hi = see_hi;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     all_lo = max(all_lo, __shfl_xor(all_lo, off));
@@ -437,27 +457,19 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   any_lo = __builtin_amdgcn_readfirstlane(any_lo);
   any_hi = __builtin_amdgcn_readfirstlane(any_hi);
 
-  bf16x8 qf[kNb][kSteps];
-#pragma unroll
-  for (int n = 0; n < kNb; ++n) {
-    const uint8_t* qp = a.q + (static_cast<int64_t>(s.token0) + token[n]) * a.q_token + head[n] * a.q_head;
+  bf16x8 qf[kSteps];
+  {
+    const uint8_t* qp = a.q + (static_cast<int64_t>(s.token0) + token) * a.q_token + head * a.q_head;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      qf[n][i] = *reinterpret_cast<const bf16x8*>(qp + i * 32 + half * 16);
+      qf[i] = *reinterpret_cast<const bf16x8*>(qp + i * 32 + half * 16);
   }
-  // a scale of zero makes every score 0; it must not make -inf * 0 of a
-  // masked one
-  const float c = FP8 ? fmaxf(a.scale_log2 * *a.k_scale, 0x1p-120f) : a.scale_log2;
+  const float c = score_factor<FP8>(a);
 
-  f32x16 acc[kNb][kDb];
-  float m[kNb], l[kNb];
+  f32x16 acc[kDb];
 #pragma unroll
-  for (int n = 0; n < kNb; ++n) {
-    m[n] = kNegInf;
-    l[n] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < kDb; ++b) acc[n][b] = f32x16{};
-  }
+  for (int b = 0; b < kDb; ++b) acc[b] = f32x16{};
+  float m = kNegInf, l = 0.0f;
 
   const int32_t* table = a.table ? a.table + r * a.ld_table : nullptr;
   const int64_t head_k = kvh * a.k_head, head_v = kvh * a.v_head;
@@ -467,128 +479,118 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
   const int ka = T::k_at(col, half);
   const int va = T::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) +
                  8 * (lane & 1);
-
   Stage<D, FP8, false> xk;
   Stage<D, FP8, true> xv;
   int id = 0;                             // page of this wave's rows of the next tile
   auto look_up = [&](int key0) {
     if (table) id = page_of(a, table, group_at<T::kRows>(s, key0 + wave * T::kRows));
   };
-  auto fetch = [&](uint8_t* nk, uint8_t* nv, int key0) {
-    const Place p = place_of<T::kRows>(a, s, head_k, head_v, key0 + wave * T::kRows, id);
-    xk.load(p, static_cast<int>(a.k_token), wave, nk);
-    xv.load(p, static_cast<int>(a.v_token), wave, nv);
+  auto place = [&](int key0) {
+    return place_of<T::kRows>(a, s, head_k, head_v, key0 + wave * T::kRows, id);
   };
+  // E4M3 at D = 256 has registers for one of K and V in flight: V follows K
+  constexpr bool kOneByOne = FP8 && D > 128;
+
   // One tile, its keys in (lk, lv); the next one's go to (nk, nv).
   auto step = [&](const uint8_t* lk, const uint8_t* lv, uint8_t* nk, uint8_t* nv, int key0) {
     const bool more = key0 + T::kKeys < end;
-    if (more) fetch(nk, nv, key0 + T::kKeys);
     const bool seen = key0 < any_hi && key0 + T::kKeys > any_lo;      // by some row of the wave
-    if (!seen) look_up(key0 + 2 * T::kKeys);
+    Place p = {};
+    if (more) {
+      p = place(key0 + T::kKeys);
+      xk.load(p, static_cast<int>(a.k_token), wave, nk);
+      if constexpr (!kOneByOne) xv.load(p, static_cast<int>(a.v_token), wave, nv);
+    }
+    f32x16 sc[kBlocks];
     if (seen) {
-      f32x16 sc[kNb][kBlocks];
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           const bf16x8 kf = *reinterpret_cast<const bf16x8*>(lk + (ka ^ (32 * i)) + 32 * b * D * 2);
-#pragma unroll
-          for (int n = 0; n < kNb; ++n)
-            sc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[n][i], i ? sc[n][b] : f32x16{}, 0, 0, 0);
+          sc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[i], i ? sc[b] : f32x16{}, 0, 0, 0);
         }
-      // reads kReach products ahead: an LDS read takes several products' time
       order<0x100, kReach>();
 #pragma unroll
       for (int i = 0; i < kBlocks * kSteps - kReach; ++i) {
-        order<0x008, kNb>();
+        order<0x008, 1>();
         order<0x100, 1>();
       }
-      order<0x008, kNb * kReach>();
-      // a scalar load in flight makes LDS waits full ones: here no reads are
-      look_up(key0 + 2 * T::kKeys);
+      order<0x008, kReach>();
+    }
+    if constexpr (kOneByOne) {
+      if (more) {
+        xk.store(nk, wave);
+        xv.load(p, static_cast<int>(a.v_token), wave, nv);
+      }
+    }
+    // a scalar load in flight makes LDS waits full ones: here no reads are
+    look_up(key0 + 2 * T::kKeys);
+    if (seen) {
       if (key0 < all_lo || key0 + T::kKeys > all_hi) {
 #pragma unroll
-        for (int n = 0; n < kNb; ++n)
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              // see_lo <= j < see_hi in one comparison
-              const unsigned j = key0 + 4 * half - see_lo[n] + (32 * b + 8 * (i >> 2) + (i & 3));
-              if (j >= static_cast<unsigned>(see_hi[n] - see_lo[n])) sc[n][b][i] = kNegInf;
-            }
-      }
-      float top[kNb], shift[kNb];
-      bool move = false;
-#pragma unroll
-      for (int n = 0; n < kNb; ++n) {
-        float t = sc[n][0][0];
-#pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) t = fmaxf(t, sc[n][b][i]);
-        top[n] = half_max(t) * c;
-        move |= top[n] > m[n] + kSlack;
-      }
-      if (__any(move)) {
-#pragma unroll
-        for (int n = 0; n < kNb; ++n) {
-          const float m2 = fmaxf(m[n], top[n]);
-          const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - m2);
-          m[n] = m2;
-          l[n] *= f;
-#pragma unroll
-          for (int b = 0; b < kDb; ++b) acc[n][b] *= f;
-        }
-      }
-      unsigned pw[kNb][kBlocks][8];
-#pragma unroll
-      for (int n = 0; n < kNb; ++n) {
-        shift[n] = (m[n] == kNegInf ? 0.0f : m[n]) - kLift;
-        float sum = 0.0f;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][b][i], c, -shift[n]));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][b][i + 1], c, -shift[n]));
-            sum += p0 + p1;
-            pw[n][b][i >> 1] = pack2<FP8>(p0, p1);
+          for (int i = 0; i < 16; ++i) {
+            // see_lo <= j < see_hi in one comparison
+            const unsigned j = key0 + 4 * half - see_lo + (32 * b + 8 * (i >> 2) + (i & 3));
+            if (j >= static_cast<unsigned>(see_hi - see_lo)) sc[b][i] = kNegInf;
           }
-        l[n] += sum;
       }
+      float top = sc[0][0];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[b][i]);
+      top = half_max(top) * c;
+      if (__any(top > m + kSlack)) {
+        const float f = moved(&m, top);
+        l *= f;
+#pragma unroll
+        for (int b = 0; b < kDb; ++b) acc[b] *= f;
+      }
+      const float shift = shift_of<FP8>(m);
+      unsigned pw[kBlocks][8];
+      float sum = 0.0f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], c, -shift));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i + 1], c, -shift));
+          sum += p0 + p1;
+          pw[b][i >> 1] = pack2<FP8>(p0, p1);
+        }
+      l += sum;
       // O^T += V^T P^T, 16 keys a step
 #pragma unroll
-      for (int t = 0; t < T::kKeys / 16; ++t)
+      for (int t = 0; t < T::kKeys / 16; ++t) {
+        const u32x4 pf = {pw[t >> 1][4 * (t & 1)], pw[t >> 1][4 * (t & 1) + 1],
+                          pw[t >> 1][4 * (t & 1) + 2], pw[t >> 1][4 * (t & 1) + 3]};
 #pragma unroll
         for (int b = 0; b < kDb; ++b) {
           const uint8_t* vp = lv + (va ^ (64 * b)) + 16 * t * D * 2;
-          const s16x4 v0 = read_tr(vp);
-          const s16x4 v1 = read_tr(vp + 8 * D * 2);
-          const s16x8 vf = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-          for (int n = 0; n < kNb; ++n) {
-            const u32x4 pf = {pw[n][t >> 1][4 * (t & 1)], pw[n][t >> 1][4 * (t & 1) + 1],
-                              pw[n][t >> 1][4 * (t & 1) + 2], pw[n][t >> 1][4 * (t & 1) + 3]};
-            if constexpr (FP8)
-              acc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  __builtin_bit_cast(half8_t, vf), __builtin_bit_cast(half8_t, pf), acc[n][b], 0, 0, 0);
-            else
-              acc[n][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  __builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf), acc[n][b], 0, 0, 0);
-          }
+          const s16x4 w0 = read_tr(vp);
+          const s16x4 w1 = read_tr(vp + 8 * D * 2);
+          const s16x8 vf = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
+          if constexpr (FP8)
+            acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(half8_t, vf), __builtin_bit_cast(half8_t, pf), acc[b], 0, 0, 0);
+          else
+            acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                __builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf), acc[b], 0, 0, 0);
         }
-      constexpr int kProducts = T::kKeys / 16 * kDb;
+      }
       order<0x100, 2 * kReach>();
 #pragma unroll
-      for (int i = 0; i < kProducts - kReach; ++i) {
-        order<0x008, kNb>();
+      for (int i = 0; i < T::kKeys / 16 * kDb - kReach; ++i) {
+        order<0x008, 1>();
         order<0x100, 2>();
       }
-      order<0x008, kNb * kReach>();
+      order<0x008, kReach>();
     }
     if (more) {
-      xk.store(nk, wave);
+      if constexpr (!kOneByOne) xk.store(nk, wave);
       xv.store(nv, wave);
     }
     tile_barrier();
@@ -596,46 +598,42 @@ __global__ void __launch_bounds__(256, D > 128 ? 1 : 2) attn_tile_kernel(Args a)
 
   if (begin < end) {
     look_up(begin);
-    fetch(lds_k0, lds_v0, begin);
+    const Place p = place(begin);
+    xk.load(p, static_cast<int>(a.k_token), wave, lds.k0);
+    xv.load(p, static_cast<int>(a.v_token), wave, lds.v0);
     look_up(begin + T::kKeys);
-    xk.store(lds_k0, wave);
-    xv.store(lds_v0, wave);
+    xk.store(lds.k0, wave);
+    xv.store(lds.v0, wave);
     tile_barrier();
     for (int key0 = begin; key0 < end; key0 += 2 * T::kKeys) {
-      step(lds_k0, lds_v0, lds_k1, lds_v1, key0);
-      if (key0 + T::kKeys < end) step(lds_k1, lds_v1, lds_k0, lds_v0, key0 + T::kKeys);
+      step(lds.k0, lds.v0, lds.k1, lds.v1, key0);
+      if (key0 + T::kKeys < end) step(lds.k1, lds.v1, lds.k0, lds.v0, key0 + T::kKeys);
     }
   }
+  l = half_sum(l);
+  if (!real) return;
+  const int64_t out_row = static_cast<int64_t>(s.token0) + token;
+  if (splits == 1) {
+    const float inv = output_factor<FP8>(a, l);
+    uint8_t* op = a.out + out_row * a.out_token + head * a.out_head;
 #pragma unroll
-  for (int n = 0; n < kNb; ++n) {
-    const float sum = half_sum(l[n]);
-    if (!real[n]) continue;
-    const int64_t out_row = static_cast<int64_t>(s.token0) + token[n];
-    if (splits == 1) {
-      const float inv = sum > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / sum : 0.0f;
-      uint8_t* op = a.out + out_row * a.out_token + head[n] * a.out_head;
+    for (int b = 0; b < kDb; ++b)
 #pragma unroll
-      for (int b = 0; b < kDb; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const u32x2 w = {pack2<false>(acc[b][4 * i] * inv, acc[b][4 * i + 1] * inv),
+                         pack2<false>(acc[b][4 * i + 2] * inv, acc[b][4 * i + 3] * inv)};
+        *reinterpret_cast<u32x2*>(op + (32 * b + 8 * i + 4 * half) * 2) = w;
+      }
+  } else {
+    const int64_t at = tile_slot(a, split, out_row, head);
+    float* pp = a.part + at * D;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x16& o = acc[n][b];
-          const u32x2 w = {pack2<false>(o[4 * i] * inv, o[4 * i + 1] * inv),
-                           pack2<false>(o[4 * i + 2] * inv, o[4 * i + 3] * inv)};
-          *reinterpret_cast<u32x2*>(op + (32 * b + 8 * i + 4 * half) * 2) = w;
-        }
-    } else {
-      const int64_t at = tile_slot(a, split, out_row, head[n]);
-      float* pp = a.part + at * D;
+    for (int b = 0; b < kDb; ++b)
 #pragma unroll
-      for (int b = 0; b < kDb; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x16& o = acc[n][b];
-          *reinterpret_cast<f32x4*>(pp + 32 * b + 8 * i + 4 * half) =
-              f32x4{o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
-        }
-      if (half == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m[n], sum};
-    }
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(pp + 32 * b + 8 * i + 4 * half) =
+            f32x4{acc[b][4 * i], acc[b][4 * i + 1], acc[b][4 * i + 2], acc[b][4 * i + 3]};
+    if (half == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{m, l};
   }
 }
 
@@ -735,21 +733,18 @@ struct Stream {
 // through an LDS area of the wave's own); the four waves are joined at the
 // end.  Bound by the read of the keys and values.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(Args a) {
+__device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>& lds,
+                                         float (*lds_m)[16], float (*lds_l)[16]) {
   using S = Stream<D, FP8>;
   constexpr int kSteps = D / 32;
   constexpr int kDb = D / 16;
-  constexpr int kWave = S::kKeys * D * 2;      // LDS bytes of a wave: V, later its sums
-  constexpr float kSlack = 8.0f;
-  constexpr float kLift = FP8 ? 6.0f : 0.0f;
-  static_assert(kWave == 16 * D * 4, "the sums take the place of V");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kWave];
-  __shared__ float lds_m[4][16], lds_l[4][16];
+  // a wave's V, and later its 16 rows of sums, in an array of its own
+  static_assert(S::kKeys * D * 2 == 16 * D * 4 && 16 * D * 4 <= Tile<D, FP8>::kBytes);
 
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int kvh = blockIdx.x % a.n_kv_heads;
-  const int rest = blockIdx.x / a.n_kv_heads;
+  const int kvh = block % a.n_kv_heads;
+  const int rest = block / a.n_kv_heads;
   const int split = rest % a.few_splits, r = rest / a.few_splits;
   const int group = static_cast<int>(a.group.d);
   const Span s = span_of(a, r, 0, kFewRows);
@@ -776,7 +771,7 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
       qf[i] = *reinterpret_cast<const bf16x8*>(qp + at);
     }
   }
-  const float c = FP8 ? fmaxf(a.scale_log2 * *a.k_scale, 0x1p-120f) : a.scale_log2;
+  const float c = score_factor<FP8>(a);
 
   f32x4 acc[kDb];
 #pragma unroll
@@ -785,7 +780,7 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
 
   const int32_t* table = a.table ? a.table + r * a.ld_table : nullptr;
   const int64_t head_k = kvh * a.k_head, head_v = kvh * a.v_head;
-  uint8_t* lv = lds + wave * kWave;
+  uint8_t* lv = wave == 0 ? lds.k0 : wave == 1 ? lds.k1 : wave == 2 ? lds.v0 : lds.v1;
   S st;
   int ids[2] = {0, 0};                 // pages of the next tile's two groups
   auto look_up = [&](int key0) {
@@ -830,14 +825,12 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
                       fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
     top = quad_max(top) * c;
     if (__any(top > m + kSlack)) {
-      const float m2 = fmaxf(m, top);
-      const float f = m2 == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m2);
-      m = m2;
+      const float f = moved(&m, top);
       l *= f;
 #pragma unroll
       for (int b = 0; b < kDb; ++b) acc[b] *= f;
     }
-    const float shift = (m == kNegInf ? 0.0f : m) - kLift;
+    const float shift = shift_of<FP8>(m);
     u32x4 pf;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
@@ -887,7 +880,7 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
   const int out_token = static_cast<int>(a.group.div(row));
   const int out_head = kvh * group + row - out_token * group;
   const int64_t at = few_slot(a, split, r, kvh, row);
-  const float inv = ll > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / ll : 0.0f;
+  const float inv = output_factor<FP8>(a, ll);
   uint8_t* op = a.out + (static_cast<int64_t>(s.token0) + out_token) * a.out_token + out_head * a.out_head;
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
@@ -895,7 +888,8 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const f32x4 p = *reinterpret_cast<const f32x4*>(lds + i * kWave + row * (D * 4) + ((ch ^ row) << 4));
+      const uint8_t* part = i == 0 ? lds.k0 : i == 1 ? lds.k1 : i == 2 ? lds.v0 : lds.v1;
+      const f32x4 p = *reinterpret_cast<const f32x4*>(part + row * (D * 4) + ((ch ^ row) << 4));
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] = __builtin_fmaf(p[x], w[i], o[x]);
     }
@@ -909,15 +903,43 @@ __global__ void __launch_bounds__(256, D > 128 && !FP8 ? 1 : 2) few_rows_kernel(
   if (splits > 1 && piece == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{mm, ll};
 }
 
-// Joins the chunks of each row: one wave a row.
-template <int D, bool FP8>
+// Tiles of rows, requests of few rows, or both in one launch (the first
+// workgroups are the tiles'), so that a step of chunks and decodes has the
+// matrix work and the reads of the decodes side by side.
+template <int D, bool FP8, bool TILES, bool FEW>
+__global__ void __launch_bounds__(256, !TILES && D > 128 && !FP8 ? 1 : 2) attention_kernel(Args a) {
+  constexpr int kBytes = TILES ? Tile<D, FP8>::kBytes : 16 * D * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_k0[kBytes], lds_k1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_v0[kBytes], lds_v1[kBytes];
+  const Lds<D> lds = {lds_k0, lds_k1, lds_v0, lds_v1};
+  const int block = static_cast<int>(blockIdx.x);
+  if constexpr (TILES) {
+    if (!FEW || block < a.tile_blocks) {
+      tile_rows<D, FP8>(a, block, lds);
+      return;
+    }
+  }
+  if constexpr (FEW) {
+    __shared__ float lds_m[4][16], lds_l[4][16];
+    few_rows<D, FP8>(a, TILES ? block - a.tile_blocks : block, lds, lds_m, lds_l);
+  }
+}
+
+// Joins the chunks of each row, in chunk order within each of WAVES waves
+// (one, or four for rows of many chunks: the reads of the chunks' sums are
+// what takes time) and then over the waves.
+template <int D, bool FP8, int WAVES>
 __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   constexpr int kEach = D / 64;
+  __shared__ float lds_o[WAVES > 1 ? WAVES * D : 1];
   const int lane = threadIdx.x & 63;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+  const int mine = WAVES > 1 ? wave : 0;            // of the row's waves
+  const int64_t row = WAVES > 1 ? static_cast<int64_t>(blockIdx.x)
+                                : static_cast<int64_t>(blockIdx.x) * 4 + wave;
   if (row >= static_cast<int64_t>(a.n_tokens) * a.n_heads) return;
   const int t = static_cast<int>(row / a.n_heads), head = static_cast<int>(row % a.n_heads);
-  const int r = find_request<true>(a, t);
+  const int r = __builtin_amdgcn_readfirstlane(find_request<true>(a, t));
   const int group = static_cast<int>(a.group.d);
   const int token0 = clampi(a.cu[r], 0, a.n_tokens);
   const int token1 = clampi(a.cu[r + 1], token0, a.n_tokens);
@@ -926,26 +948,53 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   const int in_request = (t - token0) * group + head - kvh * group;
   const bool few = a.few_splits > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
   const Span s = few ? span_of(a, r, 0, kFewRows)
-                     : span_of(a, r, in_request & -a.tile_rows, a.tile_rows);
+                     : span_of(a, r, in_request & -kTileRows, kTileRows);
   const int splits = few ? splits_of(s, a.few_chunk, a.few_splits) : splits_of(s, a.chunk, a.splits);
   if (splits == 1) return;
   const int64_t at = few ? few_slot(a, 0, r, kvh, in_request) : tile_slot(a, 0, t, head);
   const int64_t step = few ? few_slot(a, 1, r, kvh, in_request) - at : tile_slot(a, 1, t, head) - at;
+  // a lane takes the bound and the sum of weights of every 64th chunk
   float m = kNegInf;
-  for (int i = 0; i < splits; ++i) {
+  for (int i = lane; i < splits; i += 64) {
     const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + i * step) * 2);
     if (ml[1] > 0.0f) m = fmaxf(m, ml[0]);
   }
-  float l = 0.0f, o[kEach] = {};
-  for (int i = 0; i < splits; ++i) {
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + i * step) * 2);
-    const float f = ml[1] > 0.0f ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
-    l = __builtin_fmaf(ml[1], f, l);
-    const float* p = a.part + (at + i * step) * D + lane * kEach;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) o[e] = __builtin_fmaf(p[e], f, o[e]);
+  for (int off = 1; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+  float l = 0.0f, o[kEach] = {};
+  for (int i0 = 0; i0 < splits; i0 += 64) {
+    float f = 0.0f;
+    if (i0 + lane < splits) {
+      const f32x2 ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + (i0 + lane) * step) * 2);
+      f = ml[1] > 0.0f ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
+      l = __builtin_fmaf(ml[1], f, l);
+    }
+    const int n = splits - i0 < 64 ? splits - i0 : 64;
+    const float* p = a.part + (at + i0 * step) * D + lane * kEach;
+#pragma unroll 8
+    for (int i = mine; i < n; i += WAVES) {
+      const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+      typedef float vec __attribute__((ext_vector_type(kEach)));
+      const vec x = *reinterpret_cast<const vec*>(p + i * step * D);
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) o[e] = __builtin_fmaf(x[e], fi, o[e]);
+    }
   }
-  const float inv = l > 0.0f ? (FP8 ? *a.v_scale : 1.0f) / l : 0.0f;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) l += __shfl_xor(l, off);
+  if constexpr (WAVES > 1) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) lds_o[wave * D + lane * kEach + e] = o[e];
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      o[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) o[e] += lds_o[w * D + lane * kEach + e];
+    }
+  }
+  const float inv = output_factor<FP8>(a, l);
   __bf16* op = reinterpret_cast<__bf16*>(a.out + t * a.out_token + head * a.out_head) + lane * kEach;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) op[e] = static_cast<__bf16>(o[e] * inv);
@@ -984,6 +1033,38 @@ int64_t span_keys(const AttnCall& c, int64_t tokens) {
   return (c.window && c.causal && keys > seen ? seen : keys) + 15;
 }
 
+// Chunks of the tiles' keys by their estimated time.  Two workgroups fit a
+// CU, so `tiles` of them run in rounds of 512; a last round of less than
+// half takes about 0.62 of one (a workgroup alone on its CU is faster).
+// Cutting the keys evens the rounds out (2048 new tokens of 40 heads over
+// 32001 keys, 1.25 rounds: 1.60 ms uncut, 1.40 ms cut in two) but writes and
+// reads each chunk's sums (7 prompts of up to 2001 tokens: 121 us uncut, 203
+// us cut in two).  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.
+void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
+  const int64_t keys = span_keys(c, kTileRows / group + 2);
+  const double wgs = (static_cast<double>(c.n_tokens) * group / kTileRows + 0.5 * c.n_requests) *
+                     c.n_kv_heads;
+  // rows that see from none to all of the keys even out by themselves (the
+  // longest are first)
+  const bool graded = c.causal && (!c.table || c.max_kv < 2 * c.max_new);
+  const double round_us = 2.0 * kCus * kTileRows * keys * 4.0 * c.d / 1e9;
+  const double sums_us = static_cast<double>(c.n_tokens) * c.n_heads * c.d * 8.0 / 4e6;
+  double best = 0.0;
+  int64_t splits = 1;
+  for (int64_t n = 1; n <= 16 && (n == 1 || keys >= 256 * n); ++n) {
+    const double r = wgs * n / (2.0 * kCus), full = floor(r);
+    const double rounds = graded && r > 1.0 ? r : full + (r - full > 0.5 ? 1.0 : r > full ? 0.62 : 0.0);
+    const double us = round_us * rounds / n + (n > 1 ? 6.0 + n * sums_us : 0.0);
+    if (n == 1 || us < best) {
+      best = us;
+      splits = n;
+    }
+  }
+  p->chunk = (keys + splits * 128 - 1) / (splits * 128) * 128;
+  p->splits = (keys + p->chunk - 1) / p->chunk;
+  if (p->splits < 1) p->splits = 1;
+}
+
 Plan plan_of(const AttnCall& c) {
   Plan p = {};
   const int64_t group = c.n_heads / c.n_kv_heads;
@@ -991,10 +1072,8 @@ Plan plan_of(const AttnCall& c) {
   const bool few = c.table && group <= kFewRows;
   const bool many = !c.table || c.max_new * group > kFewRows;
   if (many) {
-    const int64_t rows = tile_rows(static_cast<int>(c.d));
-    p.tiles = c.n_tokens * group / rows + c.n_requests;
-    cut(span_keys(c, rows / group + 2), p.tiles * c.n_kv_heads, kCus, 128, 256, &p.splits,
-        &p.chunk);
+    p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
+    cut_tiles(c, group, &p);
   }
   if (few)
   {
@@ -1012,15 +1091,20 @@ Plan plan_of(const AttnCall& c) {
 
 template <int D, bool FP8>
 void launch(const Args& a, hipStream_t stream) {
-  if (a.tiles > 0)
-    attn_tile_kernel<D, FP8><<<static_cast<unsigned>(static_cast<int64_t>(a.tiles) * a.splits * a.n_kv_heads),
-                               256, 0, stream>>>(a);
-  if (a.few_splits > 0)
-    few_rows_kernel<D, FP8><<<static_cast<unsigned>(static_cast<int64_t>(a.n_requests) * a.few_splits * a.n_kv_heads),
-                              256, 0, stream>>>(a);
+  const unsigned few = static_cast<unsigned>(static_cast<int64_t>(a.n_requests) * a.few_splits * a.n_kv_heads);
+  if (a.tiles > 0 && a.few_splits > 0)
+    attention_kernel<D, FP8, true, true><<<a.tile_blocks + few, 256, 0, stream>>>(a);
+  else if (a.tiles > 0)
+    attention_kernel<D, FP8, true, false><<<a.tile_blocks, 256, 0, stream>>>(a);
+  else
+    attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
   if (a.splits > 1 || a.few_splits > 1) {
+    // four waves a row for many chunks, as long as the rows are few
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
-    combine_kernel<D, FP8><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
+    if ((a.splits > 8 || a.few_splits > 8) && rows <= 8192)
+      combine_kernel<D, FP8, 4><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a);
+    else
+      combine_kernel<D, FP8, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
   }
 }
 
@@ -1069,8 +1153,8 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.causal = c.causal;
   a.window = static_cast<int>(c.window);
   a.tiles = static_cast<int>(p.tiles);
-  a.tile_rows = tile_rows(static_cast<int>(c.d));
   a.splits = static_cast<int>(p.splits);
+  a.tile_blocks = static_cast<int>(p.tiles * p.splits * c.n_kv_heads);
   a.chunk = static_cast<int>(p.chunk);
   a.few_splits = static_cast<int>(p.few_splits);
   a.few_chunk = static_cast<int>(p.few_chunk);
