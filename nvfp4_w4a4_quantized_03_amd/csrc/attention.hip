@@ -85,8 +85,11 @@ struct Args {
   int64_t cols_len;                               // columns * page size
   int max_kv, causal, window, tiles;
   int tile_blocks;                                // workgroups of the tiles
-  // chunks of keys: of tiles of many rows, of requests of few
-  int splits, chunk, few_splits, few_chunk;
+  int splits, chunk;                              // chunks of the tiles' keys
+  // requests of few rows (few_pieces: 0, none): most pieces that their keys
+  // are cut into; keys of a piece and pieces of a request, or 0 for a cut
+  // that the kernel makes from the lengths; workgroups
+  int few_pieces, few_chunk, few_splits, few_blocks;
 };
 
 __device__ __forceinline__ int clampi(int64_t x, int64_t lo, int64_t hi) {
@@ -162,19 +165,152 @@ __device__ __forceinline__ int splits_of(const Span& s, int chunk, int most) {
 __device__ __forceinline__ int64_t tile_slot(const Args& a, int split, int64_t token, int head) {
   return (static_cast<int64_t>(split) * a.n_tokens + token) * a.n_heads + head;
 }
-__device__ __forceinline__ int64_t few_slot(const Args& a, int split, int r, int kvh, int row) {
+__device__ __forceinline__ int64_t few_slot(const Args& a, int piece, int kvh, int row) {
   const int64_t before = a.splits > 1 ? tile_slot(a, a.splits, 0, 0) : 0;
-  return before + ((static_cast<int64_t>(split) * a.n_requests + r) * a.n_kv_heads + kvh) * kFewRows + row;
+  return before + (static_cast<int64_t>(piece) * a.n_kv_heads + kvh) * kFewRows + row;
+}
+
+// How the keys of the requests of few rows are cut into pieces of equal
+// length, a request's pieces one after another.  Up to kPlanned requests the
+// cut follows the lengths (a pass over them, 64 at a time, by every wave):
+// one piece of the average work for each of kFewSlots workgroups when all
+// are alike (32 requests of 32768 E4M3 keys of 4 heads of 256: 325 us; with
+// 2048 keys a piece 353 us), down to a quarter of it when they differ (64
+// requests of 1 to 16384 keys: 92 us with 2048 keys a piece, 80 us with
+// 1024, 116 us with 4096), never less than few_least keys.
+constexpr int kPlanned = 256;
+constexpr int kFewSlots = 512;
+constexpr int few_least(int d) { return d == 64 ? 256 : 512; }
+struct Cut {
+  int chunk, pieces;
+  int first[kPlanned / 64];        // lane i: first piece of requests i, 64 + i, ...
+};
+
+// Inclusive sums over the lanes of non-negative values, in registers (DPP: a
+// shift of 1, 2, 4, 8 in each row of 16 lanes, then the rows' ends passed on).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int lane_sums(int x) {
+  x += dpp_or_zero<0x111, 0xF>(x);
+  x += dpp_or_zero<0x112, 0xF>(x);
+  x += dpp_or_zero<0x114, 0xF>(x);
+  x += dpp_or_zero<0x118, 0xF>(x);
+  x += dpp_or_zero<0x142, 0xA>(x);
+  x += dpp_or_zero<0x143, 0xC>(x);
+  return x;
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float x) {
+  return __uint_as_float(dpp_or_zero<CTRL, ROWS>(static_cast<int>(__float_as_uint(x))));
+}
+// Sum and maximum over the wave of non-negative values (in lane 63's order:
+// the same in every wave).
+__device__ __forceinline__ float of_last(float x) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 63));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x += dpp_or_zero<0x111, 0xF>(x);
+  x += dpp_or_zero<0x112, 0xF>(x);
+  x += dpp_or_zero<0x114, 0xF>(x);
+  x += dpp_or_zero<0x118, 0xF>(x);
+  x += dpp_or_zero<0x142, 0xA>(x);
+  x += dpp_or_zero<0x143, 0xC>(x);
+  return of_last(x);
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, dpp_or_zero<0x111, 0xF>(x));
+  x = fmaxf(x, dpp_or_zero<0x112, 0xF>(x));
+  x = fmaxf(x, dpp_or_zero<0x114, 0xF>(x));
+  x = fmaxf(x, dpp_or_zero<0x118, 0xF>(x));
+  x = fmaxf(x, dpp_or_zero<0x142, 0xA>(x));
+  x = fmaxf(x, dpp_or_zero<0x143, 0xC>(x));
+  return of_last(x);
+}
+
+template <int D>
+__device__ __forceinline__ Cut cut_of(const Args& a) {
+  Cut c = {a.few_chunk, a.few_pieces, {}};
+  if (a.few_chunk) return c;
+  const int lane = threadIdx.x & 63;
+  int keys[kPlanned / 64];         // -1: not a request of few rows
+  float total = 0.0f, most = 0.0f, n = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kPlanned / 64; ++q) {
+    keys[q] = -1;
+    if (q * 64 >= a.n_requests) continue;
+    const int i = q * 64 + lane;
+    if (i < a.n_requests) {
+      const Span s = span_of(a, i, 0, kFewRows);
+      const int64_t rows = static_cast<int64_t>(s.n_new) * a.group.d;
+      if (rows > 0 && rows <= kFewRows) {
+        keys[q] = s.hi - s.start;
+        total += static_cast<float>(keys[q]);
+        most = fmaxf(most, static_cast<float>(keys[q]));
+        n += 1.0f;
+      }
+    }
+  }
+  total = wave_sum(total);
+  most = wave_max(most);
+  n = wave_sum(n);
+  const float uneven = fminf(n * most / fmaxf(total, 1.0f), 4.0f);
+  const float want = total * static_cast<float>(a.n_kv_heads) / (kFewSlots * fmaxf(uneven, 1.0f));
+  // rounded up to whole tiles of the four waves
+  c.chunk = (static_cast<int>(fminf(want, 0x1p30f)) + 127) & -128;
+  c.chunk = __builtin_amdgcn_readfirstlane(c.chunk > few_least(D) ? c.chunk : few_least(D));
+  const float per_key = 1.0f / static_cast<float>(c.chunk);
+  int before = 0;
+#pragma unroll
+  for (int q = 0; q < kPlanned / 64; ++q) {
+    c.first[q] = before;
+    if (q * 64 >= a.n_requests) continue;
+    int count = keys[q] < 0 ? 0 : 1;
+    if (keys[q] > c.chunk) {
+      // ceil(keys / chunk), the quotient in binary32 put right
+      count = static_cast<int>(static_cast<float>(keys[q]) * per_key);
+      while (static_cast<int64_t>(count) * c.chunk < keys[q]) ++count;
+      while (static_cast<int64_t>(count - 1) * c.chunk >= keys[q]) --count;
+    }
+    const int sums = lane_sums(count);
+    c.first[q] = before + sums - count;
+    before += __builtin_amdgcn_readlane(sums, 63);
+  }
+  c.pieces = before;
+  return c;
+}
+
+// First piece of request r, and the request of a piece.
+__device__ __forceinline__ int first_piece(const Args& a, const Cut& c, int r) {
+  if (a.few_chunk) return r * a.few_splits;
+  int f = 0;
+#pragma unroll
+  for (int q = 0; q < kPlanned / 64; ++q)
+    if (r >> 6 == q) f = __builtin_amdgcn_readlane(c.first[q], r & 63);
+  return f;
+}
+__device__ __forceinline__ int request_of(const Args& a, const Cut& c, int piece) {
+  if (a.few_chunk) return piece / a.few_splits;
+  int n = 0;                       // requests that begin at or before the piece
+#pragma unroll
+  for (int q = 0; q < kPlanned / 64; ++q)
+    n += __popcll(__ballot(q * 64 + static_cast<int>(threadIdx.x & 63) < a.n_requests &&
+                           c.first[q] <= piece));
+  return n - 1;
 }
 
 // ---------------------------------------------------------------- staging
 
 // 16 bytes from global memory: said so, since a load that might be of LDS
 // counts with the LDS reads and makes each of their waits wait for it.
+// ONCE: nothing reads them again, so they need not displace what is cached.
+template <bool ONCE>
 __device__ __forceinline__ u32x4 load16b(const uint8_t* base, unsigned off) {
   typedef const __attribute__((address_space(1))) uint8_t* gptr;
   typedef const __attribute__((address_space(1))) u32x4* gvec;
-  return *(gvec)((gptr)base + off);
+  const gvec p = (gvec)((gptr)base + off);
+  return ONCE ? __builtin_nontemporal_load(p) : *p;
 }
 
 __device__ const u32x4 kZeros[64] = {};           // a row for pages out of range
@@ -291,7 +427,7 @@ struct Stage {
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < T::kLoads; ++i)
-        x[i] = load16b(base, min(max(r0 * stride + i * kStep * stride, first), end) + c0 * 16);
+        x[i] = load16b<false>(base, min(max(r0 * stride + i * kStep * stride, first), end) + c0 * 16);
     } else {
       // LDS takes consecutive lanes' pieces one after another; which chunk of
       // the row a lane brings makes the exchange
@@ -430,7 +566,7 @@ __device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>
   const int group = static_cast<int>(a.group.d);
   const int64_t n_rows = static_cast<int64_t>(clampi(a.cu[r + 1], 0, a.n_tokens) -
                                               clampi(a.cu[r], 0, a.n_tokens)) * group;
-  if (row0 < 0 || row0 >= n_rows || (a.few_splits > 0 && n_rows <= kFewRows)) return;
+  if (row0 < 0 || row0 >= n_rows || (a.few_pieces > 0 && n_rows <= kFewRows)) return;
   const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
   const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
@@ -683,7 +819,7 @@ struct Stream {
     for (int p = 0; p < 2; ++p) {
       const int row = inside(lane & 15, at[p].first, at[p].end) * kt + (lane >> 4) * 16;
 #pragma unroll
-      for (int i = 0; i < kK; ++i) k[p][i] = load16b(at[p].k, row + i * 64);
+      for (int i = 0; i < kK; ++i) k[p][i] = load16b<true>(at[p].k, row + i * 64);
     }
   }
   __device__ __forceinline__ void load_v() {
@@ -692,7 +828,7 @@ struct Stream {
     for (int i = 0; i < kV; ++i) {
       const int p = i * 64 / kChunks / 16;                  // a load lies in one group
       const int r = (i * 64 + lane) / kChunks - 16 * p, c = (i * 64 + lane) % kChunks;
-      v[i] = load16b(at[p].v, inside(r, at[p].first, at[p].end) * vt + c * 16);
+      v[i] = load16b<true>(at[p].v, inside(r, at[p].first, at[p].end) * vt + c * 16);
     }
   }
   // The 8 rows that 32 lanes of a transposing read touch differ by 32 bytes.
@@ -733,8 +869,8 @@ struct Stream {
 // through an LDS area of the wave's own); the four waves are joined at the
 // end.  Bound by the read of the keys and values.
 template <int D, bool FP8>
-__device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>& lds,
-                                         float (*lds_m)[16], float (*lds_l)[16]) {
+__device__ __forceinline__ void few_rows(const Args& a, const Cut& cut, int piece, int kvh,
+                                         const Lds<D>& lds, float (*lds_m)[16], float (*lds_l)[16]) {
   using S = Stream<D, FP8>;
   constexpr int kSteps = D / 32;
   constexpr int kDb = D / 16;
@@ -743,17 +879,16 @@ __device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>&
 
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-  const int kvh = block % a.n_kv_heads;
-  const int rest = block / a.n_kv_heads;
-  const int split = rest % a.few_splits, r = rest / a.few_splits;
+  const int r = __builtin_amdgcn_readfirstlane(request_of(a, cut, piece));
+  const int split = piece - first_piece(a, cut, r);
   const int group = static_cast<int>(a.group.d);
   const Span s = span_of(a, r, 0, kFewRows);
   const int64_t n_rows = static_cast<int64_t>(s.n_new) * group;
   if (n_rows < 1 || n_rows > kFewRows) return;
-  const int splits = splits_of(s, a.few_chunk, a.few_splits);
+  const int splits = splits_of(s, cut.chunk, a.few_chunk ? a.few_splits : 0x7FFFFFFF);
   if (split >= splits) return;
-  const int begin = s.start + split * a.few_chunk;
-  const int end = split == splits - 1 ? s.hi : begin + a.few_chunk;
+  const int begin = s.start + split * cut.chunk;
+  const int end = split == splits - 1 ? s.hi : begin + cut.chunk;
 
   const bool real = col < n_rows;
   const int token = static_cast<int>(a.group.div(real ? col : 0));
@@ -866,7 +1001,7 @@ __device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>&
   for (int b = 0; b < kDb; ++b)
     *reinterpret_cast<f32x4*>(lv + col * (D * 4) + (((4 * b + quad) ^ col) << 4)) = acc[b];
   __syncthreads();
-  const int row = threadIdx.x >> 4, piece = threadIdx.x & 15;
+  const int row = threadIdx.x >> 4, place = threadIdx.x & 15;
   if (row >= n_rows) return;
   float w[4], mm = kNegInf, ll = 0.0f;
 #pragma unroll
@@ -879,12 +1014,12 @@ __device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>&
   }
   const int out_token = static_cast<int>(a.group.div(row));
   const int out_head = kvh * group + row - out_token * group;
-  const int64_t at = few_slot(a, split, r, kvh, row);
+  const int64_t at = few_slot(a, piece, kvh, row);
   const float inv = output_factor<FP8>(a, ll);
   uint8_t* op = a.out + (static_cast<int64_t>(s.token0) + out_token) * a.out_token + out_head * a.out_head;
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
-    const int ch = piece + 16 * e;
+    const int ch = place + 16 * e;
     f32x4 o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -900,7 +1035,7 @@ __device__ __forceinline__ void few_rows(const Args& a, int block, const Lds<D>&
       *reinterpret_cast<f32x4*>(a.part + at * D + ch * 4) = o;
     }
   }
-  if (splits > 1 && piece == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{mm, ll};
+  if (splits > 1 && place == 0) *reinterpret_cast<f32x2*>(a.part_ml + at * 2) = f32x2{mm, ll};
 }
 
 // Tiles of rows, requests of few rows, or both in one launch (the first
@@ -921,7 +1056,10 @@ __global__ void __launch_bounds__(256, !TILES && D > 128 && !FP8 ? 1 : 2) attent
   }
   if constexpr (FEW) {
     __shared__ float lds_m[4][16], lds_l[4][16];
-    few_rows<D, FP8>(a, TILES ? block - a.tile_blocks : block, lds, lds_m, lds_l);
+    const int unit = TILES ? block - a.tile_blocks : block;
+    const Cut cut = cut_of<D>(a);
+    if (unit < cut.pieces * a.n_kv_heads)
+      few_rows<D, FP8>(a, cut, unit / a.n_kv_heads, unit % a.n_kv_heads, lds, lds_m, lds_l);
   }
 }
 
@@ -946,13 +1084,21 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   if (t < token0 || t >= token1) return;             // a row of no request
   const int kvh = static_cast<int>(a.group.div(static_cast<unsigned>(head)));
   const int in_request = (t - token0) * group + head - kvh * group;
-  const bool few = a.few_splits > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
-  const Span s = few ? span_of(a, r, 0, kFewRows)
-                     : span_of(a, r, in_request & -kTileRows, kTileRows);
-  const int splits = few ? splits_of(s, a.few_chunk, a.few_splits) : splits_of(s, a.chunk, a.splits);
+  const bool few = a.few_pieces > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
+  int splits;
+  int64_t at, step;
+  if (few) {
+    const Cut cut = cut_of<D>(a);
+    splits = splits_of(span_of(a, r, 0, kFewRows), cut.chunk, a.few_chunk ? a.few_splits : 0x7FFFFFFF);
+    const int piece = first_piece(a, cut, r);
+    at = few_slot(a, piece, kvh, in_request);
+    step = few_slot(a, piece + 1, kvh, in_request) - at;
+  } else {
+    splits = splits_of(span_of(a, r, in_request & -kTileRows, kTileRows), a.chunk, a.splits);
+    at = tile_slot(a, 0, t, head);
+    step = tile_slot(a, 1, t, head) - at;
+  }
   if (splits == 1) return;
-  const int64_t at = few ? few_slot(a, 0, r, kvh, in_request) : tile_slot(a, 0, t, head);
-  const int64_t step = few ? few_slot(a, 1, r, kvh, in_request) - at : tile_slot(a, 1, t, head) - at;
   // a lane takes the bound and the sum of weights of every 64th chunk
   float m = kNegInf;
   for (int i = lane; i < splits; i += 64) {
@@ -1003,34 +1149,22 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kCus = 256;
-constexpr int64_t kLongest = 2048;
+constexpr int64_t kLongest = 4096;
 
 struct Plan {
   int64_t tiles, splits, chunk;           // tiles == 0: no request of many rows
-  int64_t few_splits, few_chunk;          // few_splits == 0: none of few
+  // few_pieces == 0: none of few rows; few_chunk == 0: cut by the kernel
+  int64_t few_pieces, few_chunk, few_splits;
   int64_t slots;                          // places of chunks' sums
 };
 
-// Chunks that fill `fill` workgroups when `items` take one each: whole
-// multiples of `unit` keys, at least `least`.
-void cut(int64_t keys, int64_t items, int64_t fill, int64_t unit, int64_t least, int64_t* splits,
-         int64_t* chunk) {
-  int64_t want = (fill + items - 1) / items;
-  const int64_t most = (keys + least - 1) / least;
-  want = want < most ? want : most;
-  want = want > 1 ? want : 1;
-  *chunk = ((keys + want - 1) / want + unit - 1) / unit * unit;
-  if (*chunk < unit) *chunk = unit;
-  *splits = (keys + *chunk - 1) / *chunk;
-  if (*splits < 1) *splits = 1;
-}
-
-// Keys that the first and last of `tokens` neighbours see together, the
-// first 16-key group rounded down included.
+// Keys that the first and last of `tokens` neighbours see together, with a
+// window the first 16-key group rounded down included.
 int64_t span_keys(const AttnCall& c, int64_t tokens) {
   const int64_t keys = c.table ? c.max_kv : c.max_new;
+  if (!c.window) return keys;
   const int64_t seen = c.window + tokens - 1;
-  return (c.window && c.causal && keys > seen ? seen : keys) + 15;
+  return (c.causal && keys > seen ? seen : keys) + 15;
 }
 
 // Chunks of the tiles' keys by their estimated time.  Two workgroups fit a
@@ -1075,33 +1209,39 @@ Plan plan_of(const AttnCall& c) {
     p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
     cut_tiles(c, group, &p);
   }
-  if (few)
-  {
-    const int64_t keys = span_keys(c, kFewRows), items = c.n_requests * c.n_kv_heads;
-    // lengths differ: no workgroup takes more than kLongest keys while
-    // another has none (but for so many requests that they balance anyway)
-    const int64_t by_length = items < (1 << 16) ? items * ((keys + kLongest - 1) / kLongest) : 0;
-    cut(keys, items, by_length > 4 * kCus ? by_length : 4 * kCus, 128, 256, &p.few_splits,
-        &p.few_chunk);
+  if (few) {
+    const int64_t keys = span_keys(c, kFewRows), least = few_least(static_cast<int>(c.d));
+    if (c.n_requests == 1 && keys > least) {
+      // its length is the bound: enough pieces for every CU
+      const int64_t want = (4 * kCus + c.n_kv_heads - 1) / c.n_kv_heads;
+      p.few_chunk = ((keys + want - 1) / want + 127) / 128 * 128;
+      if (p.few_chunk < least) p.few_chunk = least;
+      p.few_splits = p.few_pieces = (keys + p.few_chunk - 1) / p.few_chunk;
+    } else if (c.n_requests <= kPlanned && keys > least) {
+      // kFewSlots pieces at most four times over, and a last one a request
+      p.few_pieces = c.n_requests + (4 * kFewSlots + c.n_kv_heads - 1) / c.n_kv_heads;
+    } else {
+      // short keys are not cut; of very many requests only long ones are
+      p.few_splits = c.n_requests <= kPlanned ? 1 : (keys + kLongest - 1) / kLongest;
+      p.few_chunk = p.few_splits > 1 ? kLongest : (keys + 127) / 128 * 128;
+      p.few_pieces = c.n_requests * p.few_splits;
+    }
   }
   if (p.splits > 1) p.slots += p.splits * c.n_tokens * c.n_heads;
-  if (p.few_splits > 1) p.slots += p.few_splits * c.n_requests * c.n_kv_heads * kFewRows;
+  if (p.few_splits != 1) p.slots += p.few_pieces * c.n_kv_heads * kFewRows;
   return p;
 }
 
 template <int D, bool FP8>
 void launch(const Args& a, hipStream_t stream) {
-  const unsigned few = static_cast<unsigned>(static_cast<int64_t>(a.n_requests) * a.few_splits * a.n_kv_heads);
-  if (a.tiles > 0 && a.few_splits > 0)
-    attention_kernel<D, FP8, true, true><<<a.tile_blocks + few, 256, 0, stream>>>(a);
-  else if (a.tiles > 0)
-    attention_kernel<D, FP8, true, false><<<a.tile_blocks, 256, 0, stream>>>(a);
-  else
-    attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
-  if (a.splits > 1 || a.few_splits > 1) {
+  const unsigned tiles = static_cast<unsigned>(a.tile_blocks), few = static_cast<unsigned>(a.few_blocks);
+  if (tiles && few) attention_kernel<D, FP8, true, true><<<tiles + few, 256, 0, stream>>>(a);
+  else if (tiles) attention_kernel<D, FP8, true, false><<<tiles, 256, 0, stream>>>(a);
+  else attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
+  if (a.splits > 1 || (a.few_pieces > 0 && a.few_splits != 1)) {
     // four waves a row for many chunks, as long as the rows are few
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
-    if ((a.splits > 8 || a.few_splits > 8) && rows <= 8192)
+    if ((a.splits > 8 || a.few_splits != 1) && rows <= 8192)
       combine_kernel<D, FP8, 4><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a);
     else
       combine_kernel<D, FP8, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
@@ -1156,8 +1296,10 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.splits = static_cast<int>(p.splits);
   a.tile_blocks = static_cast<int>(p.tiles * p.splits * c.n_kv_heads);
   a.chunk = static_cast<int>(p.chunk);
-  a.few_splits = static_cast<int>(p.few_splits);
+  a.few_pieces = static_cast<int>(p.few_pieces);
   a.few_chunk = static_cast<int>(p.few_chunk);
+  a.few_splits = static_cast<int>(p.few_splits);
+  a.few_blocks = static_cast<int>(p.few_pieces * c.n_kv_heads);
   const bool fp8 = paged && c.pool.fp8;
   if (c.d == 64) fp8 ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
   else if (c.d == 128) fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);

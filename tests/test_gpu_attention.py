@@ -169,6 +169,22 @@ def test_paged_many_requests(n):
     check(nv.paged_attention(*call, **kw), reference(parts, 0.125, True, 0, 64, False), n)
 
 
+@pytest.mark.parametrize("n,longest,kv_heads,d,fp8", [
+    (2, 5000, 2, 64, False), (64, 3000, 1, 64, True), (70, 4000, 1, 128, False),
+    (256, 2500, 1, 64, False), (257, 4500, 1, 64, False)])
+def test_paged_pieces_of_many_lengths(n, longest, kv_heads, d, fp8):
+    """Keys cut into pieces over requests of very different lengths, among
+    them empty ones and chunks that are no single tokens."""
+    _say("pieces", n, longest, kv_heads, d, fp8)
+    rng = np.random.default_rng(n)
+    lens = [(1, int(b)) for b in np.exp(rng.uniform(0, np.log(longest), n)).astype(int)]
+    lens[0] = (1, longest)
+    if n > 2:
+        lens[1], lens[2], lens[n // 2] = (0, 700), (40, 900), (1, 0)
+    *call, kw, parts = build(rng, lens, 2 * kv_heads, kv_heads, d, 16, fp8, "head")
+    check(nv.paged_attention(*call, **kw), reference(parts, d ** -0.5, True, 0, d, fp8), n)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("new", [1, 2, 40])
 def test_paged_split_keys(new, fp8):
