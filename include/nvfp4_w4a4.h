@@ -380,7 +380,7 @@ int kv_page_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,
  *                them stands at position kv_lens[r] - 1.
  *   n_heads      a multiple of n_kv_heads; head h reads key/value head
  *                h / (n_heads / n_kv_heads).  n_heads <= 65536, n_tokens *
- *                n_heads <= 2^30, n_requests * n_kv_heads <= 2^26.
+ *                n_heads <= 2^25, n_requests * n_kv_heads <= 2^20.
  *   d            64, 128 or 256 (else UNSUPPORTED).
  *   k_cache ... token_stride, scales   the cache as for kv_page_write; a token
  *                stride below 2^26 bytes.

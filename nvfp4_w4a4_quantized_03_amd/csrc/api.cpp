@@ -98,9 +98,9 @@ int check_attention(const nvfp4::AttnCall& c) {
       c.max_kv < 0 || c.max_kv > kInt - 65536 || c.max_new > kInt - 65536 || c.window < 0 ||
       c.window > kInt - 65536)
     return NVFP4_ERR_INVALID_VALUE;
-  // rows, tiles and workgroups are counted in 32 bits
-  if (c.n_tokens > (int64_t(1) << 30) / c.n_heads ||
-      c.n_requests > (int64_t(1) << 26) / c.n_kv_heads)
+  // a launch has fewer than 2^32 threads: 64 a row to join, 256 a tile
+  if (c.n_tokens > (int64_t(1) << 25) / c.n_heads ||
+      c.n_requests > (int64_t(1) << 20) / c.n_kv_heads)
     return NVFP4_ERR_INVALID_VALUE;
   if (!(c.scale > 0.0f) || isinf(c.scale)) return NVFP4_ERR_INVALID_VALUE;
   if (c.d != 64 && c.d != 128 && c.d != 256) return NVFP4_ERR_UNSUPPORTED;

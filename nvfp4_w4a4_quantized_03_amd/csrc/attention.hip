@@ -257,8 +257,9 @@ __device__ __forceinline__ Cut cut_of(const Args& a) {
   n = wave_sum(n);
   const float uneven = fminf(n * most / fmaxf(total, 1.0f), 4.0f);
   const float want = total * static_cast<float>(a.n_kv_heads) / (kFewSlots * fmaxf(uneven, 1.0f));
-  // rounded up to whole tiles of the four waves
-  c.chunk = (static_cast<int>(fminf(want, 0x1p30f)) + 127) & -128;
+  // rounded up to whole tiles of the four waves (at least `want`, which is
+  // what bounds the number of pieces)
+  c.chunk = (static_cast<int>(fminf(want, 0x1p30f)) + 128) & -128;
   c.chunk = __builtin_amdgcn_readfirstlane(c.chunk > few_least(D) ? c.chunk : few_least(D));
   const float per_key = 1.0f / static_cast<float>(c.chunk);
   int before = 0;
@@ -1185,7 +1186,7 @@ void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
   const double sums_us = static_cast<double>(c.n_tokens) * c.n_heads * c.d * 8.0 / 4e6;
   double best = 0.0;
   int64_t splits = 1;
-  for (int64_t n = 1; n <= 16 && (n == 1 || keys >= 256 * n); ++n) {
+  for (int64_t n = 1; n <= 16 && (n == 1 || (keys >= 256 * n && wgs < 16.0 * kCus)); ++n) {
     const double r = wgs * n / (2.0 * kCus), full = floor(r);
     const double rounds = graded && r > 1.0 ? r : full + (r - full > 0.5 ? 1.0 : r > full ? 0.62 : 0.0);
     const double us = round_us * rounds / n + (n > 1 ? 6.0 + n * sums_us : 0.0);
@@ -1219,11 +1220,15 @@ Plan plan_of(const AttnCall& c) {
       p.few_splits = p.few_pieces = (keys + p.few_chunk - 1) / p.few_chunk;
     } else if (c.n_requests <= kPlanned && keys > least) {
       // kFewSlots pieces at most four times over, and a last one a request
-      p.few_pieces = c.n_requests + (4 * kFewSlots + c.n_kv_heads - 1) / c.n_kv_heads;
+      // (and one for the binary32 of the kernel's division)
+      p.few_pieces = c.n_requests + (4 * kFewSlots + c.n_kv_heads - 1) / c.n_kv_heads + 1;
     } else {
       // short keys are not cut; of very many requests only long ones are
       p.few_splits = c.n_requests <= kPlanned ? 1 : (keys + kLongest - 1) / kLongest;
-      p.few_chunk = p.few_splits > 1 ? kLongest : (keys + 127) / 128 * 128;
+      const int64_t most = (int64_t(1) << 21) / (c.n_requests * c.n_kv_heads);
+      if (p.few_splits > most) p.few_splits = most > 1 ? most : 1;
+      p.few_chunk = ((keys + p.few_splits - 1) / p.few_splits + 127) / 128 * 128;
+      if (p.few_chunk < 128) p.few_chunk = 128;
       p.few_pieces = c.n_requests * p.few_splits;
     }
   }
