@@ -19,15 +19,19 @@
 // product may take the 16 keys of a step in any order, so V^T is read in
 // that one: two transposing LDS reads of 4 keys each per operand.
 //
-// Staging.  K and V go through registers into LDS (E4M3 codes are widened
-// there once per workgroup and not once per wave: K to bf16, V to fp16, both
-// exact), two tiles deep: while a tile is used the next one is in flight.
-// 16-byte chunks of a row are exchanged by an exclusive or with the row
-// number so that the fragment reads of 16 rows fall on different banks.
+// Staging of tiles.  Two tiles of K and V in LDS: while one is used the next
+// is in flight, bf16 from memory straight to LDS, E4M3 codes through
+// registers, where they are widened once per workgroup and not once per wave
+// (K to bf16, V to fp16, both exact).  16-byte chunks of a row are exchanged
+// by an exclusive or with the row number so that the operand reads of 16 rows
+// fall on different banks (no conflict counted).
 //
-// Splits.  With few tiles the keys are cut into chunks that other
-// workgroups take; each leaves its sums in binary32 with its bound, and
-// combine_kernel joins them in chunk order (no atomics: results do not
+// Requests of few rows (decodes) have no use for tiles: they are bound by the
+// read of their keys and values, which a kernel of its own streams.
+//
+// Chunks.  With few tiles, and for decodes, the keys are cut into chunks that
+// other workgroups take; each leaves its sums in binary32 with its bound, and
+// combine_kernel joins them in a fixed order (no atomics: results do not
 // depend on timing).
 //
 // Precision.  Scores, bounds, sums and outputs are binary32.  The weights
@@ -301,6 +305,73 @@ __device__ __forceinline__ int request_of(const Args& a, const Cut& c, int piece
   return n - 1;
 }
 
+// Tile `index` of the launch: its request and which of the request's tiles it
+// is.  Up to kPlanned requests the tiles come by their place in the request,
+// the last ones first: under a causal mask those have the most keys, and a
+// long tile that starts late would end alone (7 prompts of up to 2001 tokens,
+// d 256: 103 us in the requests' order, 100 us in this one; 16 requests of 5
+// speculated tokens: 31.5 and 29 us).  With S(p) = sum_r max(0, tiles_r - p) tiles at places >= p, tile `index` is at
+// the largest p with S(p) > index.
+__device__ __forceinline__ int64_t rows_of(const Args& a, int r) {
+  const int t0 = clampi(a.cu[r], 0, a.n_tokens);
+  return static_cast<int64_t>(clampi(a.cu[r + 1], t0, a.n_tokens) - t0) * a.group.d;
+}
+__device__ __forceinline__ bool tile_of(const Args& a, int index, int* r, int* level) {
+  if (a.n_requests > kPlanned) {
+    const int tile = a.tiles - 1 - index;
+    *r = __builtin_amdgcn_readfirstlane(find_request<false>(a, tile));
+    *level = static_cast<int>(tile - first_tile(a, *r));
+    return true;
+  }
+  constexpr int kQ = kPlanned / 64;
+  const int lane = threadIdx.x & 63;
+  int tiles[kQ], most = 0, total = 0;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    tiles[q] = 0;
+    if (q * 64 >= a.n_requests) continue;
+    if (q * 64 + lane < a.n_requests) {
+      const int64_t rows = rows_of(a, q * 64 + lane);
+      if (!(a.few_pieces > 0 && rows <= kFewRows))
+        tiles[q] = static_cast<int>((rows + kTileRows - 1) / kTileRows);
+    }
+    most = max(most, tiles[q]);
+    total += tiles[q];
+  }
+  most = static_cast<int>(wave_max(static_cast<float>(most)));
+  if (index >= __builtin_amdgcn_readlane(lane_sums(total), 63)) return false;
+  int lo = 0, hi = most, above = 0;     // S(lo) > index >= S(hi) = above
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) n += max(tiles[q] - mid, 0);
+    n = __builtin_amdgcn_readlane(lane_sums(n), 63);
+    if (n > index) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = n;
+    }
+  }
+  int nth = index - above;              // among the requests with a tile at lo
+  *level = lo;
+  *r = 0;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const uint64_t have = __ballot(tiles[q] > lo);
+    const int n = __popcll(have);
+    if (nth >= 0 && nth < n) {
+      const int before = __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(have >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(have), 0));
+      const uint64_t it = __ballot(tiles[q] > lo && before == nth);
+      *r = q * 64 + __builtin_ctzll(it);
+    }
+    nth -= n;
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- staging
 
 // 16 bytes from global memory: said so, since a load that might be of LDS
@@ -545,7 +616,16 @@ struct Lds {
 // Workgroup `block` of the tiles: 128 rows, 4 waves of 32.  Two waves a SIMD
 // at every D, so that one's exponentials run under another's products; D =
 // 256 (128 registers of sums, 64 of queries) affords that with tiles of 32
-// keys.
+// keys: 8192 tokens of 20 heads of 256 in 640 us (1.07 PFLOP/s), with one
+// wave a SIMD 900 us.  A 16384-token prompt of 40 heads of 128 takes 2.58 ms
+// (1.06 PFLOP/s, 43 % of the matrix peak): the matrix cores are busy 56 % of
+// the cycles and the vector units 51 %, and the clock is held at 1.8 GHz by
+// power, so what is left is energy and not idle time.  Measured and not
+// taken there: 64 rows a wave (half the LDS reads, but one wave a SIMD: 3.1
+// ms), scores of the next tile taken under the exponentials of this one
+// within a wave (3.0 ms, no registers left to read ahead), 32-key tiles at
+// three waves a SIMD (2.55 ms; E4M3 chunks cut in two lose 6 %), raised wave
+// priority around the products (no change).
 template <int D, bool FP8>
 __device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>& lds) {
   using T = Tile<D, FP8>;
@@ -560,14 +640,12 @@ __device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>
   const int kvh = block % a.n_kv_heads;
   const int rest = block / a.n_kv_heads;
   const int split = rest % a.splits;
-  const int tile = a.tiles - 1 - rest / a.splits;    // the longest rows of a prompt first
-
-  const int r = __builtin_amdgcn_readfirstlane(find_request<false>(a, tile));
-  const int64_t row0 = (tile - first_tile(a, r)) * kTileRows;
+  int r, level;
+  if (!tile_of(a, rest / a.splits, &r, &level)) return;
+  const int64_t row0 = static_cast<int64_t>(level) * kTileRows;
   const int group = static_cast<int>(a.group.d);
-  const int64_t n_rows = static_cast<int64_t>(clampi(a.cu[r + 1], 0, a.n_tokens) -
-                                              clampi(a.cu[r], 0, a.n_tokens)) * group;
-  if (row0 < 0 || row0 >= n_rows || (a.few_pieces > 0 && n_rows <= kFewRows)) return;
+  const int64_t n_rows = rows_of(a, r);
+  if (row0 >= n_rows || (a.few_pieces > 0 && n_rows <= kFewRows)) return;
   const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
   const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
@@ -868,7 +946,9 @@ struct Stream {
 // group of heads, a few speculated ones.  Its keys are streamed once, each
 // wave taking 32 at a time straight from memory (no barrier: V passes
 // through an LDS area of the wave's own); the four waves are joined at the
-// end.  Bound by the read of the keys and values.
+// end.  Bound by the read of the keys and values: 32 requests of 32768 E4M3
+// keys, 4 heads of 256, in 325 us (6.6 TB/s; 128-row tiles take 986 us), 64
+// ragged requests of bf16, 16 heads of 64, in 77 us (5.3 TB/s).
 template <int D, bool FP8>
 __device__ __forceinline__ void few_rows(const Args& a, const Cut& cut, int piece, int kvh,
                                          const Lds<D>& lds, float (*lds_m)[16], float (*lds_l)[16]) {
@@ -1100,6 +1180,38 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
     step = tile_slot(a, 1, t, head) - at;
   }
   if (splits == 1) return;
+  typedef float vec __attribute__((ext_vector_type(kEach)));
+  if constexpr (WAVES == 1) {
+    constexpr int kShort = 8;
+    if (splits <= kShort) {
+      // all reads at once
+      f32x2 ml = {kNegInf, 0.0f};
+      if (lane < splits) ml = *reinterpret_cast<const f32x2*>(a.part_ml + (at + lane * step) * 2);
+      vec x[kShort];
+#pragma unroll
+      for (int i = 0; i < kShort; ++i)
+        x[i] = i < splits ? *reinterpret_cast<const vec*>(a.part + (at + i * step) * D + lane * kEach)
+                          : vec{};
+      float m = ml[1] > 0.0f ? ml[0] : kNegInf;
+#pragma unroll
+      for (int off = 1; off < kShort; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+      const float f = ml[1] > 0.0f ? __builtin_amdgcn_exp2f(ml[0] - m) : 0.0f;
+      float l = 0.0f;
+      vec o = {};
+#pragma unroll
+      for (int i = 0; i < kShort; ++i) {
+        const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+        l = __builtin_fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml[1]), i)), fi, l);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) o[e] = __builtin_fmaf(x[i][e], fi, o[e]);
+      }
+      const float inv = output_factor<FP8>(a, l);
+      __bf16* op = reinterpret_cast<__bf16*>(a.out + t * a.out_token + head * a.out_head) + lane * kEach;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) op[e] = static_cast<__bf16>(o[e] * inv);
+      return;
+    }
+  }
   // a lane takes the bound and the sum of weights of every 64th chunk
   float m = kNegInf;
   for (int i = lane; i < splits; i += 64) {
@@ -1121,7 +1233,6 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
 #pragma unroll 8
     for (int i = mine; i < n; i += WAVES) {
       const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-      typedef float vec __attribute__((ext_vector_type(kEach)));
       const vec x = *reinterpret_cast<const vec*>(p + i * step * D);
 #pragma unroll
       for (int e = 0; e < kEach; ++e) o[e] = __builtin_fmaf(x[e], fi, o[e]);
