@@ -284,6 +284,23 @@ def test_prompt(lens, heads, kv_heads, d, causal, window):
     assert (big[:, 0] == 7).all() and (big[:, heads + 1:] == 7).all()
 
 
+@pytest.mark.parametrize("n", [70, 256, 257])
+def test_prompt_many_of_several_tiles(n):
+    """The order of the tiles over more prompts than lanes, and over more than
+    are ordered."""
+    _say("many prompts", n)
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 150, n).tolist()
+    lens[3] = 400
+    x64, x = bf16(rng.standard_normal((sum(lens), 4, 64)))
+    cu = [0]
+    for a in lens:
+        cu.append(cu[-1] + a)
+    got = nv.prompt_attention(x[:, :2], x[:, 2:3], x[:, 3:], i32(cu), 400, window=90)
+    parts = [(x64[a:b, :2], x64[a:b, 2:3], x64[a:b, 3:]) for a, b in zip(cu, cu[1:])]
+    check(got, reference(parts, 0.125, True, 90, 64, False), n)
+
+
 def test_prompt_agrees_with_chunks():
     """A prompt at once and in three chunks over the cache: the same rows
     within both tolerances."""
