@@ -478,8 +478,18 @@ def fp8_kv_cast(x, scale, out=None):
     return out
 
 
+def _on(t, dtype, index):
+    """Whether t is a tensor of this type on GPU `index`: the usual answer
+    without the checks that find out what to complain about."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and \
+        t.get_device() == index
+
+
 def _ints(t, name, dtype, device, numel=None):
     """A contiguous 1-D integer GPU tensor."""
+    if _on(t, dtype, device.index) and t.dim() == 1 and t.is_contiguous() and \
+            (numel is None or t.numel() == numel):
+        return t.data_ptr()
     _device_tensor(t, name, dtype, numel, device)
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous 1-D tensor" % name)
@@ -488,7 +498,8 @@ def _ints(t, name, dtype, device, numel=None):
 
 def _table_args(t, device, rows):
     """Pointer, columns and row stride of an int32 block table."""
-    _device_tensor(t, "block_table", torch.int32, device=device)
+    if not _on(t, torch.int32, device.index):
+        _device_tensor(t, "block_table", torch.int32, device=device)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != rows or shape[1] < 1 or \
             (shape[1] > 1 and stride[1] != 1):
@@ -499,7 +510,8 @@ def _table_args(t, device, rows):
 
 def _head_rows(t, name, device=None, dtype=torch.bfloat16, shape=None):
     """Pointer, token stride and head stride of [tokens, heads, d] rows."""
-    _device_tensor(t, name, dtype, device=device)
+    if device is None or not _on(t, dtype, device.index):
+        _device_tensor(t, name, dtype, device=device)
     got, stride = t.shape, t.stride()
     if len(got) != 3 or stride[2] != 1 or (shape is not None and got != shape):
         raise ValueError("%s must be [tokens, heads, d] with unit stride along "
@@ -515,15 +527,17 @@ def _pool_args(k_cache, v_cache, k_scale, v_scale, device):
     pointers, dtype, sizes and strides; and the scales' pointers."""
     _device_tensor(k_cache, "k_cache", device=device)
     dtype, shape, stride = k_cache.dtype, k_cache.shape, k_cache.stride()
-    _device_tensor(v_cache, "v_cache", dtype, device=device)
+    if not _on(v_cache, dtype, device.index):
+        _device_tensor(v_cache, "v_cache", dtype, device=device)
     if len(shape) != 4 or v_cache.shape != shape or \
             v_cache.stride() != stride or stride[3] != 1:
         raise ValueError("k_cache and v_cache must be [n_pages, n_kv_heads, "
                          "page_size, d] with the same strides, unit along d")
     if dtype == torch.uint8:
         dt = DTYPE_E4M3
-        _global_tensor(k_scale, "k_scale", device)
-        _global_tensor(v_scale, "v_scale", device)
+        for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not _on(t, torch.float32, device.index) or t.numel() != 1:
+                _global_tensor(t, nm, device)
         scales = k_scale.data_ptr(), v_scale.data_ptr()
     elif dtype == torch.bfloat16:
         dt = DTYPE_BF16
@@ -564,7 +578,8 @@ def kv_page_tables(new_lens, cached_lens, block_table, free_pages, page_size,
     if out is None:
         slots = new_lens.new_empty(t, dtype=torch.int64)
         buf = new_lens.new_empty(t + 2 * n + 2)
-        cu, kv, positions, used = buf.split_with_sizes((n + 1, n, t, 1))
+        cu, kv, positions, used = torch.unsafe_split_with_sizes(
+            buf, (n + 1, n, t, 1))
         out = KVPages(cu, kv, positions, slots, used)
         at = buf.data_ptr()
         p = (at, at + 4 * n + 4, at + 8 * n + 4, slots.data_ptr(),
