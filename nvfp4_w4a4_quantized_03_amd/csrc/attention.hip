@@ -1355,9 +1355,11 @@ void launch(const Args& a, hipStream_t stream) {
   else if (tiles) attention_kernel<D, FP8, true, false><<<tiles, 256, 0, stream>>>(a);
   else attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
   if (a.splits > 1 || (a.few_pieces > 0 && a.few_splits != 1)) {
-    // four waves a row for many chunks, as long as the rows are few
+    // four waves a row for many chunks, as long as the rows are few (a step of
+    // chunks and decodes, 7220 rows of mostly three chunks: 84 us with four, 79
+    // with one)
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
-    if ((a.splits > 8 || a.few_splits != 1) && rows <= 8192)
+    if ((!tiles || a.splits > 8) && rows <= 8192)
       combine_kernel<D, FP8, 4><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a);
     else
       combine_kernel<D, FP8, 1><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, stream>>>(a);
