@@ -239,6 +239,24 @@ def test_paged_page_out_of_range_reads_zeros():
     check(nv.paged_attention(*call, **kw), reference([(q, k, v)], 0.125, True, 0, 64, False), "")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,kv,window", [(1, 300, 64), (3, 1200, 700), (40, 300, 64)])
+def test_paged_before_the_window_is_unused(new, kv, window, fp8):
+    """Keys that no row of the call sees may be anything, their pages gone."""
+    _say("before the window", new, kv, window, fp8)
+    rng = np.random.default_rng(window)
+    qd, kc, vc, table, cu, lens, mn, mk, kw, parts = build(rng, [(new, kv)], 4, 2, 128, 16, fp8,
+                                                           "head")
+    first = kv - new - window + 1
+    bad = 0x7F if fp8 else float("nan")
+    for p in range(first % 16):
+        for c in (kc, vc):
+            c[int(table[0, first // 16]), :, p] = bad
+    table[0, :first // 16] = -1
+    got = nv.paged_attention(qd, kc, vc, table, cu, lens, mn, mk, window=window, **kw)
+    check(got, reference(parts, 128 ** -0.5, True, window, 128, fp8), window)
+
+
 def test_paged_zero_scales():
     """A K scale of zero makes every weight equal, a V scale of zero every
     output."""
