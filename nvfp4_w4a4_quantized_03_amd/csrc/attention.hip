@@ -62,7 +62,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileRows = 128;         // rows of a workgroup, 32 a wave
-constexpr int kFewRows = 16;           // rows of a request that few_rows_kernel takes
+constexpr int kFewRows = 16;           // rows of a request that few_rows takes
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -1261,6 +1261,8 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kCus = 256;
+// keys of a piece where requests are too many to be planned by the kernel:
+// they even out by number, and only a request far longer than most is cut
 constexpr int64_t kLongest = 4096;
 
 struct Plan {
@@ -1307,6 +1309,7 @@ void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
     }
   }
   p->chunk = (keys + splits * 128 - 1) / (splits * 128) * 128;
+  if (p->chunk < 128) p->chunk = 128;
   p->splits = (keys + p->chunk - 1) / p->chunk;
   if (p->splits < 1) p->splits = 1;
 }
@@ -1314,9 +1317,10 @@ void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
 Plan plan_of(const AttnCall& c) {
   Plan p = {};
   const int64_t group = c.n_heads / c.n_kv_heads;
-  // a prompt of few rows has few keys too: its tile costs no more
-  const bool few = c.table && group <= kFewRows;
   const bool many = !c.table || c.max_new * group > kFewRows;
+  // a prompt of few rows has few keys too: its tile costs no more; and a
+  // single request of many rows has none of few next to it
+  const bool few = c.table && group <= kFewRows && !(many && c.n_requests == 1);
   if (many) {
     p.tiles = c.n_tokens * group / kTileRows + c.n_requests;
     cut_tiles(c, group, &p);
@@ -1337,7 +1341,8 @@ Plan plan_of(const AttnCall& c) {
       // short keys are not cut; of very many requests only long ones are
       p.few_splits = c.n_requests <= kPlanned ? 1 : (keys + kLongest - 1) / kLongest;
       const int64_t most = (int64_t(1) << 21) / (c.n_requests * c.n_kv_heads);
-      if (p.few_splits > most) p.few_splits = most > 1 ? most : 1;
+      if (p.few_splits > most) p.few_splits = most;
+      if (p.few_splits < 1) p.few_splits = 1;
       p.few_chunk = ((keys + p.few_splits - 1) / p.few_splits + 127) / 128 * 128;
       if (p.few_chunk < 128) p.few_chunk = 128;
       p.few_pieces = c.n_requests * p.few_splits;
@@ -1353,7 +1358,7 @@ void launch(const Args& a, hipStream_t stream) {
   const unsigned tiles = static_cast<unsigned>(a.tile_blocks), few = static_cast<unsigned>(a.few_blocks);
   if (tiles && few) attention_kernel<D, FP8, true, true><<<tiles + few, 256, 0, stream>>>(a);
   else if (tiles) attention_kernel<D, FP8, true, false><<<tiles, 256, 0, stream>>>(a);
-  else attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
+  else if (few) attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
   if (a.splits > 1 || (a.few_pieces > 0 && a.few_splits != 1)) {
     // four waves a row for many chunks, as long as the rows are few (a step of
     // chunks and decodes, 7220 rows of mostly three chunks: 84 us with four, 79
@@ -1368,8 +1373,12 @@ void launch(const Args& a, hipStream_t stream) {
 
 }  // namespace
 
+// Enough for either mask: the plan depends on it, the callers' query does not.
 int64_t attention_workspace(const AttnCall& c) {
-  return plan_of(c).slots * (c.d + 2) * 4;
+  AttnCall other = c;
+  other.causal = !c.causal;
+  const int64_t a = plan_of(c).slots, b = plan_of(other).slots;
+  return (a > b ? a : b) * (c.d + 2) * 4;
 }
 
 hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {

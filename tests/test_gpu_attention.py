@@ -227,6 +227,44 @@ def test_paged_offsets_past_32_bits():
     check(got, reference([(q64, k64, v64)], d ** -0.5, True, 0, d, False), "far pages")
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_paged_workspace_fits_every_mask(seed):
+    """One workspace query serves causal and full masks, windows or none:
+    chunks whose keys are cut differently by each."""
+    rng = np.random.default_rng(100 + seed)
+    new = int(rng.integers(20, 400))
+    lens = [(new, new + int(rng.integers(0, 1500)))]
+    if seed % 2:
+        lens.append((1, int(rng.integers(1, 2500))))
+    d, window = (64, 128, 256)[seed % 3], (0, 300, 900)[seed // 3 % 3]
+    fp8, causal = bool(seed & 1), seed % 4 != 3
+    _say("workspace", lens, d, window, fp8, causal)
+    *call, kw, parts = build(rng, lens, 2, 1, d, 16, fp8, "head")
+    check(nv.paged_attention(*call, causal=causal, window=window, **kw),
+          reference(parts, d ** -0.5, causal, window, d, fp8), seed)
+
+
+def test_nothing_to_attend_to():
+    """Tokens that belong to no request, bounds of zero: nothing is written."""
+    _say("bounds of zero")
+    q = torch.zeros(3, 34, 64, dtype=torch.bfloat16, device=DEV)
+    cache = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16, device=DEV)
+    table = i32([[0]])
+    for heads in (34, 2):
+        out = torch.full((3, heads, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        nv.paged_attention(q[:, :heads], cache, cache, table, i32([0, 0]), i32([0]), 0, 0, out=out)
+        nv.prompt_attention(q[:, :heads], q[:, :2], q[:, :2], i32([0, 0]), 0, out=out)
+        assert (out == 7).all()
+    many = i32([0] * 301)
+    out = torch.full((3, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    nv.paged_attention(q[:, :2], cache, cache, i32([[0]] * 300), many, many[:300], 0, 0, out=out)
+    assert (out == 7).all()
+    out = nv.paged_attention(q[:, :2], cache, cache, table, i32([0, 3]), i32([0]), 3, 0)
+    assert not out.any()
+    empty = nv.paged_attention(q[:0, :2], cache, cache, table, i32([0, 0]), i32([0]), 0, 0)
+    assert empty.shape == (0, 2, 64)
+
+
 def test_paged_page_out_of_range_reads_zeros():
     _say("page out of range")
     rng = np.random.default_rng(7)
