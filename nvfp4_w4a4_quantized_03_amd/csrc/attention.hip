@@ -45,6 +45,7 @@
 
 #include "internal.h"
 #include "kv_device.h"
+#include "kv_place.h"
 
 namespace nvfp4 {
 namespace {
@@ -446,25 +447,20 @@ __device__ __forceinline__ int page_of(const Args& a, const int32_t* row_of_tabl
   return ((cptr)row_of_table)[a.page.div(static_cast<unsigned>(key))];
 }
 
-// Where `rows` keys from `key` on (of one 16-key group) are, and which of them
-// may be read: rows outside [lo, hi) are read at the nearest one inside, so
-// that whatever a cache holds past a request's end is never used.  A page
+// Where the ROWS keys from `key` on (of one 16-key group) are, and which of
+// them may be read: rows outside [lo, hi) are read at the nearest one inside,
+// so that whatever a cache holds past a request's end is never used.  A page
 // out of range reads as zeros.
 struct Place {
   const uint8_t* k;
   const uint8_t* v;
-  int first, end;
+  RowBounds rows;
 };
-template <int ROWS>
-__device__ __forceinline__ int group_at(const Span& s, int key) {
-  const int last = (s.hi - 1) & ~(ROWS - 1);
-  return key < last ? key : last;
-}
 template <int ROWS>
 __device__ __forceinline__ Place place_of(const Args& a, const Span& s, int64_t head_k,
                                           int64_t head_v, int key, int id) {
-  const int g = group_at<ROWS>(s, key);
-  Place p = {a.k + head_k, a.v + head_v, s.lo - g, s.hi - 1 - g};
+  const int g = group_at<ROWS>(s.hi, key);
+  Place p = {a.k + head_k, a.v + head_v, rows_seen(s.lo, s.hi, g)};
   if (a.table) {
     const int off = g - static_cast<int>(a.page.div(static_cast<unsigned>(g)) * a.page.d);
     if (id >= 0 && id < a.n_pages) {
@@ -473,7 +469,7 @@ __device__ __forceinline__ Place place_of(const Args& a, const Span& s, int64_t 
       p.v += at;
     } else {
       p.k = p.v = reinterpret_cast<const uint8_t*>(kZeros);
-      p.first = p.end = 0;               // every row at the one of zeros
+      p.rows = {0, 0};                   // every row at the one of zeros
     }
   } else {
     p.k += (static_cast<int64_t>(s.token0) + g) * a.k_token;
@@ -494,12 +490,11 @@ struct Stage {
     const uint8_t* base = IS_V ? p.v : p.k;
     const int r0 = lane / T::kChunks, c0 = lane % T::kChunks;
     constexpr int kStep = 64 / T::kChunks;        // rows from one load to the next
-    // the clamp on byte offsets: no multiplication per load
-    const int first = p.first * stride, end = p.end * stride;
+    const ByteBounds bytes = bytes_seen(p.rows, stride);
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < T::kLoads; ++i)
-        x[i] = load16b<false>(base, min(max(r0 * stride + i * kStep * stride, first), end) + c0 * 16);
+        x[i] = load16b<false>(base, byte_of(r0 * stride + i * kStep * stride, bytes) + c0 * 16);
     } else {
       // LDS takes consecutive lanes' pieces one after another; which chunk of
       // the row a lane brings makes the exchange
@@ -509,7 +504,7 @@ struct Stage {
         const int r = wave * T::kRows % 16 + r0 + i * kStep;
         const int c = c0 ^ (IS_V ? T::v_swap(r) : T::k_swap(r));
         lds_load16(rsrc, lds + (wave * T::kLoads + i) * 1024,
-                   min(max(r0 * stride + i * kStep * stride, first), end) + c * 16);
+                   byte_of(r0 * stride + i * kStep * stride, bytes) + c * 16);
       }
     }
   }
@@ -698,7 +693,7 @@ __device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>
   Stage<D, FP8, true> xv;
   int id = 0;                             // page of this wave's rows of the next tile
   auto look_up = [&](int key0) {
-    if (table) id = page_of(a, table, group_at<T::kRows>(s, key0 + wave * T::kRows));
+    if (table) id = page_of(a, table, group_at<T::kRows>(s.hi, key0 + wave * T::kRows));
   };
   auto place = [&](int key0) {
     return place_of<T::kRows>(a, s, head_k, head_v, key0 + wave * T::kRows, id);
@@ -888,15 +883,15 @@ struct Stream {
 #pragma unroll
     for (int p = 0; p < 2; ++p) at[p] = place_of<16>(a, s, head_k, head_v, key0 + 16 * p, ids[p]);
   }
-  __device__ __forceinline__ static int inside(int r, int first, int end) {
-    r = r < first ? first : r;
-    return r > end ? end : r;
+  __device__ __forceinline__ static int inside(int r, const RowBounds& b) {
+    r = r < b.first ? b.first : r;
+    return r > b.end ? b.end : r;
   }
   __device__ __forceinline__ void load_k() {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const int row = inside(lane & 15, at[p].first, at[p].end) * kt + (lane >> 4) * 16;
+      const int row = inside(lane & 15, at[p].rows) * kt + (lane >> 4) * 16;
 #pragma unroll
       for (int i = 0; i < kK; ++i) k[p][i] = load16b<true>(at[p].k, row + i * 64);
     }
@@ -907,7 +902,7 @@ struct Stream {
     for (int i = 0; i < kV; ++i) {
       const int p = i * 64 / kChunks / 16;                  // a load lies in one group
       const int r = (i * 64 + lane) / kChunks - 16 * p, c = (i * 64 + lane) % kChunks;
-      v[i] = load16b<true>(at[p].v, inside(r, at[p].first, at[p].end) * vt + c * 16);
+      v[i] = load16b<true>(at[p].v, inside(r, at[p].rows) * vt + c * 16);
     }
   }
   // The 8 rows that 32 lanes of a transposing read touch differ by 32 bytes.
@@ -1002,7 +997,7 @@ __device__ __forceinline__ void few_rows(const Args& a, const Cut& cut, int piec
   auto look_up = [&](int key0) {
     if (!table) return;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) ids[p] = page_of(a, table, group_at<16>(s, key0 + 16 * p));
+    for (int p = 0; p < 2; ++p) ids[p] = page_of(a, table, group_at<16>(s.hi, key0 + 16 * p));
   };
   int key0 = begin + wave * S::kKeys;
   constexpr int kStride = 4 * S::kKeys;

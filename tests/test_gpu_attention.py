@@ -429,3 +429,97 @@ def test_graph_replays():
         assert torch.equal(got, out)
         cut = [(q, k[:len(k) - shorter], v[:len(v) - shorter]) for q, k, v in parts]
         check(got, reference(cut, 128 ** -0.5, True, 0, 128, True), shorter)
+
+
+def wide_pool(pages, kv_heads, page, d, fp8, stride):
+    """A cache whose tokens are `stride` elements apart, K and V columns of
+    one buffer full of NaN."""
+    mem = torch.empty(pages * page, stride, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+    mem.fill_(0x7F if fp8 else float("nan"))
+    return tuple(mem.as_strided((pages, kv_heads, page, d), (page * stride, d, stride, 1),
+                                i * kv_heads * d) for i in range(2))
+
+
+@pytest.mark.parametrize("d,fp8,stride", [
+    # the widest accepted token strides: the last multiple of 16 bytes below 2^26
+    (64, False, (1 << 25) - 8), (128, False, (1 << 25) - 8), (256, False, (1 << 25) - 8),
+    (64, True, (1 << 26) - 16), (128, True, (1 << 26) - 16), (256, True, (1 << 26) - 16)])
+def test_paged_widest_token_stride(d, fp8, stride):
+    """Keys times token stride past 2^31 and 2^32 bytes, for a chunk (tiles of
+    rows), a decode and a windowed chunk: the bits of the same cache packed."""
+    _say("widest token stride", d, fp8, stride)
+    rng = np.random.default_rng(d)
+    lens, heads, kv_heads, page = [(50, 100), (1, 39), (17, 34)], 4, 2, 16
+    size = 1 if fp8 else 2
+    assert 33 * stride * size > 2 ** 31 and 65 * stride * size > 2 ** 32
+    qd, kc, vc, table, cu, kv, mn, mk, kw, parts = build(rng, lens, heads, kv_heads, d, page, fp8,
+                                                         "head")
+    wide = wide_pool(kc.shape[0], kv_heads, page, d, fp8, stride)
+    for w, c in zip(wide, (kc, vc)):
+        w.copy_(c)
+    for causal, window in ((True, 0), (True, 21), (False, 0)):
+        packed = nv.paged_attention(qd, kc, vc, table, cu, kv, mn, mk, causal=causal,
+                                    window=window, **kw)
+        check(packed, reference(parts, d ** -0.5, causal, window, d, fp8), (causal, window))
+        got = nv.paged_attention(qd, *wide, table, cu, kv, mn, mk, causal=causal, window=window,
+                                 **kw)
+        assert torch.equal(got.view(torch.int16), packed.view(torch.int16)), (causal, window)
+
+
+def test_write_widest_token_stride():
+    """The page write into such a cache."""
+    _say("write, widest token stride")
+    rng = np.random.default_rng(12)
+    wide = wide_pool(3, 2, 16, 64, True, (1 << 26) - 16)
+    kd, vd = (bf16(rng.standard_normal((40, 2, 64)))[1] for _ in range(2))
+    packed = tuple(torch.full((3, 2, 16, 64), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(2))
+    scale = torch.full((1,), 0.01, device=DEV)
+    slots = torch.from_numpy(rng.permutation(48)[:40]).to(DEV)
+    for cache in (wide, packed):
+        nv.kv_page_write(kd, vd, *cache, slots, scale, scale)
+    assert torch.equal(wide[0], packed[0]) and torch.equal(wide[1], packed[1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_widest_token_stride(d):
+    """Rows of keys and values as far apart as the prompt form takes them."""
+    _say("prompt, widest token stride", d)
+    rng = np.random.default_rng(d + 1)
+    lens, heads, kv_heads, stride = [80, 3, 17], 4, 2, (1 << 25) - 8
+    n = sum(lens)
+    x64, x = bf16(rng.standard_normal((n, heads + 2 * kv_heads, d)))
+    q, k, v = x[:, :heads], x[:, heads:heads + kv_heads], x[:, heads + kv_heads:]
+    mem = torch.full((n, stride), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide = tuple(mem.as_strided((n, kv_heads, d), (stride, d, 1), i * kv_heads * d)
+                 for i in range(2))
+    wide[0].copy_(k)
+    wide[1].copy_(v)
+    cu = [0]
+    for a in lens:
+        cu.append(cu[-1] + a)
+    for causal, window in ((True, 0), (True, 21), (False, 0)):
+        packed = nv.prompt_attention(q, k, v, i32(cu), max(lens), causal=causal, window=window)
+        parts = [(x64[a:b, :heads], x64[a:b, heads:heads + kv_heads], x64[a:b, heads + kv_heads:])
+                 for a, b in zip(cu, cu[1:])]
+        check(packed, reference(parts, d ** -0.5, causal, window, d, False), (causal, window))
+        got = nv.prompt_attention(q, *wide, i32(cu), max(lens), causal=causal, window=window)
+        assert torch.equal(got.view(torch.int16), packed.view(torch.int16)), (causal, window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_chunk_offsets_past_32_bits(fp8):
+    """Pages more than 2^32 bytes into the cache, read by tiles of rows."""
+    _say("chunk, offsets past 32 bits", fp8)
+    rng = np.random.default_rng(13)
+    kv_heads, d, page, pages = 1, 128, 16, 2200000
+    *call, kw, parts = build(rng, [(20, 75)], 4, kv_heads, d, page, fp8, "head")
+    qd, kc, vc, table, cu, kv, mn, mk = call
+    far = tuple(torch.empty(pages, kv_heads, page, d, dtype=kc.dtype, device=DEV) for _ in range(2))
+    assert far[0].numel() * far[0].element_size() > 2 ** 32
+    ids = [pages - 1, 0, pages - 2, 1, pages - 5]
+    for b, p in enumerate(ids):
+        for f, c in zip(far, (kc, vc)):
+            f[p] = c[int(table[0, b])]
+    table[0, :5] = i32(ids)
+    got = nv.paged_attention(qd, *far, table, cu, kv, mn, mk, **kw)
+    check(got, reference(parts, d ** -0.5, True, 0, d, fp8), "far pages")
