@@ -44,6 +44,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "kv_cut.h"
 #include "kv_device.h"
 #include "kv_place.h"
 
@@ -160,10 +161,9 @@ __device__ __forceinline__ Span span_of(const Args& a, int r, int row0, int rows
   return s;
 }
 
-// Chunks that the keys of a tile are cut into.
+// Chunks that the keys of a span are cut into.
 __device__ __forceinline__ int splits_of(const Span& s, int chunk, int most) {
-  const int n = (s.hi - s.start + chunk - 1) / chunk;
-  return n < 1 ? 1 : n > most ? most : n;
+  return chunks_of(s.hi - s.start, chunk, most);
 }
 
 // Places of a chunk's sums: of a row of a tile, of a row of a few-row request.
@@ -176,15 +176,12 @@ __device__ __forceinline__ int64_t few_slot(const Args& a, int piece, int kvh, i
 }
 
 // How the keys of the requests of few rows are cut into pieces of equal
-// length, a request's pieces one after another.  Up to kPlanned requests the
-// cut follows the lengths (a pass over them, 64 at a time, by every wave):
-// one piece of the average work for each of kFewSlots workgroups when all
-// are alike (32 requests of 32768 E4M3 keys of 4 heads of 256: 325 us; with
-// 2048 keys a piece 353 us), down to a quarter of it when they differ (64
-// requests of 1 to 16384 keys: 92 us with 2048 keys a piece, 80 us with
-// 1024, 116 us with 4096), never less than few_least keys.
+// length (kv_cut.h), a request's pieces one after another.  Up to kPlanned
+// requests the cut follows the lengths (a pass over them, 64 at a time, by
+// every wave): 32 requests of 32768 E4M3 keys of 4 heads of 256 take 325 us,
+// with 2048 keys a piece 353 us; 64 requests of 1 to 16384 keys 77 us, with
+// 2048 keys a piece 92 us, 1024 80 us, 4096 116 us.
 constexpr int kPlanned = 256;
-constexpr int kFewSlots = 512;
 constexpr int few_least(int d) { return d == 64 ? 256 : 512; }
 struct Cut {
   int chunk, pieces;
@@ -260,25 +257,14 @@ __device__ __forceinline__ Cut cut_of(const Args& a) {
   total = wave_sum(total);
   most = wave_max(most);
   n = wave_sum(n);
-  const float uneven = fminf(n * most / fmaxf(total, 1.0f), 4.0f);
-  const float want = total * static_cast<float>(a.n_kv_heads) / (kFewSlots * fmaxf(uneven, 1.0f));
-  // rounded up to whole tiles of the four waves (at least `want`, which is
-  // what bounds the number of pieces)
-  c.chunk = (static_cast<int>(fminf(want, 0x1p30f)) + 128) & -128;
-  c.chunk = __builtin_amdgcn_readfirstlane(c.chunk > few_least(D) ? c.chunk : few_least(D));
+  c.chunk = __builtin_amdgcn_readfirstlane(piece_keys(total, most, n, a.n_kv_heads, few_least(D)));
   const float per_key = 1.0f / static_cast<float>(c.chunk);
   int before = 0;
 #pragma unroll
   for (int q = 0; q < kPlanned / 64; ++q) {
     c.first[q] = before;
     if (q * 64 >= a.n_requests) continue;
-    int count = keys[q] < 0 ? 0 : 1;
-    if (keys[q] > c.chunk) {
-      // ceil(keys / chunk), the quotient in binary32 put right
-      count = static_cast<int>(static_cast<float>(keys[q]) * per_key);
-      while (static_cast<int64_t>(count) * c.chunk < keys[q]) ++count;
-      while (static_cast<int64_t>(count - 1) * c.chunk >= keys[q]) --count;
-    }
+    const int count = keys[q] < 0 ? 0 : pieces_of(keys[q], c.chunk, per_key);
     const int sums = lane_sums(count);
     c.first[q] = before + sums - count;
     before += __builtin_amdgcn_readlane(sums, 63);
@@ -1329,9 +1315,7 @@ Plan plan_of(const AttnCall& c) {
       if (p.few_chunk < least) p.few_chunk = least;
       p.few_splits = p.few_pieces = (keys + p.few_chunk - 1) / p.few_chunk;
     } else if (c.n_requests <= kPlanned && keys > least) {
-      // kFewSlots pieces at most four times over, and a last one a request
-      // (and one for the binary32 of the kernel's division)
-      p.few_pieces = c.n_requests + (4 * kFewSlots + c.n_kv_heads - 1) / c.n_kv_heads + 1;
+      p.few_pieces = pieces_bound(c.n_requests, c.n_kv_heads);
     } else {
       // short keys are not cut; of very many requests only long ones are
       p.few_splits = c.n_requests <= kPlanned ? 1 : (keys + kLongest - 1) / kLongest;
