@@ -1242,9 +1242,17 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kCus = 256;
-// keys of a piece where requests are too many to be planned by the kernel:
-// they even out by number, and only a request far longer than most is cut
+// Requests too many to be planned by the kernel even out by number, and only
+// those far longer than most are cut: pieces of at least kLongest keys, at most
+// kMostPieces (of a request and a head) by the bound of the lengths, so that
+// neither the empty ones nor the workspace grow with it.  257 requests of
+// 1000 E4M3 keys, 8 heads of 128, called with a bound of 131072: 98 us
+// and 49 MiB, with pieces of 4096 keys however many that makes 261 us and 522 MiB;
+// one of 131072 keys among 256 of 2048: 525 and 537 us, with half of
+// kMostPieces 1269 us, with twice as many 346 us (but 512 requests of 4
+// heads of 256, one of them of 65536: 559, 961, 643 and 957 us).
 constexpr int64_t kLongest = 4096;
+constexpr int64_t kMostPieces = 8192;
 
 struct Plan {
   int64_t tiles, splits, chunk;           // tiles == 0: no request of many rows
@@ -1319,7 +1327,7 @@ Plan plan_of(const AttnCall& c) {
     } else {
       // short keys are not cut; of very many requests only long ones are
       p.few_splits = c.n_requests <= kPlanned ? 1 : (keys + kLongest - 1) / kLongest;
-      const int64_t most = (int64_t(1) << 21) / (c.n_requests * c.n_kv_heads);
+      const int64_t most = kMostPieces / (c.n_requests * c.n_kv_heads);
       if (p.few_splits > most) p.few_splits = most;
       if (p.few_splits < 1) p.few_splits = 1;
       p.few_chunk = ((keys + p.few_splits - 1) / p.few_splits + 127) / 128 * 128;

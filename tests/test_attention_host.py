@@ -289,3 +289,21 @@ def test_oracle_tables_by_hand():
     assert kv.tolist() == [34, 3] and used == 2
     assert pos.tolist() == list(range(20, 34)) + [0, 1, 2, -1]
     assert slots.tolist() == [9 * 16 + i for i in range(4, 16)] + [112, 113] + [32, 33, 34, -1]
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(40, 8, 128), (20, 4, 256), (16, 16, 64),
+                                              (40, 40, 128), (8, 1, 64), (16, 1, 256)])
+@pytest.mark.parametrize("most", [600, 32768, 131072, 1 << 20])
+def test_decode_workspace_is_bounded(lib, heads, kv_heads, d, most):
+    """The sums of cut decodes take no more places, whatever the number of
+    requests and the bound of their lengths, than 8192 pieces of 16 rows, or
+    where the kernel cuts by the lengths (256 requests) than those pieces; and
+    a 257th request does not multiply them."""
+    def need(n):
+        return lib.kv_paged_attention_workspace(n, heads, kv_heads, d, n, 1, most, 0)
+    row = (d + 2) * 4
+    for n in (257, 300, 512, 1000, 2048, 4096, 10000):
+        assert need(n) <= 8192 * 16 * row, n
+        assert need(n) <= 4 * max(need(256), 1 << 20), n
+    for n in (2, 5, 32, 100, 255, 256):
+        assert need(n) <= (n * kv_heads + 2048 + 2 * kv_heads) * 16 * row, n

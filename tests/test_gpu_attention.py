@@ -523,3 +523,17 @@ def test_paged_chunk_offsets_past_32_bits(fp8):
     table[0, :5] = i32(ids)
     got = nv.paged_attention(qd, *far, table, cu, kv, mn, mk, **kw)
     check(got, reference(parts, d ** -0.5, True, 0, d, fp8), "far pages")
+
+
+@pytest.mark.parametrize("n,kv_heads,d,fp8", [(300, 2, 64, True), (1100, 4, 64, False),
+                                              (2100, 4, 128, True)])
+def test_paged_more_requests_than_planned(n, kv_heads, d, fp8):
+    """Requests cut by the bound of their lengths, far above the lengths
+    themselves, and so many that none is cut."""
+    _say("more requests than planned", n, kv_heads, d, fp8)
+    rng = np.random.default_rng(n)
+    lens = [(1, int(b)) for b in rng.integers(1, 40, n)]
+    lens[1], lens[n // 2], lens[n - 1] = (0, 30), (1, 2500), (2, 700)
+    *call, kw, parts = build(rng, lens, 2 * kv_heads, kv_heads, d, 16, fp8, "head")
+    call[-1] = 150000
+    check(nv.paged_attention(*call, **kw), reference(parts, d ** -0.5, True, 0, d, fp8), n)

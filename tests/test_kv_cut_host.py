@@ -55,7 +55,7 @@ int main() {
   std::mt19937_64 rng(7);
   const int mosts[] = {1, 300, 513, 5000, 32768, 131072, 1 << 24, (1 << 24) + 1, 1 << 30,
                        (1 << 30) + 129, 0x7FFFFFFF - 65536};
-  const int counts[] = {1, 2, 3, 63, 64, 65, 200, 255, 256};
+  const int counts[] = {1, 2, 3, 63, 64, 65, 200, 255, 256, 257, 700, 1023, 1024};
   for (int least : {256, 512})
     for (int kv_heads : {1, 2, 3, 4, 8, 16, 40, 64, 1024, 65536})
       for (int n : counts)
