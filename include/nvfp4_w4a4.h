@@ -389,7 +389,8 @@ int kv_page_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,
  *   cu_new, kv_lens  device, as kv_page_tables makes them (non-decreasing,
  *                cu_new[n_requests] <= n_tokens, kv_lens <= max_blocks *
  *                page_size).
- *   max_new, max_kv  host: upper bounds of the new lengths and of kv_lens.
+ *   max_new, max_kv  host: upper bounds of the new lengths and of kv_lens (a
+ *                request beyond them may be left unwritten or cut off).
  *   scale        factor of the scores, finite and > 0 (1 / sqrt(d)).
  *   causal       nonzero: a token at position p sees the keys at <= p; zero:
  *                every key of its request.

@@ -64,7 +64,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTileRows = 128;         // rows of a workgroup, 32 a wave
-constexpr int kFewRows = 16;           // rows of a request that few_rows takes
+constexpr int kFewRows = 16;           // most rows of a request that few_rows takes
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -92,10 +92,11 @@ struct Args {
   int max_kv, causal, window, tiles;
   int tile_blocks;                                // workgroups of the tiles
   int splits, chunk;                              // chunks of the tiles' keys
-  // requests of few rows (few_pieces: 0, none): most pieces that their keys
-  // are cut into; keys of a piece and pieces of a request, or 0 for a cut
-  // that the kernel makes from the lengths; workgroups
-  int few_pieces, few_chunk, few_splits, few_blocks;
+  // requests of few rows (few_pieces: 0, none): most rows of one (and places
+  // of a piece's sums), most pieces that their keys are cut into; keys of a
+  // piece and pieces of a request, or 0 for a cut that the kernel makes from
+  // the lengths; workgroups
+  int few_rows, few_pieces, few_chunk, few_splits, few_blocks;
 };
 
 __device__ __forceinline__ int clampi(int64_t x, int64_t lo, int64_t hi) {
@@ -172,7 +173,7 @@ __device__ __forceinline__ int64_t tile_slot(const Args& a, int split, int64_t t
 }
 __device__ __forceinline__ int64_t few_slot(const Args& a, int piece, int kvh, int row) {
   const int64_t before = a.splits > 1 ? tile_slot(a, a.splits, 0, 0) : 0;
-  return before + (static_cast<int64_t>(piece) * a.n_kv_heads + kvh) * kFewRows + row;
+  return before + (static_cast<int64_t>(piece) * a.n_kv_heads + kvh) * a.few_rows + row;
 }
 
 // How the keys of the requests of few rows are cut into pieces of equal
@@ -246,7 +247,7 @@ __device__ __forceinline__ Cut cut_of(const Args& a) {
     if (i < a.n_requests) {
       const Span s = span_of(a, i, 0, kFewRows);
       const int64_t rows = static_cast<int64_t>(s.n_new) * a.group.d;
-      if (rows > 0 && rows <= kFewRows) {
+      if (rows > 0 && rows <= a.few_rows) {
         keys[q] = s.hi - s.start;
         total += static_cast<float>(keys[q]);
         most = fmaxf(most, static_cast<float>(keys[q]));
@@ -319,7 +320,7 @@ __device__ __forceinline__ bool tile_of(const Args& a, int index, int* r, int* l
     if (q * 64 >= a.n_requests) continue;
     if (q * 64 + lane < a.n_requests) {
       const int64_t rows = rows_of(a, q * 64 + lane);
-      if (!(a.few_pieces > 0 && rows <= kFewRows))
+      if (!(a.few_pieces > 0 && rows <= a.few_rows))
         tiles[q] = static_cast<int>((rows + kTileRows - 1) / kTileRows);
     }
     most = max(most, tiles[q]);
@@ -626,7 +627,7 @@ __device__ __forceinline__ void tile_rows(const Args& a, int block, const Lds<D>
   const int64_t row0 = static_cast<int64_t>(level) * kTileRows;
   const int group = static_cast<int>(a.group.d);
   const int64_t n_rows = rows_of(a, r);
-  if (row0 >= n_rows || (a.few_pieces > 0 && n_rows <= kFewRows)) return;
+  if (row0 >= n_rows || (a.few_pieces > 0 && n_rows <= a.few_rows)) return;
   const Span s = span_of(a, r, static_cast<int>(row0), kTileRows);
   const int splits = splits_of(s, a.chunk, a.splits);
   if (split >= splits) return;
@@ -946,7 +947,7 @@ __device__ __forceinline__ void few_rows(const Args& a, const Cut& cut, int piec
   const int group = static_cast<int>(a.group.d);
   const Span s = span_of(a, r, 0, kFewRows);
   const int64_t n_rows = static_cast<int64_t>(s.n_new) * group;
-  if (n_rows < 1 || n_rows > kFewRows) return;
+  if (n_rows < 1 || n_rows > a.few_rows) return;
   const int splits = splits_of(s, cut.chunk, a.few_chunk ? a.few_splits : 0x7FFFFFFF);
   if (split >= splits) return;
   const int begin = s.start + split * cut.chunk;
@@ -1146,7 +1147,8 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a) {
   if (t < token0 || t >= token1) return;             // a row of no request
   const int kvh = static_cast<int>(a.group.div(static_cast<unsigned>(head)));
   const int in_request = (t - token0) * group + head - kvh * group;
-  const bool few = a.few_pieces > 0 && static_cast<int64_t>(token1 - token0) * group <= kFewRows;
+  const bool few = a.few_pieces > 0 && static_cast<int64_t>(token1 - token0) * group <= a.few_rows;
+  if (!few && a.tiles == 0) return;                  // more new tokens than the caller's bound
   int splits;
   int64_t at, step;
   if (few) {
@@ -1246,18 +1248,18 @@ constexpr int64_t kCus = 256;
 // those far longer than most are cut: pieces of at least kLongest keys, at most
 // kMostPieces (of a request and a head) by the bound of the lengths, so that
 // neither the empty ones nor the workspace grow with it.  257 requests of
-// 1000 E4M3 keys, 8 heads of 128, called with a bound of 131072: 98 us
-// and 49 MiB, with pieces of 4096 keys however many that makes 261 us and 522 MiB;
-// one of 131072 keys among 256 of 2048: 525 and 537 us, with half of
-// kMostPieces 1269 us, with twice as many 346 us (but 512 requests of 4
-// heads of 256, one of them of 65536: 559, 961, 643 and 957 us).
+// 1000 E4M3 keys, 5 rows, 8 heads of 128, called with a bound of 131072: 98
+// us and 15 MiB in 6168 pieces, 261 us and 163 MiB in pieces of kLongest keys
+// however many that makes.  One of 131072 keys among 256 of 2048: 525 us,
+// uncut 1269 us, twice as many pieces 346 us (but 512 requests of 4 heads of
+// 256, one of them of 65536 keys: 559 us, twice as many pieces 957 us).
 constexpr int64_t kLongest = 4096;
 constexpr int64_t kMostPieces = 8192;
 
 struct Plan {
   int64_t tiles, splits, chunk;           // tiles == 0: no request of many rows
   // few_pieces == 0: none of few rows; few_chunk == 0: cut by the kernel
-  int64_t few_pieces, few_chunk, few_splits;
+  int64_t few_rows, few_pieces, few_chunk, few_splits;
   int64_t slots;                          // places of chunks' sums
 };
 
@@ -1315,6 +1317,7 @@ Plan plan_of(const AttnCall& c) {
     cut_tiles(c, group, &p);
   }
   if (few) {
+    p.few_rows = many ? kFewRows : c.max_new * group;
     const int64_t keys = span_keys(c, kFewRows), least = few_least(static_cast<int>(c.d));
     if (c.n_requests == 1 && keys > least) {
       // its length is the bound: enough pieces for every CU
@@ -1336,7 +1339,7 @@ Plan plan_of(const AttnCall& c) {
     }
   }
   if (p.splits > 1) p.slots += p.splits * c.n_tokens * c.n_heads;
-  if (p.few_splits != 1) p.slots += p.few_pieces * c.n_kv_heads * kFewRows;
+  if (p.few_splits != 1) p.slots += p.few_pieces * c.n_kv_heads * p.few_rows;
   return p;
 }
 
@@ -1410,6 +1413,7 @@ hipError_t launch_attention(const AttnCall& c, hipStream_t stream) {
   a.splits = static_cast<int>(p.splits);
   a.tile_blocks = static_cast<int>(p.tiles * p.splits * c.n_kv_heads);
   a.chunk = static_cast<int>(p.chunk);
+  a.few_rows = static_cast<int>(p.few_rows);
   a.few_pieces = static_cast<int>(p.few_pieces);
   a.few_chunk = static_cast<int>(p.few_chunk);
   a.few_splits = static_cast<int>(p.few_splits);

@@ -307,3 +307,16 @@ def test_decode_workspace_is_bounded(lib, heads, kv_heads, d, most):
         assert need(n) <= 4 * max(need(256), 1 << 20), n
     for n in (2, 5, 32, 100, 255, 256):
         assert need(n) <= (n * kv_heads + 2048 + 2 * kv_heads) * 16 * row, n
+
+
+@pytest.mark.parametrize("heads,kv_heads,d,new", [
+    (40, 40, 128, 1), (40, 40, 128, 3), (40, 40, 128, 16), (40, 8, 128, 1), (40, 8, 128, 3),
+    (16, 16, 64, 1), (16, 16, 64, 16), (16, 1, 256, 1)])
+def test_decode_workspace_holds_rows_that_exist(lib, heads, kv_heads, d, new):
+    """A piece has places for the rows that its request can have, not for the
+    most that the kernel takes at once."""
+    rows = new * heads // kv_heads
+    for n in (1, 2, 100, 256, 257):
+        pieces = max(n * kv_heads + 2048 + 2 * kv_heads, 8192 if n > 256 else 0)
+        assert lib.kv_paged_attention_workspace(n * new, heads, kv_heads, d, n, new, 131072, 0) <= \
+            pieces * rows * (d + 2) * 4, n

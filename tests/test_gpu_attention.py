@@ -537,3 +537,32 @@ def test_paged_more_requests_than_planned(n, kv_heads, d, fp8):
     *call, kw, parts = build(rng, lens, 2 * kv_heads, kv_heads, d, 16, fp8, "head")
     call[-1] = 150000
     check(nv.paged_attention(*call, **kw), reference(parts, d ** -0.5, True, 0, d, fp8), n)
+
+
+@pytest.mark.parametrize("n,heads,kv_heads,new", [(5, 6, 6, 1), (3, 6, 6, 5), (40, 6, 2, 1),
+                                                  (2, 16, 1, 1), (1, 7, 7, 2), (270, 3, 1, 2)])
+def test_paged_places_of_few_rows(n, heads, kv_heads, new):
+    """Cut keys of requests of 1 to 16 rows: each piece's sums in places of
+    their own, none past the workspace (the bytes behind it stay)."""
+    _say("places of few rows", n, heads, kv_heads, new)
+    rng = np.random.default_rng(n + heads)
+    lens = [(int(a), int(b)) for a, b in zip(rng.integers(1, new + 1, n), rng.integers(1, 50, n))]
+    lens[0], lens[n - 1] = (new, 4400), (new, 3000)
+    qd, kc, vc, table, cu, kv, mn, mk, kw, parts = build(rng, lens, heads, kv_heads, 64, 16, False,
+                                                         "head")
+    want = reference(parts, 0.125, True, 0, 64, False)
+    tokens, lib = qd.shape[0], nv.library()
+    size = lib.kv_paged_attention_workspace(tokens, heads, kv_heads, 64, n, mn, mk, 0)
+    assert size > 0
+    work = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(qd)
+    torch.cuda.synchronize()
+    p = [t.data_ptr() for t in (qd, kc, vc, table, cu, kv, out, work)]
+    rc = lib.kv_paged_attention(
+        p[0], qd.stride(0), qd.stride(1), tokens, heads, p[1], p[2], nv.DTYPE_BF16, kc.shape[0], 16,
+        kv_heads, 64, kc.stride(0), kc.stride(1), kc.stride(2), None, None, p[3], table.shape[1],
+        table.stride(0), p[4], p[5], n, mn, mk, 0.125, 1, 0, p[6], out.stride(0), out.stride(1),
+        p[7], size, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    check(out, want, n)
+    assert (work[size:] == 0xA5).all()
