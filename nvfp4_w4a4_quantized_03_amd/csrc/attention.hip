@@ -308,8 +308,9 @@ __device__ __forceinline__ bool tile_of(const Args& a, int index, int* r, int* l
   if (a.n_requests > kPlanned) {
     const int tile = a.tiles - 1 - index;
     *r = __builtin_amdgcn_readfirstlane(find_request<false>(a, tile));
+    // tiles before the first request's, where the offsets do not begin at 0
     *level = static_cast<int>(tile - first_tile(a, *r));
-    return true;
+    return *level >= 0;
   }
   constexpr int kQ = kPlanned / 64;
   const int lane = threadIdx.x & 63;

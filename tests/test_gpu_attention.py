@@ -566,3 +566,28 @@ def test_paged_places_of_few_rows(n, heads, kv_heads, new):
     assert rc == 0
     check(out, want, n)
     assert (work[size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_offsets_that_begin_past_zero(n):
+    """Some of a step's requests: offsets that do not begin at row 0 nor end
+    at the last one; the rows of the others are not written."""
+    _say("offsets past zero", n)
+    rng = np.random.default_rng(n + 1)
+    lens = [(int(a), int(a + b)) for a, b in zip(rng.integers(0, 12, n), rng.integers(0, 40, n))]
+    lens[0], lens[n - 1] = (20, 33), (140, 150)
+    qd, kc, vc, table, cu, kv, mn, mk, kw, parts = build(rng, lens, 4, 2, 64, 16, False, "head")
+    before, after = 700, 300
+    q = torch.full((before + qd.shape[0] + after, 4, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    q[before:-after] = qd
+    out = torch.full_like(q, 7.0)
+    nv.paged_attention(q, kc, vc, table, cu + before, kv, mn, mk, out=out, **kw)
+    check(out[before:-after], reference(parts, 0.125, True, 0, 64, False), "paged")
+    assert (out[:before] == 7).all() and (out[-after:] == 7).all()
+    x64, x = bf16(rng.standard_normal((q.shape[0], 8, 64)))
+    out.fill_(7.0)
+    nv.prompt_attention(x[:, :4], x[:, 4:6], x[:, 6:], cu + before, mn, out=out)
+    at = (cu + before).tolist()
+    parts = [(x64[a:b, :4], x64[a:b, 4:6], x64[a:b, 6:]) for a, b in zip(at, at[1:])]
+    check(out[before:-after], reference(parts, 0.125, True, 0, 64, False), "prompt")
+    assert (out[:before] == 7).all() and (out[-after:] == 7).all()
