@@ -357,7 +357,9 @@ int kv_page_tables(const int32_t* new_lens, const int32_t* cached_lens,
  *                * d < 2^35.
  *   k_scale, v_scale  device floats (finite, >= 0) for E4M3, else ignored.
  *   slots        device, [n_tokens]; a slot outside [0, n_pages * page_size)
- *                is skipped.  Equal slots: one of the tokens is kept.
+ *                is skipped.  The others must differ: of two tokens with one
+ *                slot, parts of either may be kept (K and V each for itself,
+ *                16 elements at a time).
  * BF16 rounds to nearest even; E4M3 codes are those of fp8_kv_cast.
  * n_tokens >= 0 (0 does nothing).
  */
@@ -407,7 +409,9 @@ int kv_page_write(const void* k, int64_t k_token_stride, int64_t k_head_stride,
  * sums in binary32 and one final rounding; the weights enter the second
  * matrix product rounded to bf16 (BF16 cache) or fp16 (E4M3 cache).  Only
  * keys that some row of the call sees are used: what pages hold past a
- * request's end, or before its window, is never used.
+ * request's end, or before its window, is never used.  Those that some row
+ * sees should be finite: an infinity or NaN among the values of a key that
+ * other rows of a request see may make a row NaN that does not see it.
  */
 int kv_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                        int64_t n_tokens, int64_t n_heads, const void* k_cache,

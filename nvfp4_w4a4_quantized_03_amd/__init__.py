@@ -603,8 +603,8 @@ def kv_page_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None):
     views of a fused projection's output are fine); k_cache, v_cache:
     [n_pages, n_kv_heads, page_size, d], bfloat16, or uint8 E4M3 codes under
     the static scales (float32 [1], fp8_kv_calibrate); any order of the first
-    three axes in memory.  slots: int64 [n_tokens]; one outside the cache is
-    skipped."""
+    three axes in memory.  slots: int64 [n_tokens], each a different one; one
+    outside the cache is skipped."""
     dtype = getattr(k, "dtype", None)
     if dtype == torch.bfloat16:
         dt = DTYPE_BF16
@@ -654,7 +654,8 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_new, kv_lens, max_new,
     bounds of the new lengths and of kv_lens.  scale defaults to
     1 / sqrt(d).  window > 0: a token sees the last `window` positions only,
     itself included.  Returns [n_tokens, n_heads, d] bfloat16 (or fills
-    out)."""
+    out).  Rows of no request (padding past cu_new's end) are not written: in a
+    new output they hold whatever the memory held."""
     qp = _head_rows(q, "q")
     dev = q.device
     tokens, heads, d = q.shape
