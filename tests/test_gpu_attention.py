@@ -591,3 +591,66 @@ def test_offsets_that_begin_past_zero(n):
     parts = [(x64[a:b, :4], x64[a:b, 4:6], x64[a:b, 6:]) for a, b in zip(at, at[1:])]
     check(out[before:-after], reference(parts, 0.125, True, 0, 64, False), "prompt")
     assert (out[:before] == 7).all() and (out[-after:] == 7).all()
+
+
+@pytest.mark.parametrize("new,kv,window,fp8", [
+    (1, 70001, 0, False), (1, 70001, 50003, True), (3, 66000, 0, True), (3, 66000, 40001, False),
+    (60, 40007, 0, False), (60, 40007, 30001, True), (200, 33333, 0, True),
+    (200, 33333, 20011, False)])
+def test_masks_to_the_key(new, kv, window, fp8):
+    """Long contexts, queries of zero, so that every visible key weighs exactly
+    the same, and values of zero but for 64 marks of 1 at an edge of the mask,
+    each in an element of its own: a row gives 1 / (keys it sees) at the marks
+    it sees, within the bf16 rounding (2^-8, and 2^-22 for the division), and
+    zero at the others."""
+    _say("masks to the key", new, kv, window, fp8)
+    d, page, kv_heads, heads = 64, 16, 2, 4
+    rng = np.random.default_rng(new + kv)
+    cols = -(-kv // page)
+    k_cache, v_cache = pool(rng, cols + 2, kv_heads, page, d, fp8, "head")
+    table = torch.full((1, cols), -1, dtype=torch.int32, device=DEV)
+    step = nv.kv_page_tables(i32([kv]), i32([0]), table, i32(rng.permutation(cols + 2).tolist()),
+                             page, kv)
+    one = torch.ones(1, device=DEV) if fp8 else None
+    q = torch.zeros(new, heads, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.randn(kv, kv_heads, d, device=DEV).to(torch.bfloat16)
+    rows = np.arange(kv - new, kv)
+    first = np.maximum(rows - window + 1, 0) if window else np.zeros_like(rows)
+    edges = [kv - 64, min(kv - new - 32, kv - 64)] + ([int(first[0]) - 32, int(first[-1]) - 32] if window
+                                                 else [0])
+    for edge in edges:
+        v = torch.zeros(kv, kv_heads, d, dtype=torch.bfloat16, device=DEV)
+        for e in range(64):
+            v[edge + e, :, e] = 1.0
+        nv.kv_page_write(k, v, k_cache, v_cache, step.slots, one, one)
+        got = nv.paged_attention(q, k_cache, v_cache, table, i32([0, new]), step.kv_lens, new, kv,
+                                 window=window, k_scale=one, v_scale=one).double().cpu().numpy()
+        at = edge + np.arange(64)
+        sees = (at[None] <= rows[:, None]) & (at[None] >= first[:, None])
+        want = np.where(sees, 1.0 / (rows - first + 1)[:, None], 0.0)[:, None]
+        assert np.all(np.abs(got - want) <= want * (2.0 ** -8 + 2.0 ** -22)), edge
+        assert np.all(got[np.broadcast_to(~sees[:, None], got.shape)] == 0.0), edge
+
+
+@pytest.mark.parametrize("n,causal,window", [(9000, True, 0), (9000, True, 5003), (5000, False, 0),
+                                             (5000, False, 1777)])
+def test_prompt_masks_to_the_key(n, causal, window):
+    """The same in a prompt, with marks at four places."""
+    _say("prompt masks to the key", n, causal, window)
+    d, heads, kv_heads = 64, 2, 1
+    q = torch.zeros(n, heads, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.randn(n, kv_heads, d, device=DEV).to(torch.bfloat16)
+    rows = np.arange(n)
+    first = np.maximum(rows - window + 1, 0) if window else np.zeros_like(rows)
+    last = rows if causal else np.full(n, n - 1)
+    for edge in (0, 1000, n // 2 + 1, n - 64):
+        v = torch.zeros(n, kv_heads, d, dtype=torch.bfloat16, device=DEV)
+        for e in range(64):
+            v[edge + e, :, e] = 1.0
+        got = nv.prompt_attention(q, k, v, i32([0, n]), n, causal=causal,
+                                  window=window).double().cpu().numpy()
+        at = edge + np.arange(64)
+        sees = (at[None] <= last[:, None]) & (at[None] >= first[:, None])
+        want = np.where(sees, 1.0 / (last - first + 1)[:, None], 0.0)[:, None]
+        assert np.all(np.abs(got - want) <= want * (2.0 ** -8 + 2.0 ** -22)), edge
+        assert np.all(got[np.broadcast_to(~sees[:, None], got.shape)] == 0.0), edge
