@@ -183,6 +183,10 @@ __device__ __forceinline__ int64_t few_slot(const Args& a, int piece, int kvh, i
 // with 2048 keys a piece 353 us; 64 requests of 1 to 16384 keys 77 us, with
 // 2048 keys a piece 92 us, 1024 80 us, 4096 116 us.
 constexpr int kPlanned = 256;
+// Fewest keys of a piece.  A small call is bound by its launches, so the choice
+// shows little: d 64, 256 or 512 keys: within 1 us from 1 to 256 requests
+// (1024: 43 instead of 36 us for 64 ragged ones of up to 4000); d 256, 256 or 512
+// keys: 19 and 21 us for 8 requests of 2000 keys, 26 and 23 us for 32 of 1000.
 constexpr int few_least(int d) { return d == 64 ? 256 : 512; }
 struct Cut {
   int chunk, pieces;
@@ -297,9 +301,10 @@ __device__ __forceinline__ int request_of(const Args& a, const Cut& c, int piece
 // is.  Up to kPlanned requests the tiles come by their place in the request,
 // the last ones first: under a causal mask those have the most keys, and a
 // long tile that starts late would end alone (7 prompts of up to 2001 tokens,
-// d 256: 103 us in the requests' order, 100 us in this one; 16 requests of 5
-// speculated tokens: 31.5 and 29 us).  With S(p) = sum_r max(0, tiles_r - p) tiles at places >= p, tile `index` is at
-// the largest p with S(p) > index.
+// d 256: 102 us in the requests' order, 99 us in this one; 3 chunks and 21
+// decodes: 82 and 79 us; 16 requests of 5 tokens over 8192 keys: the same).
+// With S(p) = sum_r max(0, tiles_r - p) tiles at places >= p, tile `index` is
+// at the largest p with S(p) > index.
 __device__ __forceinline__ int64_t rows_of(const Args& a, int r) {
   const int t0 = clampi(a.cu[r], 0, a.n_tokens);
   return static_cast<int64_t>(clampi(a.cu[r + 1], t0, a.n_tokens) - t0) * a.group.d;
@@ -549,14 +554,15 @@ __device__ __forceinline__ void order() {
   __builtin_amdgcn_sched_group_barrier(KIND, N, 0);
 }
 
-// The weights are 2^(c s - m + kLift) with a bound m that may be up to kSlack
-// below the largest score: it is moved, and the sums with it, only when a
-// score passes it by more.  fp16 weights (next to E4M3 values) are lifted
-// away from fp16's subnormals; 2^14 is still in its range.
+// The weights are 2^(c s - m) with a bound m that may be up to kSlack below
+// the largest score: it is moved, and the sums with it, only when a score
+// passes it by more.  fp16 weights (next to E4M3 values) are lifted away from
+// fp16's subnormals, 2^(c s - m + kLift); 2^14 is still in its range.
 constexpr float kSlack = 8.0f;
+constexpr float kLift = 6.0f;
 template <bool FP8>
 __device__ __forceinline__ float shift_of(float m) {
-  return (m == kNegInf ? 0.0f : m) - (FP8 ? 6.0f : 0.0f);
+  return (m == kNegInf ? 0.0f : m) - (FP8 ? kLift : 0.0f);
 }
 // Raises m to top; returns the factor of the sums so far.
 __device__ __forceinline__ float moved(float* m, float top) {
@@ -600,11 +606,11 @@ struct Lds {
 // at every D, so that one's exponentials run under another's products; D =
 // 256 (128 registers of sums, 64 of queries) affords that with tiles of 32
 // keys: 8192 tokens of 20 heads of 256 in 640 us (1.07 PFLOP/s), with one
-// wave a SIMD 900 us.  A 16384-token prompt of 40 heads of 128 takes 2.58 ms
-// (1.06 PFLOP/s, 43 % of the matrix peak): the matrix cores are busy 56 % of
-// the cycles and the vector units 51 %, and the clock is held at 1.8 GHz by
-// power, so what is left is energy and not idle time.  Measured and not
-// taken there: 64 rows a wave (half the LDS reads, but one wave a SIMD: 3.1
+// wave a SIMD 900 us.  A 16384-token prompt of 40 heads of 128 takes 2.53 ms
+// (1.09 PFLOP/s, 43 % of the matrix peak and 73 % of what a large library
+// product reaches): the matrix cores are busy 57 % of the cycles and the
+// vector units 53 %, at a clock of 1.8 GHz, so products and exponentials mostly
+// take turns and hardly run side by side.  Measured and not taken there: 64 rows a wave (half the LDS reads, but one wave a SIMD: 3.1
 // ms), scores of the next tile taken under the exponentials of this one
 // within a wave (3.0 ms, no registers left to read ahead), 32-key tiles at
 // three waves a SIMD (2.55 ms; E4M3 chunks cut in two lose 6 %), raised wave
@@ -1276,10 +1282,14 @@ int64_t span_keys(const AttnCall& c, int64_t tokens) {
 // Chunks of the tiles' keys by their estimated time.  Two workgroups fit a
 // CU, so `tiles` of them run in rounds of 512; a last round of less than
 // half takes about 0.62 of one (a workgroup alone on its CU is faster).
-// Cutting the keys evens the rounds out (2048 new tokens of 40 heads over
-// 32001 keys, 1.25 rounds: 1.60 ms uncut, 1.40 ms cut in two) but writes and
-// reads each chunk's sums (7 prompts of up to 2001 tokens: 121 us uncut, 203
-// us cut in two).  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.
+// Cutting the keys evens the rounds out but writes and reads each chunk's
+// sums.  Uncut, in 2, 3 and 4 chunks, with what the estimate takes in brackets:
+// 2048 tokens of 40 heads over 32001 E4M3 keys, 1.25 rounds: 1556, 1362,
+// [1388], 1338 us; the same over bf16 keys: 1438, 1297, [1324], 1302; 512
+// tokens over 16384 keys: 311, 233, [187], 215; 3 chunks and 21 decodes: 194, 118,
+// 88, [79]; 7 prompts of up to 2001 tokens: [99], 151, 128, 192; a prompt of
+// 16384: [2526], 3599, 2990, 4239; 8192 tokens, all keys: [1277], 1423, 1490,
+// 1544.  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.
 void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
   const int64_t keys = span_keys(c, kTileRows / group + 2);
   const double wgs = (static_cast<double>(c.n_tokens) * group / kTileRows + 0.5 * c.n_requests) *
@@ -1351,9 +1361,13 @@ void launch(const Args& a, hipStream_t stream) {
   else if (tiles) attention_kernel<D, FP8, true, false><<<tiles, 256, 0, stream>>>(a);
   else if (few) attention_kernel<D, FP8, false, true><<<few, 256, 0, stream>>>(a);
   if (a.splits > 1 || (a.few_pieces > 0 && a.few_splits != 1)) {
-    // four waves a row for many chunks, as long as the rows are few (a step of
-    // chunks and decodes, 7220 rows of mostly three chunks: 84 us with four, 79
-    // with one)
+    // four waves a row for many chunks, as long as the rows are few: one request
+    // of 6000 keys (20 rows, d 256) 18 us with four and 20 with one, 64 ragged
+    // ones of up to 4000 (1024 rows, d 64) 36 and 38 us, 256 of 1500 (10240
+    // rows, d 128) 158 and 138 us.  Between about 2000 rows and the bound one
+    // wave is the faster too (200 ragged requests, 3200 to 8000 rows: by 4 to
+    // 18 %).  A step of chunks and decodes, 7220 rows of mostly three chunks,
+    // takes one: 79 us, with four 84
     const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.n_heads;
     if ((!tiles || a.splits > 8) && rows <= 8192)
       combine_kernel<D, FP8, 4><<<static_cast<unsigned>(rows), 256, 0, stream>>>(a);

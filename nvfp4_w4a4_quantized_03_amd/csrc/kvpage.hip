@@ -18,8 +18,9 @@
 //
 // Write.  One lane per 16 elements of a token's K or V row (16 or 32 bytes
 // stored), consecutive lanes on consecutive elements: HBM-bound (32768 tokens
-// of 4 heads of 256, bf16 to E4M3: 38 us, 5.3 TB/s; 32 tokens: 3.8 us, a
-// launch).  The FP8 form is the exact cast of fp8kv.hip.  Measured and not
+// of 4 heads of 256, bf16 to E4M3: 38 us, 5.3 TB/s; float32 to E4M3: 64 us,
+// 5.2 TB/s; float32 to bf16: 81 us, 5.0 TB/s; bf16 to bf16: 57 us, 4.7 TB/s;
+// 32 tokens: 3.8 us, a launch).  The FP8 form is the exact cast of fp8kv.hip.  Measured and not
 // taken: cached stores (42 us), K and V of a group by one lane (40 us).
 #include <hip/hip_runtime.h>
 
