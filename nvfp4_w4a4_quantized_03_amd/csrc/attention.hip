@@ -1289,7 +1289,12 @@ int64_t span_keys(const AttnCall& c, int64_t tokens) {
 // tokens over 16384 keys: 311, 233, [187], 215; 3 chunks and 21 decodes: 194, 118,
 // 88, [79]; 7 prompts of up to 2001 tokens: [99], 151, 128, 192; a prompt of
 // 16384: [2526], 3599, 2990, 4239; 8192 tokens, all keys: [1277], 1423, 1490,
-// 1544.  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.
+// 1544.  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.  Cut workgroups
+// fill at most kMostRounds rounds, which bounds the workspace: beyond that the
+// rounds are even enough and only the sums are left (8192 tokens over 32768
+// keys, 5 rounds: 4.46 ms uncut, 4.80 in 2 and 5.1 in 6 chunks; over 131072 keys:
+// 19.9, 20.8 and 21.7 ms, with 975 MiB of sums).
+constexpr double kMostRounds = 7.0;
 void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
   const int64_t keys = span_keys(c, kTileRows / group + 2);
   const double wgs = (static_cast<double>(c.n_tokens) * group / kTileRows + 0.5 * c.n_requests) *
@@ -1301,7 +1306,7 @@ void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
   const double sums_us = static_cast<double>(c.n_tokens) * c.n_heads * c.d * 8.0 / 4e6;
   double best = 0.0;
   int64_t splits = 1;
-  for (int64_t n = 1; n <= 16 && (n == 1 || (keys >= 256 * n && wgs < 16.0 * kCus)); ++n) {
+  for (int64_t n = 1; n <= 16 && (n == 1 || (keys >= 256 * n && wgs * n <= 2.0 * kCus * kMostRounds)); ++n) {
     const double r = wgs * n / (2.0 * kCus), full = floor(r);
     const double rounds = graded && r > 1.0 ? r : full + (r - full > 0.5 ? 1.0 : r > full ? 0.62 : 0.0);
     const double us = round_us * rounds / n + (n > 1 ? 6.0 + n * sums_us : 0.0);

@@ -320,3 +320,13 @@ def test_decode_workspace_holds_rows_that_exist(lib, heads, kv_heads, d, new):
         pieces = max(n * kv_heads + 2048 + 2 * kv_heads, 8192 if n > 256 else 0)
         assert lib.kv_paged_attention_workspace(n * new, heads, kv_heads, d, n, new, 131072, 0) <= \
             pieces * rows * (d + 2) * 4, n
+
+
+@pytest.mark.parametrize("heads,kv_heads,d", [(40, 8, 128), (20, 4, 256), (16, 16, 64), (64, 1, 128)])
+@pytest.mark.parametrize("most", [32768, 131072, 1 << 20])
+def test_chunk_workspace_is_bounded(lib, heads, kv_heads, d, most):
+    """The sums of cut chunks take the rows of seven rounds of 512 tiles at
+    most, whatever the number of new tokens and the length of the context."""
+    for new in (17, 64, 300, 700, 1500, 2048, 3000, 3500, 4096, 6000, 7000, 8192, 10000, 13000, 16384):
+        need = lib.kv_paged_attention_workspace(new, heads, kv_heads, d, 1, new, most, 0)
+        assert 0 <= need <= 7 * 512 * 128 * (d + 2) * 4, new
