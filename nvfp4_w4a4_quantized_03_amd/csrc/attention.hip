@@ -1292,8 +1292,10 @@ int64_t span_keys(const AttnCall& c, int64_t tokens) {
 // 1544.  Rates: 1 PFLOP/s, 4 TB/s for the sums, 6 us a launch.  Cut workgroups
 // fill at most kMostRounds rounds, which bounds the workspace: beyond that the
 // rounds are even enough and only the sums are left (8192 tokens over 32768
-// keys, 5 rounds: 4.46 ms uncut, 4.80 in 2 and 5.1 in 6 chunks; over 131072 keys:
-// 19.9, 20.8 and 21.7 ms, with 975 MiB of sums).
+// keys, 5 rounds: 4.46 ms uncut, 4.80 in 2 and 5.0 in 3 chunks; over 131072
+// keys 19.9 ms uncut, 20.8 in 2 and 21.7 in 6, with 975 MiB of sums).  3500
+// tokens over 65536 keys, 2.1 rounds: 4.90 ms uncut, 4.65 in the 3 chunks that
+// this still allows.
 constexpr double kMostRounds = 7.0;
 void cut_tiles(const AttnCall& c, int64_t group, Plan* p) {
   const int64_t keys = span_keys(c, kTileRows / group + 2);
