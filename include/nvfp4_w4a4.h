@@ -461,13 +461,122 @@ int64_t prompt_attention_workspace(int64_t n_tokens, int64_t n_heads,
                                    int64_t n_kv_heads, int64_t d, int64_t n_prompts,
                                    int64_t max_len, int64_t window);
 
+/*
+ * MXFP4 tensors (OCP microscaling, 4-bit form): 4-bit E2M1 values, one E8M0
+ * scale 2^(byte - 127) per 32 consecutive elements of a row, no scale per
+ * tensor.  It is the 4-bit format that gfx950's matrix instructions take as it
+ * is stored, next to NVFP4, which they do not.
+ *   codes : uint8 [rows][k/2], packed as NVFP4 codes are.
+ *   scales: uint8 [rows][k/32]; byte 0xFF is NaN.
+ *   Blocks of 32 run along k, the reduction axis of the product.
+ *
+ * mxfp4_quantize -- x [rows][ldx] of x_dtype (F32 or BF16, 16-byte aligned,
+ *   ldx * size a multiple of 16) to codes (16-byte aligned) and scales;
+ *   rows >= 1, k >= 32, k % 32 == 0, ldx >= k.  Per block with the largest
+ *   magnitude m: byte = max(floor(log2 m) - 2, -127) + 127 (0 for m = 0), code
+ *   = sign(x) | E2M1(|x| 2^(127 - byte)), rounded once to nearest, ties to the
+ *   even code, saturating at 6; bit-exact with this for every finite input.  A
+ *   block that holds an infinity or a NaN gets byte 0xFF.  x must not overlap
+ *   the outputs, nor they each other.
+ *
+ * mxfp4_dequantize -- out [rows][ldo] of out_dtype (F32 or BF16, 16-byte
+ *   aligned, ldo * size a multiple of 16) = the values of packed codes
+ *   (16-byte aligned) and scales: exact (two significant bits), infinite where
+ *   scales above those that mxfp4_quantize gives leave the type's range, NaN
+ *   under a byte of 0xFF.
+ *
+ * mxfp4_gemm -- Y = A B^T for A [m][k] and B [n][k] (K-major weights) in the
+ *   layout above; codes and scale arrays 16-byte aligned (else MISALIGNED).
+ *   m, n >= 1, k >= 32, k % 32 == 0; k % 256 == 0 takes the whole-stage
+ *   kernels.  out [m][ldo] of out_dtype (F32 or BF16), ldo >= n, 4-byte
+ *   aligned, no overlap with the inputs.  Products and scales are exact, sums
+ *   are binary32, BF16 is rounded to nearest even from that.  A row with a
+ *   scale byte of 0xFF gives NaN.
+ */
+int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx,
+                   uint8_t* codes, uint8_t* scales, void* stream);
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k,
+                     void* out, int out_dtype, int64_t ldo, void* stream);
+int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+               const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
+               void* out, int out_dtype, int64_t ldo, void* stream);
+
+/*
+ * gdn_attention -- linear attention with a decay for each head, with the delta
+ * rule of a Gated DeltaNet layer ([P3] 前提2) or without it, over the new
+ * tokens of each request: whole prompts, chunks of them, single tokens and
+ * drafts, mixed in one call.  Per request and head, with the state S [dk][dv],
+ * for each token in order:
+ *     S <- alpha S,   u = beta (v - S^T k)   (beta == NULL: u = v),
+ *     S <- S + k u^T, o = scale S^T q.
+ *
+ *   q, k         device, BF16 [n_tokens][n_k_heads][dk]; v BF16 [n_tokens]
+ *                [n_heads][dv]; each with token and head strides in elements
+ *                (columns of a fused projection's output, say), 16-byte
+ *                aligned, strides multiples of 8.
+ *   n_heads      a multiple of n_k_heads; head h reads query and key head
+ *                h / (n_heads / n_k_heads).  n_tokens * n_heads <= 2^27,
+ *                n_requests * n_heads <= 2^20.
+ *   dk, dv       dk 64 or 128; dv a multiple of 16, at most 512 (else
+ *                UNSUPPORTED).
+ *   alpha        device, floats [n_tokens][ld_alpha], ld_alpha >= n_heads: the
+ *                decays, 0 <= alpha <= 1 (w4a4_gemm_gdn_gates makes them).
+ *   beta         device, floats [n_tokens][ld_beta], finite; NULL: the plain
+ *                rule (ld_beta ignored).
+ *   state        device, in/out, floats [n_slots][slot_stride], the first
+ *                n_heads * dk * dv of a slot used as [n_heads][dk][dv]; 16-byte
+ *                aligned, slot_stride a multiple of 4.
+ *   slots        device, [n_requests]: the slot of each request, all different
+ *                (NULL: request r has slot r); a request whose slot is outside
+ *                [0, n_slots) is left out: its rows of out are not written.
+ *   cu_lens      device, [n_requests + 1]: request r's rows are [cu_lens[r],
+ *                cu_lens[r + 1]) (kv_page_tables' cu_new).  Non-decreasing,
+ *                the last <= n_tokens; rows of no request are not written.
+ *                The state of a request without rows is left as it is.
+ *   cached_lens  device, [n_requests], or NULL (all continue): a request with
+ *                cached_lens[r] <= 0 starts from S = 0 and does not read what
+ *                its slot holds.
+ *   max_len      host: upper bound of the lengths (it chooses the kernels;
+ *                longer requests are computed all the same).
+ *   scale        factor of the outputs, finite and > 0 (1 / sqrt(dk)).
+ *   normalize    nonzero: q and k are divided by sqrt(sum x^2 + 1e-6) over
+ *                their dk elements first (the delta rule wants unit keys).
+ *   out          device, out, BF16 [n_tokens][n_heads][dv] with its own
+ *                strides, multiples of 4, 8-byte aligned.
+ *   workspace    device, 16-byte aligned, of the bytes that
+ *                gdn_attention_workspace returns for the same sizes (NULL if
+ *                0); calls in flight together need one each.
+ * out, state and workspace must not overlap each other or an input.
+ *
+ * The state, its sums and the gates' products are binary32; out is rounded
+ * once.
+ */
+int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                  const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                  const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                  int64_t n_tokens, int64_t n_k_heads, int64_t n_heads, int64_t dk,
+                  int64_t dv, const float* alpha, int64_t ld_alpha, const float* beta,
+                  int64_t ld_beta, float* state, int64_t n_slots, int64_t slot_stride,
+                  const int32_t* slots, const int32_t* cu_lens,
+                  const int32_t* cached_lens, int64_t n_requests, int64_t max_len,
+                  float scale, int normalize, void* out, int64_t out_token_stride,
+                  int64_t out_head_stride, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+
+/* Bytes of workspace of gdn_attention for these sizes (delta: whether beta is
+   given); -1 if one of them is out of range.  Host only. */
+int64_t gdn_attention_workspace(int64_t n_tokens, int64_t n_k_heads, int64_t n_heads,
+                                int64_t dk, int64_t dv, int64_t n_requests,
+                                int64_t max_len, int delta);
+
 /* Static text for a status code (never NULL). */
 const char* nvfp4_status_string(int status);
 
 /* ABI version of this header: 3 (1 plus w4a4_gemm_gdn_gates, nvfp4_dequantize,
    nvfp4_error_stats and the fp8_kv_* calls in 2, plus w4a4_gemm_quantize_a
-   in 3).  The paged-cache and attention calls were added to 3 without a
-   change to any earlier call; look their symbols up to find them. */
+   in 3).  The paged-cache and attention calls, the mxfp4_* calls and
+   gdn_attention were added to 3 without a change to any earlier call; look
+   their symbols up to find them. */
 int nvfp4_abi_version(void);
 
 #ifdef __cplusplus

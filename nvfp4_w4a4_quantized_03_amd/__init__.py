@@ -17,6 +17,11 @@ and a GPU, and fails loudly otherwise.
     o = paged_attention(q, k_cache, v_cache, block_table, step.cu_new,
                         step.kv_lens, max_new, max_kv, k_scale=k_scale,
                         v_scale=v_scale)
+
+    m = mxfp4_quantize(x)                  # MXFP4(codes, scales)
+    y = mxfp4_gemm(m, w)                   # the card's own 4-bit product
+    o = gdn_attention(q, k, v, alpha, beta, state, step.cu_new, max_new,
+                      slots, cached_lens, normalize=True)
 """
 import ctypes
 import functools
@@ -30,7 +35,9 @@ __all__ = ["NVFP4", "quantize", "harmonize_group", "gemm", "gemm_quantize_a",
            "dequantize", "fp8_kv_calibrate", "fp8_kv_cast",
            "fake_quantize", "error_stats",
            "KVPages", "kv_page_tables", "kv_page_write", "paged_attention",
-           "prompt_attention", "library",
+           "prompt_attention",
+           "MXFP4", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm",
+           "gdn_attention", "library",
            "LIB_PATH", "NVFP4Error"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -52,6 +59,12 @@ KVPages = namedtuple("KVPages", ["cu_new", "kv_lens", "positions", "slots",
 KVPages.__doc__ = """A serving step's bookkeeping: cu_new int32
 [n_requests + 1], kv_lens int32 [n_requests], positions int32 [n_tokens] and
 slots int64 [n_tokens] (-1: none), pages_used int32 [1]."""
+
+
+MXFP4 = namedtuple("MXFP4", ["codes", "scales"])
+MXFP4.__doc__ = """A packed MXFP4 tensor: codes uint8 [rows, k/2] (element 2j
+in the low nibble of byte j) and scales uint8 [rows, k/32] (E8M0: value =
+e2m1 * 2^(scale - 127))."""
 
 
 class NVFP4Error(RuntimeError):
@@ -115,6 +128,18 @@ def library():
     L.prompt_attention.restype = i32
     L.prompt_attention_workspace.argtypes = [i64] * 7
     L.prompt_attention_workspace.restype = i64
+    L.mxfp4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.mxfp4_quantize.restype = i32
+    L.mxfp4_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    L.mxfp4_dequantize.restype = i32
+    L.mxfp4_gemm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.mxfp4_gemm.restype = i32
+    L.gdn_attention.argtypes = [vp, i64, i64] * 3 + [i64] * 5 + \
+        [vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, ctypes.c_float,
+         i32, vp, i64, i64, vp, i64, vp]
+    L.gdn_attention.restype = i32
+    L.gdn_attention_workspace.argtypes = [i64] * 7 + [i32]
+    L.gdn_attention_workspace.restype = i64
     L.nvfp4_status_string.argtypes = [i32]
     L.nvfp4_status_string.restype = ctypes.c_char_p
     L.nvfp4_abi_version.argtypes = []
@@ -714,4 +739,179 @@ def prompt_attention(q, k, v, cu_lens, max_len, scale=None, causal=True,
         d ** -0.5 if scale is None else scale, 1 if causal else 0, window, *op,
         work.data_ptr() if size > 0 else None, size, _stream(q)),
         "prompt_attention")
+    return out
+
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _call(name, t, *args):
+    """A library call on t's device and that device's current stream."""
+    index = t.get_device()
+    fn = getattr(library(), name)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _stream(t))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream(t))
+    _check(rc, name)
+
+
+def _dtype_of(dtype, name="out_dtype"):
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("%s must be float32 or bfloat16" % name)
+    return dt
+
+
+def _mxfp4_parts(q, name, device=None):
+    """Codes and scales of an MXFP4 operand, checked; rows and k."""
+    codes, scales = q
+    if device is None or not _on(codes, torch.uint8, device.index):
+        _device_tensor(codes, name + ".codes", torch.uint8, device=device)
+    if not _on(scales, torch.uint8, codes.get_device()):
+        _device_tensor(scales, name + ".scales", torch.uint8, device=codes.device)
+    shape, sshape = codes.shape, scales.shape
+    if len(shape) != 2 or len(sshape) != 2 or shape[0] != sshape[0] or \
+            shape[1] != sshape[1] * 16 or not codes.is_contiguous() or \
+            not scales.is_contiguous():
+        raise ValueError("%s must be contiguous codes [rows, k/2] and scales "
+                         "[rows, k/32]" % name)
+    return codes, scales, shape[0], shape[1] * 2
+
+
+def _matrix_out(out, rows, cols, dtype, like):
+    """The output matrix, a new one if none is given, and its row stride."""
+    if out is None:
+        return like.new_empty((rows, cols), dtype=dtype), cols
+    _device_tensor(out, "out", dtype, device=like.device)
+    if out.dim() != 2 or out.shape != (rows, cols) or out.stride(1) != 1:
+        raise ValueError("out must be [%d, %d] with unit column stride"
+                         % (rows, cols))
+    return out, out.stride(0) if rows > 1 else cols
+
+
+def mxfp4_quantize(x, out=None):
+    """MXFP4 form of a [rows, k] float32 or bfloat16 GPU tensor (k a multiple
+    of 32): E2M1 codes and one power-of-two scale per 32 elements.
+    out=(codes, scales) supplies the buffers (row slices of a fused weight,
+    say).  Returns MXFP4."""
+    dt, rows, k, ldx = _x_args(x)
+    if out is None:
+        codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
+        scales = x.new_empty((rows, k // 32), dtype=torch.uint8)
+    else:
+        codes, scales = out
+        _device_tensor(codes, "out codes", torch.uint8, device=x.device)
+        _device_tensor(scales, "out scales", torch.uint8, device=x.device)
+        if codes.shape != (rows, k // 2) or scales.shape != (rows, k // 32) \
+                or not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("out buffers have the wrong shape or layout")
+    _call("mxfp4_quantize", x, x.data_ptr(), dt, rows, k, ldx, codes.data_ptr(),
+          scales.data_ptr())
+    return MXFP4(codes, scales)
+
+
+def mxfp4_dequantize(q, out_dtype=torch.bfloat16, out=None):
+    """Values of an MXFP4 tensor q ([rows, k]), exact, as float32 or bfloat16.
+    Returns a [rows, k] GPU tensor (or fills out, which may be a row-strided
+    view)."""
+    codes, scales, rows, k = _mxfp4_parts(q, "q")
+    od = _dtype_of(out_dtype)
+    out, ldo = _matrix_out(out, rows, k, out_dtype, codes)
+    _call("mxfp4_dequantize", codes, codes.data_ptr(), scales.data_ptr(), rows, k,
+          out.data_ptr(), od, ldo)
+    return out
+
+
+def mxfp4_gemm(a, b, out_dtype=torch.bfloat16, out=None):
+    """Y = A B^T for MXFP4 operands a [m, k] and b [n, k] (weights, K-major),
+    on the card's 4-bit matrix instructions: products exact, sums float32.
+    Returns a [m, n] float32 or bfloat16 tensor (or fills out, which may be a
+    row-strided view)."""
+    ac, as_, m, k = _mxfp4_parts(a, "a")
+    bc, bs, n, kb = _mxfp4_parts(b, "b", ac.device)
+    if kb != k:
+        raise ValueError("operand shapes disagree")
+    od = _dtype_of(out_dtype)
+    out, ldo = _matrix_out(out, m, n, out_dtype, ac)
+    _call("mxfp4_gemm", ac, ac.data_ptr(), as_.data_ptr(), m, bc.data_ptr(),
+          bs.data_ptr(), n, k, out.data_ptr(), od, ldo)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _gdn_workspace(*sizes):
+    return library().gdn_attention_workspace(*sizes)
+
+
+def _gates(t, name, device, tokens, heads):
+    """Pointer and row stride of float32 gates [tokens, heads]."""
+    if not _on(t, torch.float32, device.index):
+        _device_tensor(t, name, torch.float32, device=device)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != tokens or shape[1] != heads or \
+            (heads > 1 and stride[1] != 1):
+        raise ValueError("%s must be float32 [n_tokens, n_heads] with unit "
+                         "column stride" % name)
+    return t.data_ptr(), stride[0] if tokens > 1 else heads
+
+
+def gdn_attention(q, k, v, alpha, beta, state, cu_lens, max_len, slots=None,
+                  cached_lens=None, scale=None, normalize=False, out=None):
+    """Linear attention with a decay for each head over the new tokens of each
+    request, with the delta rule of a Gated DeltaNet layer (beta given) or
+    without it (beta None); prompts, chunks and single tokens mix in one call.
+    Per token, with a head's state S [dk, dv]:
+
+        S = alpha S;  u = beta (v - S^T k)  (or v);  S += k u^T;
+        o = scale S^T q
+
+    q, k: bfloat16 GPU tensors [n_tokens, n_k_heads, dk] (dk 64 or 128); v:
+    [n_tokens, n_heads, dv] (dv a multiple of 16, n_heads a multiple of
+    n_k_heads), strided views of a fused projection's output are fine; alpha,
+    beta: float32 [n_tokens, n_heads] as gdn_gates makes them; state: float32
+    [n_slots, n_heads, dk, dv], updated in place (slots may be strided);
+    cu_lens: int32 [n_requests + 1] offsets (KVPages.cu_new); max_len: host
+    upper bound of the lengths; slots: int32 [n_requests], each a different
+    one, None for the first n_requests; one outside the state leaves its
+    request out; cached_lens: int32 [n_requests], a request with 0 starts from
+    an empty state (None: all continue).  scale defaults to 1 / sqrt(dk);
+    normalize divides q and k by sqrt(sum x^2 + 1e-6) first.  Returns
+    [n_tokens, n_heads, dv] bfloat16 (or fills out); rows of no request are not
+    written."""
+    qp = _head_rows(q, "q")
+    dev, shape = q.device, q.shape
+    kp = _head_rows(k, "k", dev, shape=shape)
+    vp = _head_rows(v, "v", dev)
+    tokens, k_heads, dk = shape
+    heads, dv = v.shape[1], v.shape[2]
+    if v.shape[0] != tokens or k_heads < 1 or heads % k_heads != 0:
+        raise ValueError("q and v disagree in tokens, or v's heads are no "
+                         "multiple of q's")
+    ap = _gates(alpha, "alpha", dev, tokens, heads)
+    bp = (None, 0) if beta is None else _gates(beta, "beta", dev, tokens, heads)
+    if not _on(state, torch.float32, dev.index):
+        _device_tensor(state, "state", torch.float32, device=dev)
+    held, stride = state.shape, state.stride()
+    if len(held) != 4 or held[1:] != (heads, dk, dv) or stride[3] != 1 or \
+            stride[2] != dv or (heads > 1 and stride[1] != dk * dv):
+        raise ValueError("state must be float32 [n_slots, n_heads, dk, dv] "
+                         "with contiguous slots")
+    cu = _ints(cu_lens, "cu_lens", torch.int32, dev)
+    n = cu_lens.numel() - 1
+    sl = None if slots is None else _ints(slots, "slots", torch.int32, dev, n)
+    cl = None if cached_lens is None else \
+        _ints(cached_lens, "cached_lens", torch.int32, dev, n)
+    max_len = int(max_len)
+    out, op = _out_rows(out, v)
+    # the workspace is allocated on the current stream and used there only
+    size = _gdn_workspace(tokens, k_heads, heads, dk, dv, n, max_len,
+                          beta is not None)
+    work = q.new_empty(size, dtype=torch.uint8) if size > 0 else None
+    _call("gdn_attention", q, *qp, *kp, *vp, tokens, k_heads, heads, dk, dv, *ap,
+          *bp, state.data_ptr(), held[0],
+          stride[0] if held[0] > 1 else heads * dk * dv, sl, cu, cl, n, max_len,
+          dk ** -0.5 if scale is None else scale, 1 if normalize else 0, *op,
+          work.data_ptr() if size > 0 else None, size)
     return out

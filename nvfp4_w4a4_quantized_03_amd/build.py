@@ -27,7 +27,7 @@ DEVICE = ["-x", "hip", "--offload-arch=" + ARCH,
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = ["quantize.hip", "harmonize.hip", "gemm.hip", "gemm_stream.hip",
            "dequantize.hip", "fp8kv.hip", "kvpage.hip", "attention.hip",
-           "api.cpp"]
+           "mxfp4.hip", "mxfp4_gemm.hip", "gdn.hip", "api.cpp"]
 
 
 def _compile(src):

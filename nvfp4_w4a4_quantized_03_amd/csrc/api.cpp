@@ -132,6 +132,37 @@ int run_attention(const nvfp4::AttnCall& c, int64_t workspace_bytes, void* strea
   return status_of(nvfp4::launch_attention(c, static_cast<hipStream_t>(stream)));
 }
 
+// Codes and scales of an MXFP4 tensor [rows][k].
+int check_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k) {
+  if (!codes || !scales) return NVFP4_ERR_INVALID_VALUE;
+  if (rows < 1 || k < 32 || k % 32 != 0 || k > kMaxDim || rows > kMaxDim / k)
+    return NVFP4_ERR_INVALID_VALUE;
+  return NVFP4_OK;
+}
+
+// A dense [rows][ld] tensor of F32 or BF16 with 16-byte aligned rows.
+int check_dense(const void* p, int dtype, int64_t rows, int64_t k, int64_t ld) {
+  if (!p || ld < k || ld > kMaxDim || rows > kMaxDim / ld) return NVFP4_ERR_INVALID_VALUE;
+  if (dtype != NVFP4_DTYPE_F32 && dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(p, 16) || (ld * (dtype == NVFP4_DTYPE_F32 ? 4 : 2)) % 16 != 0)
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+// Sizes of a gdn_attention call.
+int check_gdn(const nvfp4::GdnCall& c) {
+  constexpr int64_t kInt = 0x7FFFFFFF;
+  if (c.n_tokens < 0 || c.n_k_heads < 1 || c.n_heads < 1 || c.n_heads % c.n_k_heads != 0 ||
+      c.n_heads > (1 << 16) || c.n_requests < 1 || c.max_len < 0 || c.max_len > kInt || c.dk < 1 ||
+      c.dv < 1)
+    return NVFP4_ERR_INVALID_VALUE;
+  // a launch has fewer than 2^32 threads
+  if (c.n_tokens > (int64_t(1) << 27) / c.n_heads || c.n_requests > (int64_t(1) << 20) / c.n_heads)
+    return NVFP4_ERR_INVALID_VALUE;
+  if ((c.dk != 64 && c.dk != 128) || c.dv % 16 != 0 || c.dv > 512) return NVFP4_ERR_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -149,7 +180,9 @@ const char* nvfp4_status_string(int status) {
              "or a shape outside the call's kernels (gate pair: more than 256 "
              "columns or k not a multiple of 128; fused quantise + GEMM: more "
              "than 64 rows or k not a multiple of 128; paged cache: page size "
-             "not a multiple of 16; attention: d not 64, 128 or 256)";
+             "not a multiple of 16; attention: d not 64, 128 or 256; "
+             "gdn_attention: dk not 64 or 128, dv not a multiple of 16 or "
+             "above 512)";
     case NVFP4_ERR_MISALIGNED:
       return "NVFP4_ERR_MISALIGNED: a pointer or row stride breaks the "
              "required alignment";
@@ -582,6 +615,138 @@ int prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_strid
   if (st != NVFP4_OK) return st;
   if (!aligned(cu_lens, 4)) return NVFP4_ERR_MISALIGNED;
   return run_attention(c, workspace_bytes, stream);
+}
+
+int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx,
+                   uint8_t* codes, uint8_t* scales, void* stream) {
+  int st = check_mxfp4(codes, scales, rows, k);
+  if (st != NVFP4_OK) return st;
+  st = check_dense(x, x_dtype, rows, k, ldx);
+  if (st != NVFP4_OK) return st;
+  if (!aligned(codes, 16)) return NVFP4_ERR_MISALIGNED;
+  const int64_t xbytes = ((rows - 1) * ldx + k) * (x_dtype == NVFP4_DTYPE_F32 ? 4 : 2);
+  const int64_t cbytes = rows * (k / 2), sbytes = rows * (k / 32);
+  if (overlap(x, xbytes, codes, cbytes) || overlap(x, xbytes, scales, sbytes) ||
+      overlap(codes, cbytes, scales, sbytes))
+    return NVFP4_ERR_INVALID_VALUE;
+  return status_of(nvfp4::launch_mxfp4_quantize(x, x_dtype, rows, k, ldx, codes, scales,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t k,
+                     void* out, int out_dtype, int64_t ldo, void* stream) {
+  int st = check_mxfp4(codes, scales, rows, k);
+  if (st != NVFP4_OK) return st;
+  st = check_dense(out, out_dtype, rows, k, ldo);
+  if (st != NVFP4_OK) return st;
+  if (!aligned(codes, 16)) return NVFP4_ERR_MISALIGNED;
+  const int64_t obytes = ((rows - 1) * ldo + k) * (out_dtype == NVFP4_DTYPE_F32 ? 4 : 2);
+  if (overlap(out, obytes, codes, rows * (k / 2)) || overlap(out, obytes, scales, rows * (k / 32)))
+    return NVFP4_ERR_INVALID_VALUE;
+  return status_of(nvfp4::launch_mxfp4_dequantize(codes, scales, rows, k, out, out_dtype, ldo,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, const uint8_t* b_codes,
+               const uint8_t* b_scales, int64_t n, int64_t k, void* out, int out_dtype,
+               int64_t ldo, void* stream) {
+  int st = check_mxfp4(a_codes, a_scales, m, k);
+  if (st != NVFP4_OK) return st;
+  st = check_mxfp4(b_codes, b_scales, n, k);
+  if (st != NVFP4_OK) return st;
+  if (!out || ldo < n || ldo > kMaxDim || m > kMaxDim / ldo) return NVFP4_ERR_INVALID_VALUE;
+  if (out_dtype != NVFP4_DTYPE_F32 && out_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) ||
+      !aligned(b_scales, 16) || !aligned(out, 4))
+    return NVFP4_ERR_MISALIGNED;
+  const int64_t obytes = ((m - 1) * ldo + n) * (out_dtype == NVFP4_DTYPE_F32 ? 4 : 2);
+  if (overlap(out, obytes, a_codes, m * (k / 2)) || overlap(out, obytes, a_scales, m * (k / 32)) ||
+      overlap(out, obytes, b_codes, n * (k / 2)) || overlap(out, obytes, b_scales, n * (k / 32)))
+    return NVFP4_ERR_INVALID_VALUE;
+  return status_of(nvfp4::launch_mxfp4_gemm(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
+                                            out_dtype, ldo, static_cast<hipStream_t>(stream)));
+}
+
+int64_t gdn_attention_workspace(int64_t n_tokens, int64_t n_k_heads, int64_t n_heads, int64_t dk,
+                                int64_t dv, int64_t n_requests, int64_t max_len, int delta) {
+  nvfp4::GdnCall c = {};
+  static const float given = 0.0f;     // any non-null beta: only its presence counts
+  c.n_tokens = n_tokens; c.n_k_heads = n_k_heads; c.n_heads = n_heads; c.dk = dk; c.dv = dv;
+  c.n_requests = n_requests; c.max_len = max_len; c.beta = delta ? &given : nullptr;
+  return check_gdn(c) == NVFP4_OK ? nvfp4::gdn_workspace(c) : -1;
+}
+
+int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                  int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_token_stride, int64_t v_head_stride, int64_t n_tokens,
+                  int64_t n_k_heads, int64_t n_heads, int64_t dk, int64_t dv, const float* alpha,
+                  int64_t ld_alpha, const float* beta, int64_t ld_beta, float* state,
+                  int64_t n_slots, int64_t slot_stride, const int32_t* slots,
+                  const int32_t* cu_lens, const int32_t* cached_lens, int64_t n_requests,
+                  int64_t max_len, float scale, int normalize, void* out,
+                  int64_t out_token_stride, int64_t out_head_stride, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+  nvfp4::GdnCall c = {};
+  c.q = {q, q_token_stride, q_head_stride};
+  c.k = {k, k_token_stride, k_head_stride};
+  c.v = {v, v_token_stride, v_head_stride};
+  c.alpha = alpha; c.ld_alpha = ld_alpha; c.beta = beta; c.ld_beta = ld_beta;
+  c.n_tokens = n_tokens; c.n_k_heads = n_k_heads; c.n_heads = n_heads; c.dk = dk; c.dv = dv;
+  c.state = state; c.n_slots = n_slots; c.slot_stride = slot_stride; c.slots = slots;
+  c.cu = cu_lens; c.cached = cached_lens; c.n_requests = n_requests; c.max_len = max_len;
+  c.scale = scale; c.normalize = normalize != 0;
+  c.out = out; c.out_token = out_token_stride; c.out_head = out_head_stride;
+  c.workspace = workspace;
+  int st = check_gdn(c);
+  if (st != NVFP4_OK) return st;
+  if (!state || !cu_lens || n_slots < 1 || n_slots > kMaxDim || (!slots && n_slots < n_requests))
+    return NVFP4_ERR_INVALID_VALUE;
+  const int64_t held = n_heads * dk * dv;
+  if (slot_stride < held || slot_stride > kMaxDim || n_slots > kMaxDim / slot_stride)
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!(scale > 0.0f) || isinf(scale)) return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(state, 16) || slot_stride % 4 != 0 || !aligned(slots, 4) || !aligned(cu_lens, 4) ||
+      !aligned(cached_lens, 4))
+    return NVFP4_ERR_MISALIGNED;
+  if (n_tokens == 0) return NVFP4_OK;
+  if (!alpha || ld_alpha < n_heads || ld_alpha > kMaxDim || n_tokens > kMaxDim / ld_alpha ||
+      (beta && (ld_beta < n_heads || ld_beta > kMaxDim || n_tokens > kMaxDim / ld_beta)))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (!aligned(alpha, 4) || !aligned(beta, 4)) return NVFP4_ERR_MISALIGNED;
+  st = check_rows(q, n_tokens, q_token_stride, n_k_heads, q_head_stride, dk, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(k, n_tokens, k_token_stride, n_k_heads, k_head_stride, dk, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(v, n_tokens, v_token_stride, n_heads, v_head_stride, dv, 2, 16);
+  if (st != NVFP4_OK) return st;
+  st = check_rows(out, n_tokens, out_token_stride, n_heads, out_head_stride, dv, 2, 8);
+  if (st != NVFP4_OK) return st;
+  const int64_t need = nvfp4::gdn_workspace(c);
+  if (need < 0 || workspace_bytes < need || (need > 0 && !workspace))
+    return NVFP4_ERR_INVALID_VALUE;
+  if (need > 0 && !aligned(workspace, 16)) return NVFP4_ERR_MISALIGNED;
+  struct Range { const void* p; int64_t len; };
+  const Range in[] = {
+      {q, rows_bytes(n_tokens, q_token_stride, n_k_heads, q_head_stride, dk, 2)},
+      {k, rows_bytes(n_tokens, k_token_stride, n_k_heads, k_head_stride, dk, 2)},
+      {v, rows_bytes(n_tokens, v_token_stride, n_heads, v_head_stride, dv, 2)},
+      {alpha, ((n_tokens - 1) * ld_alpha + n_heads) * 4},
+      {beta, beta ? ((n_tokens - 1) * ld_beta + n_heads) * 4 : 0},
+      {slots, slots ? 4 * n_requests : 0},
+      {cu_lens, 4 * (n_requests + 1)},
+      {cached_lens, cached_lens ? 4 * n_requests : 0}};
+  const Range outs[] = {
+      {out, rows_bytes(n_tokens, out_token_stride, n_heads, out_head_stride, dv, 2)},
+      {state, ((n_slots - 1) * slot_stride + held) * 4}, {workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i].len < 1) continue;
+    for (const Range& r : in)
+      if (r.len > 0 && overlap(outs[i].p, outs[i].len, r.p, r.len)) return NVFP4_ERR_INVALID_VALUE;
+    for (int j = i + 1; j < 3; ++j)
+      if (outs[j].len > 0 && overlap(outs[i].p, outs[i].len, outs[j].p, outs[j].len))
+        return NVFP4_ERR_INVALID_VALUE;
+  }
+  return status_of(nvfp4::launch_gdn(c, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -155,4 +155,39 @@ struct AttnCall {
 int64_t attention_workspace(const AttnCall& c);
 hipError_t launch_attention(const AttnCall& c, hipStream_t stream);
 
+// MXFP4 tensors (mxfp4.hip) and their product (mxfp4_gemm.hip).
+hipError_t launch_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx,
+                                 uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                   int64_t k, void* out, int out_dtype, int64_t ldo,
+                                   hipStream_t stream);
+hipError_t launch_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                             const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
+                             void* out, int out_dtype, int64_t ldo, hipStream_t stream);
+
+// Linear attention with a decay per head (gdn.hip): bf16 rows, binary32 gates
+// and states; request r's tokens are rows [cu[r], cu[r + 1]) and its state is
+// that of slots[r] (nullptr: r), empty at the start where cached[r] <= 0.
+struct GdnCall {
+  KvRows q, k, v;
+  const float* alpha;
+  const float* beta;      // nullptr: the plain rule
+  int64_t ld_alpha, ld_beta;
+  int64_t n_tokens, n_k_heads, n_heads, dk, dv;
+  float* state;
+  int64_t n_slots, slot_stride;
+  const int32_t* slots;
+  const int32_t* cu;
+  const int32_t* cached;
+  int64_t n_requests, max_len;
+  float scale;
+  int normalize;
+  void* out;
+  int64_t out_token, out_head;
+  void* workspace;
+};
+// Bytes of workspace that the call needs (the pointers are not read).
+int64_t gdn_workspace(const GdnCall& c);
+hipError_t launch_gdn(const GdnCall& c, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -35,6 +35,8 @@ from .harmonize import harmonize, harmonize_exact
 from .fp8kv import (kv_amax, kv_scale, kv_cast, kv_decode, kv_cast_exact,
                     kv_scale_exact)
 from .attention import attention, page_tables
+from .mxfp4 import mxfp4_quantize, mxfp4_values
+from .gdn import gdn
 from .gemm import (gemm_exact_int, gemm_f64, gemm_f64_rows_cols,
                    gemm_f64_row_blocks, gate_alpha, gate_beta, decoded_units,
                    gdn_gates)
@@ -49,7 +51,7 @@ __all__ = [
     "harmonize", "harmonize_exact",
     "kv_amax", "kv_scale", "kv_cast", "kv_decode", "kv_cast_exact",
     "kv_scale_exact",
-    "attention", "page_tables",
+    "attention", "page_tables", "mxfp4_quantize", "mxfp4_values", "gdn",
     "gemm_exact_int", "gemm_f64", "gemm_f64_rows_cols", "gemm_f64_row_blocks",
     "gate_alpha",
     "gate_beta", "decoded_units", "gdn_gates",

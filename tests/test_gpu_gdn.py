@@ -1,0 +1,274 @@
+"""gdn_attention (through the C ABI) against the float64 oracle.
+
+Tolerances, from norms that the oracle sums without cancellation (its
+docstring): n bounds a state column's norm, w sums what each token rounds, both
+carried by alpha (with unit keys and 0 <= beta <= 1 the delta rule's I - beta k
+k^T does not lengthen an error, so errors are carried by alpha alone).
+
+  state   A token's sums of dk products in binary32 are off by (dk/16 + 6)
+          2^-24 |k| n at most, its products and additions by a few 2^-24 of n
+          and |k| |u|, its normalisation by 8 2^-24: 40 2^-24 (n + |k| |beta
+          v|) a token in all, 40 2^-24 w over the tokens.
+  out     2^-8 |o| for its own rounding; scale |q| times the state's error;
+          40 2^-24 scale |q| n for its own sum.
+Chunks of tokens round operands to two or three bf16 numbers and the outputs'
+operands to one: see the functions below.
+"""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_w4a4_quantized_03_amd as nv
+import oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _say(*a):
+    print("[gpu-gdn]", *a, flush=True)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def build(rng, lens, k_heads, heads, dk, dv, delta=True, spare=2, decay="mixed", pad=0):
+    """Tensors of a call: q, k, v as columns of one projection, slots in a
+    random order, spare slots and padding rows filled with NaN."""
+    n, tokens = len(lens), sum(lens) + pad
+    x = rng.standard_normal((tokens, 2 * k_heads * dk + heads * dv))
+    x[:, :2 * k_heads * dk] += 0.3                         # keys that resemble each other
+    x[sum(lens):] = np.nan
+    x = torch.from_numpy(x).to(BF16).to(DEV)
+    q, k, v = x.split([k_heads * dk, k_heads * dk, heads * dv], 1)
+    rate = {"mixed": np.exp(rng.uniform(np.log(1e-3), np.log(2.0), (1, heads))),
+            "slow": np.full((1, heads), 1e-4), "fast": np.full((1, heads), 8.0),
+            "none": np.zeros((1, heads))}[decay]
+    alpha = np.exp(-rate * np.exp(0.5 * rng.standard_normal((tokens, heads))))
+    if decay == "fast":
+        alpha[rng.random((tokens, heads)) < 0.2] = 0.0     # underflown gates
+    beta = 1 / (1 + np.exp(-2 * rng.standard_normal((tokens, heads))))
+    beta[rng.random((tokens, heads)) < 0.05] = 1.0
+    beta[rng.random((tokens, heads)) < 0.05] = 0.0
+    alpha, beta = (torch.from_numpy(g).to(F32).to(DEV) for g in (alpha, beta))
+    state = torch.full((n + spare, heads, dk, dv), float("nan"), device=DEV)
+    slots = rng.permutation(n + spare)[:n]
+    state[torch.from_numpy(slots).to(DEV)] = torch.from_numpy(
+        rng.standard_normal((n, heads, dk, dv))).to(F32).to(DEV)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    return dict(q=q.view(tokens, k_heads, dk), k=k.view(tokens, k_heads, dk),
+                v=v.view(tokens, heads, dv), alpha=alpha, beta=beta if delta else None,
+                state=state, cu_lens=i32(cu), max_len=max(lens), slots=i32(slots),
+                normalize=delta)
+
+
+def reference(c, held=None, scale=None):
+    """The oracle's answer for every request: [(o, S, size, reach, w)]."""
+    q, k, v, alpha = (c[x].double().cpu().numpy() for x in ("q", "k", "v", "alpha"))
+    beta = None if c["beta"] is None else c["beta"].double().cpu().numpy()
+    state = c["state"].double().cpu().numpy()
+    cu, slots = c["cu_lens"].cpu().numpy(), c["slots"].cpu().numpy()
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    got = []
+    for r in range(len(cu) - 1):
+        a, b = cu[r], cu[r + 1]
+        s0 = state[slots[r]] if held is None or held[r] > 0 else np.zeros(state.shape[1:])
+        o, s, size, (reach, w) = oracle.gdn(q[a:b], k[a:b], v[a:b], alpha[a:b],
+                                            None if beta is None else beta[a:b], s0, scale,
+                                            c["normalize"])
+        got.append((o, s, size, reach, w))
+    return got
+
+
+def tolerances(size, reach, w, o):
+    """(of out, of state): the sums that the file's header derives."""
+    e = 40 * 2.0 ** -24
+    return 1.1 * (2.0 ** -8 * np.abs(o) + e * (reach + size)) + 1e-30, 1.1 * e * w[:, None] + 1e-30
+
+
+def check(c, out, before, want, what):
+    """Outputs and states of a call; slots and rows of no request stay."""
+    cu, slots = c["cu_lens"].cpu().numpy(), c["slots"].cpu().numpy()
+    got, state = out.double().cpu().numpy(), c["state"].double().cpu().numpy()
+    for r, (o, s, size, reach, w) in enumerate(want):
+        if cu[r + 1] == cu[r]:
+            assert torch.equal(c["state"][slots[r]], before[slots[r]]), (what, r)
+            continue
+        t_out, t_state = tolerances(size, reach, w, o)
+        for name, a, b, t in (("out", got[cu[r]:cu[r + 1]], o, t_out),
+                              ("state", state[slots[r]], s, t_state)):
+            assert np.isfinite(a).all(), (what, r, name)
+            off = np.abs(a - b)
+            t = np.broadcast_to(t, off.shape)
+            worst = np.unravel_index(np.argmax(off - t), off.shape)
+            assert (off <= t).all(), (what, r, name, worst, a[worst], b[worst], t[worst])
+    rest = np.setdiff1d(np.arange(len(state)), slots)
+    assert np.isnan(state[rest]).all(), what
+
+
+def run(c, held=None, scale=None, what="", **kw):
+    want = reference(c, held, scale)
+    before = c["state"].clone()
+    if held is not None:
+        # what the slot of a first request holds is never read
+        for r, h in enumerate(held):
+            if h <= 0 and int(c["cu_lens"][r + 1]) > int(c["cu_lens"][r]):
+                c["state"][int(c["slots"][r])] = float("nan")
+    out = nv.gdn_attention(**c, cached_lens=None if held is None else i32(held), scale=scale, **kw)
+    check(c, out, before, want, what)
+    return out
+
+
+@pytest.mark.parametrize("k_heads,heads,dk,dv", [(1, 1, 64, 16), (2, 4, 128, 128), (1, 3, 64, 128),
+                                                 (2, 2, 128, 64), (1, 2, 128, 48), (3, 6, 64, 272)])
+@pytest.mark.parametrize("delta", [True, False])
+def test_single_tokens(k_heads, heads, dk, dv, delta):
+    _say("single", k_heads, heads, dk, dv, delta)
+    rng = np.random.default_rng(heads * dk + dv)
+    run(build(rng, [1] * 5, k_heads, heads, dk, dv, delta))
+
+
+@pytest.mark.parametrize("lens", [[2], [3, 1, 8], [5, 0, 1, 7, 0], [0, 0, 4]])
+@pytest.mark.parametrize("delta", [True, False])
+def test_few_tokens(lens, delta):
+    _say("few", lens, delta)
+    rng = np.random.default_rng(sum(lens))
+    run(build(rng, lens, 2, 4, 128, 64, delta))
+
+
+LENS = [[63], [64], [65], [128], [129, 1, 64], [17, 200, 0, 31, 300], [9, 10, 16, 33]]
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("delta", [True, False])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 48)])
+def test_prompts(lens, delta, dk, dv):
+    _say("prompts", lens, delta, dk, dv)
+    rng = np.random.default_rng(sum(lens) + dk)
+    held = [int(rng.integers(0, 2)) for _ in lens]
+    run(build(rng, lens, 1, 3, dk, dv, delta), held=held)
+
+
+@pytest.mark.parametrize("decay", ["slow", "fast", "none", "mixed"])
+@pytest.mark.parametrize("delta", [True, False])
+def test_decays(decay, delta):
+    """From gates that never forget to gates that underflow to zero."""
+    _say("decay", decay, delta)
+    rng = np.random.default_rng(7)
+    run(build(rng, [150, 1, 70], 2, 4, 128, 64, delta, decay=decay))
+
+
+@pytest.mark.parametrize("delta", [True, False])
+def test_long_prompt(delta):
+    _say("long", delta)
+    rng = np.random.default_rng(11)
+    run(build(rng, [2500], 1, 2, 128, 32, delta, decay="slow"), held=[0])
+
+
+@pytest.mark.parametrize("lens", [[1, 1], [100, 3]])
+def test_first_requests_do_not_read_their_slot(lens):
+    rng = np.random.default_rng(5)
+    run(build(rng, lens, 2, 2, 64, 64), held=[0, 1])
+    run(build(rng, lens, 2, 2, 64, 64), held=[0, 0])
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1], [90, 1, 30]])
+def test_left_out_and_padding(lens):
+    """Requests whose slot is out of range, and rows behind the last request,
+    are neither read nor written."""
+    rng = np.random.default_rng(6)
+    c = build(rng, lens, 2, 4, 128, 64, pad=5)
+    c["slots"][1] = -1
+    out = torch.full_like(c["v"], 3.0)
+    before = c["state"].clone()
+    want = reference(dict(c, slots=c["slots"].clamp(min=0)))
+    nv.gdn_attention(**c, out=out)
+    cu = c["cu_lens"].tolist()
+    assert bool((out[cu[1]:cu[2]] == 3).all()) and bool((out[cu[3]:] == 3).all())
+    got, state = out.double().cpu().numpy(), c["state"].double().cpu().numpy()
+    for r in (0, 2):
+        o, s, size, reach, w = want[r]
+        t_out, t_state = tolerances(size, reach, w, o)
+        assert (np.abs(got[cu[r]:cu[r + 1]] - o) <= t_out).all()
+        assert (np.abs(state[int(c["slots"][r])] - s) <= t_state).all()
+    used = [int(c["slots"][r]) for r in (0, 2)]
+    for i in range(len(state)):
+        if i not in used:
+            assert torch.equal(c["state"][i].isnan(), before[i].isnan()), i
+    c["slots"][0] = len(state)
+    again = torch.full_like(out, 3.0)
+    nv.gdn_attention(**c, out=again)
+    assert bool((again[:cu[1]] == 3).all())
+
+
+@pytest.mark.parametrize("lens", [[1, 1], [3, 130]])
+def test_strides(lens):
+    """Slots inside a larger pool, strided outputs and gates, default slots."""
+    rng = np.random.default_rng(8)
+    c = build(rng, lens, 1, 2, 64, 32)
+    n = len(lens)
+    pool = torch.full((n + 2, 2 * 64 * 32 + 100), float("nan"), device=DEV)
+    held = c["state"][c["slots"].long()].clone()
+    view = pool[:, :2 * 64 * 32].view(n + 2, 2, 64, 32)
+    view[:n] = held
+    gates = torch.zeros(c["alpha"].shape[0], 9, device=DEV)
+    gates[:, 1:3], gates[:, 4:6] = c["alpha"], c["beta"]
+    out = torch.full((c["v"].shape[0], 3, 40), 9.0, dtype=BF16, device=DEV)
+    c.update(state=view, slots=i32(list(range(n))), alpha=gates[:, 1:3], beta=gates[:, 4:6])
+    want = reference(c)
+    c2 = dict(c)
+    del c2["slots"]
+    nv.gdn_attention(**c2, out=out[:, :2, 4:36])
+    cu = c["cu_lens"].tolist()
+    for r in range(n):
+        o, s, size, reach, w = want[r]
+        t_out, t_state = tolerances(size, reach, w, o)
+        assert (np.abs(out[cu[r]:cu[r + 1], :2, 4:36].double().cpu().numpy() - o) <= t_out).all()
+        assert (np.abs(view[r].double().cpu().numpy() - s) <= t_state).all()
+    out[:, :2, 4:36] = 9.0
+    assert bool((out == 9).all())
+    assert bool(pool[n:].isnan().all()) and bool(pool[:, 2 * 64 * 32:].isnan().all())
+
+
+def test_chunks_continue_the_state():
+    """A prompt in pieces of every kind equals the whole prompt, within the
+    tolerances of the oracle's run."""
+    rng = np.random.default_rng(12)
+    c = build(rng, [333], 2, 4, 128, 64)
+    want = reference(c, held=[0])
+    whole = c["state"].clone()
+    out, at = [], 0
+    for piece in (100, 1, 64, 5, 1, 130, 32):
+        part = {x: c[x][at:at + piece] for x in ("q", "k", "v", "alpha", "beta")}
+        out.append(nv.gdn_attention(state=whole, cu_lens=i32([0, piece]), max_len=piece,
+                                    slots=c["slots"], cached_lens=i32([at]),
+                                    normalize=True, **part))
+        at += piece
+    assert at == 333
+    o, s, size, reach, w = want[0]
+    t_out, t_state = tolerances(size, reach, w, o)
+    assert (np.abs(torch.cat(out).double().cpu().numpy() - o) <= t_out).all()
+    assert (np.abs(whole[int(c["slots"][0])].double().cpu().numpy() - s) <= t_state).all()
+
+
+@pytest.mark.parametrize("lens", [[1] * 7, [70, 200, 1]])
+def test_repeats_bit_for_bit(lens):
+    rng = np.random.default_rng(13)
+    c = build(rng, lens, 2, 4, 128, 128)
+    first = c["state"].clone()
+    out = nv.gdn_attention(**c)
+    for _ in range(3):
+        again = dict(c, state=first.clone())
+        assert torch.equal(nv.gdn_attention(**again), out)
+        assert torch.equal(again["state"][c["slots"].long()], c["state"][c["slots"].long()])
+
+
+def test_scale_and_no_normalisation():
+    rng = np.random.default_rng(14)
+    for lens in ([1, 1], [80]):
+        c = build(rng, lens, 1, 2, 64, 32)
+        c["k"] = (c["k"].float() / 12).to(BF16)           # |k| < 1 without the division
+        c["normalize"] = False
+        run(c, scale=0.7)
