@@ -89,10 +89,13 @@ mxfp4_gemm_simple(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict
 //
 // A row's 64 bytes of a stage are four 16-byte pieces (the four blocks),
 // exchanged by an exclusive or with the row number so that the operand reads of
-// consecutive rows fall on different banks; its four scale bytes are one dword.
-// Where k is no multiple of 128 a row's scales begin at any byte: two dwords
-// hold them, joined by the row's shift; blocks past k are read as zeros, codes
-// and scales (beyond the resource's range, and masked).
+// consecutive rows fall on different banks.  Its scales are 4 bytes of a line of
+// their own, so they come for four stages at once: read stage by stage they made
+// as many requests to L2 as the codes did.  Every wave takes the scales of its
+// rows to registers at the start of the four stages, which frees their place in
+// LDS for the next four.  Where k is no multiple of 128 a row's scales begin at
+// any byte: five dwords hold them, joined by the row's shift, and blocks past k
+// are read as zeros (codes beyond the resource's range, scales masked).
 //
 // The products are computed transposed (B's rows down, A's across), so that a
 // lane holds four consecutive columns of one row of Y.  Tiles leave through LDS
@@ -100,21 +103,21 @@ mxfp4_gemm_simple(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict
 constexpr int kBK = 128;
 constexpr int kRowBytes = kBK / 2;
 
-__device__ __forceinline__ int piece_xor(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
+__device__ __forceinline__ int piece_xor(int row) { return (row >> 2) & 3; }
 
-// One operand's stage loads of a wave: ROWS x 64 bytes of codes, and one dword
-// of scales a row (two if RAGGED).  Offsets are 32-bit, from the tile's first
-// row; rows past the last read the last.
+// One operand's loads of a wave: ROWS x 64 bytes of codes a stage, and 16 bytes
+// of scales a row every four stages (a dword more if RAGGED).  Offsets are
+// 32-bit, from the tile's first row; rows past the last read the last.
 template <int ROWS, int NW, bool RAGGED>
-struct StageLoads {
+struct Loads {
   static constexpr int kCodes = ROWS / 16 / NW;
-  static constexpr int kWords = RAGGED ? 2 : 1;
-  static constexpr int kScales = (ROWS * kWords + 64 * NW - 1) / (64 * NW);
-  static constexpr int kIssues = kCodes + kScales;
-  static constexpr int kScaleBytes = kScales * NW * 256;      // of a slot
+  static constexpr int kPerWave = (ROWS + 64 * NW - 1) / (64 * NW);    // rows / 64 of scales
+  static constexpr int kScales = kPerWave * (RAGGED ? 2 : 1);
+  static constexpr int kRows = kPerWave * NW * 64;                     // places in LDS
+  static constexpr int kScaleBytes = kRows * (RAGGED ? 20 : 16);
   static_assert(ROWS % (16 * NW) == 0, "rows split evenly over the waves");
   __amdgpu_buffer_rsrc_t codes, scales;
-  unsigned code_off[kCodes], scale_off[kScales];
+  unsigned code_off[kCodes], scale_off[kPerWave];
 
   __device__ __forceinline__ void init(const uint8_t* c, const uint8_t* s, int64_t row0,
                                        int64_t rows, int64_t k, int wave, int lane) {
@@ -136,18 +139,17 @@ struct StageLoads {
                     ((q & 3) ^ piece_xor(row)) * 16;
     }
 #pragma unroll
-    for (int i = 0; i < kScales; ++i) {
-      const int q = (wave * kScales + i) * 64 + lane, row = q / kWords;
-      scale_off[i] = ((static_cast<unsigned>(s0 - s_from) +
-                       static_cast<unsigned>(row < last ? row : last) * blocks) & ~3u) +
-                     (q % kWords) * 4;
+    for (int i = 0; i < kPerWave; ++i) {
+      const int row = (wave * kPerWave + i) * 64 + lane;
+      scale_off[i] = (static_cast<unsigned>(s0 - s_from) +
+                      static_cast<unsigned>(row < last ? row : last) * blocks) & ~3u;
     }
   }
 
   // `left`: blocks from this stage's first to the end of K (below 4 only in
   // the last stage of a ragged K)
-  __device__ __forceinline__ void issue(int stage, int left, uint8_t* lds_codes,
-                                        uint8_t* lds_scales, int wave, int lane) const {
+  __device__ __forceinline__ void issue_codes(int stage, int left, uint8_t* lds, int wave,
+                                              int lane) const {
 #pragma unroll
     for (int i = 0; i < kCodes; ++i) {
       unsigned off = code_off[i];
@@ -155,17 +157,23 @@ struct StageLoads {
         const int q = (wave * kCodes + i) * 64 + lane;
         if (((q & 3) ^ piece_xor(q >> 2)) >= left) off = 0x80000000u;
       }
-      lds_buf16(codes, lds_codes + (wave * kCodes + i) * 1024, off, stage * kRowBytes);
+      lds_buf16(codes, lds + (wave * kCodes + i) * 1024, off, stage * kRowBytes);
     }
+  }
+
+  // the scales of stages 4 window .. 4 window + 3
+  __device__ __forceinline__ void issue_scales(int window, uint8_t* lds, int wave) const {
 #pragma unroll
-    for (int i = 0; i < kScales; ++i)
-      lds_buf4(scales, lds_scales + (wave * kScales + i) * 256, scale_off[i], stage * 4);
+    for (int i = 0; i < kPerWave; ++i) {
+      lds_buf16(scales, lds + (wave * kPerWave + i) * 1024, scale_off[i], window * 16);
+      if constexpr (RAGGED)
+        lds_buf4(scales, lds + kRows * 16 + (wave * kPerWave + i) * 256, scale_off[i] + 16,
+                 window * 16);
+    }
   }
 };
 
-// A wave's operands of one k-step of T tiles of 32 rows, and the scales of a
-// stage (byte 0: the first k-step's block of this half-wave, byte 2: the
-// second's).
+// A wave's operands of one k-step of T tiles of 32 rows.
 template <int T>
 struct Operand {
   u32x4 code[T];
@@ -180,28 +188,37 @@ __device__ __forceinline__ void read_codes(Operand<T>& o, const uint8_t* lds, in
     o.code[t] = *reinterpret_cast<const u32x4*>(lds + at + t * 32 * kRowBytes);
 }
 
-// The scale words of T rows as LDS has them, and what the products take of
-// them: byte 0 and byte 2 are this half-wave's blocks of the two k-steps.
-// Taken apart so that nothing waits for the read before the products do.
-template <int T, bool RAGGED>
+// The scales of four stages of T tiles of rows, and of them those of one stage
+// as the products take them: byte 0 and byte 2 are this half-wave's blocks of
+// the two k-steps.
+template <int T, bool RAGGED, int ROWS>
 struct Scales {
-  u32x2 w[T];
+  u32x4 w[T];
+  unsigned more[RAGGED ? T : 1];
   __device__ __forceinline__ void read(const uint8_t* lds, int row) {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      if constexpr (RAGGED) w[t] = *reinterpret_cast<const u32x2*>(lds + row * 8 + t * 256);
-      else w[t][0] = *reinterpret_cast<const unsigned*>(lds + row * 4 + t * 128);
+      w[t] = *reinterpret_cast<const u32x4*>(lds + row * 16 + t * 512);
+      if constexpr (RAGGED)
+        more[t] = *reinterpret_cast<const unsigned*>(lds + ROWS * 16 + row * 4 + t * 128);
     }
   }
+  template <int U>
   __device__ __forceinline__ void take(unsigned (&s)[T], int half, const unsigned (&shift)[T],
                                        unsigned mask) const {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-      s[t] = w[t][0];
-      if constexpr (RAGGED) s[t] = __builtin_amdgcn_alignbyte(w[t][1], s[t], shift[t]) & mask;
+      s[t] = w[t][U];
+      if constexpr (RAGGED)
+        s[t] = __builtin_amdgcn_alignbyte(U == 3 ? more[t] : w[t][(U + 1) & 3], s[t], shift[t]) & mask;
       s[t] >>= half * 8;
     }
   }
+};
+
+template <int I>
+struct Index {
+  static constexpr int value = I;
 };
 
 template <int STEP>
@@ -215,13 +232,31 @@ __device__ __forceinline__ f32x16 product(u32x4 a, unsigned sa, u32x4 b, unsigne
                                                          static_cast<int>(sb));
 }
 
+// One scheduling region of products: the next operands' reads go out behind the
+// first products, one by one (left to itself the compiler puts them behind all,
+// to reuse registers, and the next products wait for LDS), and the loads spread
+// over all of them (a burst of loads holds up the products behind it).
+template <int PRODUCTS, int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < PRODUCTS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
+    if (i < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    // LDS read
+    if (i * LOADS / PRODUCTS != (i + 1) * LOADS / PRODUCTS)
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                 // memory read
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <int WM, int WN, int TM, int TN, bool RAGGED>
 struct TileShape {
   static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32, NS = 4;
-  using LoadsA = StageLoads<BM, NW, RAGGED>;
-  using LoadsB = StageLoads<BN, NW, RAGGED>;
-  static constexpr int kSlotBytes = (BM + BN) * kRowBytes + LoadsA::kScaleBytes + LoadsB::kScaleBytes;
-  static constexpr int kIssues = LoadsA::kIssues + LoadsB::kIssues;
+  using LoadsA = Loads<BM, NW, RAGGED>;
+  using LoadsB = Loads<BN, NW, RAGGED>;
+  static constexpr int kSlotBytes = (BM + BN) * kRowBytes;
+  static constexpr int kScaleBytes = LoadsA::kScaleBytes + LoadsB::kScaleBytes;
+  static constexpr int kCodes = LoadsA::kCodes + LoadsB::kCodes;      // loads of a wave
+  static constexpr int kScales = LoadsA::kScales + LoadsB::kScales;
 };
 
 template <int WM, int WN, int TM, int TN, bool RAGGED, int OUT>
@@ -235,16 +270,15 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
   // an object of its own for each slot: a fill of one slot then does not look
   // like a write to what the reads of another wait for
   __shared__ __attribute__((aligned(1024))) uint8_t s0[S::kSlotBytes], s1[S::kSlotBytes],
-      s2[S::kSlotBytes], s3[S::kSlotBytes];
-  uint8_t* const slots[NS] = {s0, s1, s2, s3};
+      s2[S::kSlotBytes], s3[S::kSlotBytes], scale_lds[S::kScaleBytes];
 
   // workgroups are dealt to the 8 XCDs in turn: each XCD takes a contiguous
-  // range of tiles, in groups of 8 tiles of rows, so that those that run
+  // range of tiles, in groups of 4 tiles of rows, so that those that run
   // together share panels in its L2
   const int ntiles = tiles_m * tiles_n;
   int bid = blockIdx.x;
   if (ntiles % 8 == 0) bid = (bid % 8) * (ntiles / 8) + bid / 8;
-  constexpr int kGroup = 8;
+  constexpr int kGroup = 4;
   const int first_m = bid / (kGroup * tiles_n) * kGroup;
   const int gm = min(tiles_m - first_m, kGroup);
   const int in_group = bid % (kGroup * tiles_n);
@@ -282,17 +316,28 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  constexpr int kB = S::BM * kRowBytes, kSA = kB + S::BN * kRowBytes,
-                kSB = kSA + S::LoadsA::kScaleBytes;
-  auto issue = [&](int stage, uint8_t* slot) {
-    const int st = stage < nk ? stage : nk - 1;    // past the end: the last again
-    const int left = blocks - 4 * st;
-    la.issue(st, left, slot, slot + kSA, wave, lane);
-    lb.issue(st, left, slot + kB, slot + kSB, wave, lane);
+  constexpr int kB = S::BM * kRowBytes, kSB = S::LoadsA::kScaleBytes;
+  // past the end: the last stage again
+  auto issue_a = [&](int stage, uint8_t* slot) {
+    const int st = stage < nk ? stage : nk - 1;
+    la.issue_codes(st, blocks - 4 * st, slot, wave, lane);
   };
-#pragma unroll
-  for (int st = 0; st < NS - 1; ++st) issue(st, slots[st]);
-  __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kIssues));
+  auto issue_b = [&](int stage, uint8_t* slot) {
+    const int st = stage < nk ? stage : nk - 1;
+    lb.issue_codes(st, blocks - 4 * st, slot + kB, wave, lane);
+  };
+  auto issue_scales = [&](int window) {
+    la.issue_scales(window, scale_lds, wave);
+    lb.issue_scales(window, scale_lds + kSB, wave);
+  };
+  issue_scales(0);
+  issue_a(0, s0);
+  issue_b(0, s0);
+  issue_a(1, s1);
+  issue_b(1, s1);
+  issue_a(2, s2);
+  issue_b(2, s2);
+  __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kCodes));
   stage_barrier();
 
   // places of the lane's first piece (k-step 0; that of k-step 1 is 32 bytes
@@ -301,51 +346,68 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
   const int lane_at = r * kRowBytes + (h ^ piece_xor(r)) * 16;
   const int a0 = arow * kRowBytes + lane_at, a1 = a0 ^ 32;
   const int b0 = kB + brow * kRowBytes + lane_at, b1 = b0 ^ 32;
-  const int ra = arow + r, rb = brow + r;
   Operand<TM> ca, na;
   Operand<TN> cb, nb;
-  unsigned sa[TM], sb[TN];
-  read_codes(ca, slots[0], a0);
-  read_codes(cb, slots[0], b0);
-  Scales<TM, RAGGED> ta;
-  Scales<TN, RAGGED> tb;
-  ta.read(slots[0] + kSA, ra);
-  tb.read(slots[0] + kSB, rb);
-  ta.take(sa, h, ashift, nk == 1 ? tail_mask : ~0u);
-  tb.take(sb, h, bshift, nk == 1 ? tail_mask : ~0u);
+  Scales<TM, RAGGED, S::LoadsA::kRows> wa;
+  Scales<TN, RAGGED, S::LoadsB::kRows> wb;
+  read_codes(ca, s0, a0);
+  read_codes(cb, s0, b0);
+  wa.read(scale_lds, arow + r);
+  wb.read(scale_lds + kSB, brow + r);
 
-  for (int kt0 = 0; kt0 < nk; kt0 += NS) {
+  auto stage = [&](auto index, int kt, uint8_t* slot, uint8_t* next, uint8_t* fill) {
+    constexpr int U = decltype(index)::value;
+    // The scales of the next four stages go to the place that every wave has
+    // read before the barrier of the stage before this one.
+    if constexpr (U == 1) issue_scales((kt >> 2) + 1);
+    issue_a(kt + NS - 1, fill);
+    const unsigned mask = kt + 1 >= nk ? tail_mask : ~0u;
+    unsigned sa[TM], sb[TN];
+    wa.template take<U>(sa, h, ashift, mask);
+    wb.template take<U>(sb, h, bshift, mask);
+    read_codes(na, slot, a1);
+    read_codes(nb, slot, b1);
 #pragma unroll
-    for (int u = 0; u < NS; ++u) {
-      const int kt = kt0 + u;
-      if (kt < nk) {
-      uint8_t* const slot = slots[u];
-      uint8_t* const next = slots[(u + 1) % NS];
-      issue(kt + NS - 1, slots[(u + NS - 1) % NS]);
-      read_codes(na, slot, a1);
-      read_codes(nb, slot, b1);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = product<0>(cb.code[j], sb[j], ca.code[i], sa[i], acc[i][j]);
+    interleave<TM * TN, TM + TN, S::LoadsA::kCodes + (U == 1 ? S::kScales : 0)>();
+    // this wave's loads of stage kt + 1 (and of its scales) have landed: those
+    // of stage kt + 2 and A's of stage kt + 3 may be in flight, with the scales
+    // that were issued between them
+    __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kCodes - S::LoadsB::kCodes +
+                                            (U == 1 || U == 2 ? S::kScales : 0)));
+    stage_barrier();
+    issue_b(kt + NS - 1, fill);
+    read_codes(ca, next, a0);
+    read_codes(cb, next, b0);
+    if constexpr (U == 3) {
+      wa.read(scale_lds, arow + r);
+      wb.read(scale_lds + kSB, brow + r);
+    }
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = product<0>(cb.code[j], sb[j], ca.code[i], sa[i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kIssues));
-      stage_barrier();
-      read_codes(ca, next, a0);
-      read_codes(cb, next, b0);
-      ta.read(next + kSA, ra);
-      tb.read(next + kSB, rb);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = product<1>(nb.code[j], sb[j], na.code[i], sa[i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-      const unsigned mask = kt + 2 >= nk ? tail_mask : ~0u;
-      ta.take(sa, h, ashift, mask);
-      tb.take(sb, h, bshift, mask);
-      }
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = product<1>(nb.code[j], sb[j], na.code[i], sa[i], acc[i][j]);
+    interleave<TM * TN, TM + TN, S::LoadsB::kCodes>();
+  };
+  // whole rounds of four stages, then the one to three that are left: with a
+  // condition on a stage inside the loop, the compiler waits for loads that may
+  // stay in flight where the paths join
+  int kt = 0;
+  for (; kt + NS <= nk; kt += NS) {
+    stage(Index<0>(), kt, s0, s1, s3);
+    stage(Index<1>(), kt + 1, s1, s2, s0);
+    stage(Index<2>(), kt + 2, s2, s3, s1);
+    stage(Index<3>(), kt + 3, s3, s0, s2);
+  }
+  if (kt < nk) {
+    stage(Index<0>(), kt, s0, s1, s3);
+    if (kt + 1 < nk) {
+      stage(Index<1>(), kt + 1, s1, s2, s0);
+      if (kt + 2 < nk) stage(Index<2>(), kt + 2, s2, s3, s1);
     }
   }
   // no fill may still be writing LDS when it is used again or released
@@ -353,12 +415,13 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
   __syncthreads();
 
   // Each wave's 32 rows x CW columns at a time through a part of LDS of its
-  // own.  Lane l holds row l % 32 and, in element e of tile j, column 32 j + 8
+  // own, a row's 16-byte pieces exchanged by an exclusive or with its number.  Lane l holds row l % 32 and, in element e of tile j, column 32 j + 8
   // (e / 4) + 4 (l / 32) + e % 4.
   constexpr int kSize = OUT == kOutF32 ? 4 : 2;
-  constexpr int CT = OUT == kOutF32 && TN > 2 ? 2 : TN;       // tiles of columns at a time
-  constexpr int CW = CT * 32, kStride = CW * kSize + 16;
-  static_assert(S::NW * 32 * kStride <= S::kSlotBytes, "the pieces fit one slot");
+  constexpr int kFit = S::kSlotBytes / (S::NW * 32 * 32 * kSize);
+  constexpr int CT = kFit < TN ? kFit : TN;                   // tiles of columns at a time
+  constexpr int CW = CT * 32, kStride = CW * kSize, kPieces = kStride / 16;
+  static_assert(CT > 0 && TN % CT == 0, "the pieces fit one slot");
   uint8_t* const mine = s0 + wave * 32 * kStride;
   const bool whole = reinterpret_cast<uintptr_t>(out) % 16 == 0 && (ldo * kSize) % 16 == 0 &&
                      (n * kSize) % 16 == 0;
@@ -373,7 +436,8 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const f32x16& c = acc[i][j0 + j];
-          uint8_t* p = mine + r * kStride + (j * 32 + 8 * g + 4 * h) * kSize;
+          const int byte = (j * 32 + 8 * g + 4 * h) * kSize;
+          uint8_t* p = mine + r * kStride + ((byte / 16) ^ (r & (kPieces - 1))) * 16 + byte % 16;
           if constexpr (OUT == kOutF32)
             *reinterpret_cast<f32x4*>(p) = f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
           else
@@ -382,11 +446,11 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
         }
       __builtin_amdgcn_wave_barrier();
       if (whole) {
-        constexpr int kPieces = CW * kSize / 16;              // of a row
 #pragma unroll
         for (int it = 0; it < kPieces / 2; ++it) {
           const int q = it * 64 + lane, row = q / kPieces, cb16 = q % kPieces;
-          const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kStride + cb16 * 16);
+          const u32x4 v = *reinterpret_cast<const u32x4*>(mine + row * kStride +
+                                                            (cb16 ^ (row & (kPieces - 1))) * 16);
           const int64_t col = col0 + cb16 * (16 / kSize);
           if (row0 + row < m && col < n)
             __builtin_nontemporal_store(
@@ -398,7 +462,9 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
           const int row = q / CW;
           const int64_t col = col0 + q % CW;
           if (row0 + row < m && col < n) {
-            const uint8_t* p = mine + row * kStride + (q % CW) * kSize;
+            const int byte = (q % CW) * kSize;
+            const uint8_t* p = mine + row * kStride + ((byte / 16) ^ (row & (kPieces - 1))) * 16 +
+                               byte % 16;
             if constexpr (OUT == kOutF32)
               static_cast<float*>(out)[(row0 + row) * ldo + col] = *reinterpret_cast<const float*>(p);
             else
