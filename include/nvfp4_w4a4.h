@@ -487,8 +487,7 @@ int64_t prompt_attention_workspace(int64_t n_tokens, int64_t n_heads,
  *
  * mxfp4_gemm -- Y = A B^T for A [m][k] and B [n][k] (K-major weights) in the
  *   layout above; codes and scale arrays 16-byte aligned (else MISALIGNED).
- *   m, n >= 1, k >= 32, k % 32 == 0; k % 256 == 0 takes the whole-stage
- *   kernels.  out [m][ldo] of out_dtype (F32 or BF16), ldo >= n, 4-byte
+ *   m, n >= 1, k >= 32, k % 32 == 0, k <= 2^22 (else UNSUPPORTED).  out [m][ldo] of out_dtype (F32 or BF16), ldo >= n, 4-byte
  *   aligned, no overlap with the inputs.  Products and scales are exact, sums
  *   are binary32, BF16 is rounded to nearest even from that.  A row with a
  *   scale byte of 0xFF gives NaN.

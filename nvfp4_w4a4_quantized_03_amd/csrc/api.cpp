@@ -182,7 +182,7 @@ const char* nvfp4_status_string(int status) {
              "than 64 rows or k not a multiple of 128; paged cache: page size "
              "not a multiple of 16; attention: d not 64, 128 or 256; "
              "gdn_attention: dk not 64 or 128, dv not a multiple of 16 or "
-             "above 512)";
+             "above 512; mxfp4_gemm: k above 2^22)";
     case NVFP4_ERR_MISALIGNED:
       return "NVFP4_ERR_MISALIGNED: a pointer or row stride breaks the "
              "required alignment";
@@ -656,6 +656,7 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, const
   if (st != NVFP4_OK) return st;
   if (!out || ldo < n || ldo > kMaxDim || m > kMaxDim / ldo) return NVFP4_ERR_INVALID_VALUE;
   if (out_dtype != NVFP4_DTYPE_F32 && out_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_UNSUPPORTED;
+  if (k > nvfp4::kMaxMxfp4K) return NVFP4_ERR_UNSUPPORTED;
   if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) ||
       !aligned(b_scales, 16) || !aligned(out, 4))
     return NVFP4_ERR_MISALIGNED;

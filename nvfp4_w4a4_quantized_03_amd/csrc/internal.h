@@ -161,6 +161,7 @@ hipError_t launch_mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                    int64_t k, void* out, int out_dtype, int64_t ldo,
                                    hipStream_t stream);
+constexpr int64_t kMaxMxfp4K = int64_t(1) << 22;   // 32-bit offsets within a tile's rows
 hipError_t launch_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                              const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
                              void* out, int out_dtype, int64_t ldo, hipStream_t stream);

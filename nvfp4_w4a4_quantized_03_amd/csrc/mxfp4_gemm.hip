@@ -30,48 +30,162 @@ __device__ __forceinline__ unsigned bf16_pair(float a, float b) {
   return __builtin_bit_cast(unsigned, p);
 }
 
-// Simple kernel for every shape: four waves of 32 x 32 outputs, operands from
-// memory straight to registers, 64 of K an instruction.  Lane l has row l % 32
-// and the block l / 32 of the two; a block past K is zeros.
-template <int OUT>
-__global__ void __launch_bounds__(256)
-mxfp4_gemm_simple(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales,
-                  int64_t m, const uint8_t* __restrict__ b_codes,
-                  const uint8_t* __restrict__ b_scales, int64_t n, int64_t k,
-                  void* __restrict__ out, int64_t ldo, int64_t tiles_n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = blockIdx.x / tiles_n * 64 + (wave >> 1) * 32;
-  const int64_t n0 = blockIdx.x % tiles_n * 64 + (wave & 1) * 32;
-  const int r = lane & 31, h = lane >> 5;
-  const int64_t blocks = k / 32;
-  const int64_t ar = m0 + r < m ? m0 + r : m - 1, br = n0 + r < n ? n0 + r : n - 1;
-  f32x16 acc = {};
-  for (int64_t b0 = 0; b0 < blocks; b0 += 2) {
-    const int64_t b = b0 + h;
-    i32x8 av = {}, bv = {};
-    unsigned as = 0, bs = 0;
-    if (b < blocks) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(a_codes + (ar * blocks + b) * 16);
-      const u32x4 c = *reinterpret_cast<const u32x4*>(b_codes + (br * blocks + b) * 16);
-      as = a_scales[ar * blocks + b];
-      bs = b_scales[br * blocks + b];
+__device__ __forceinline__ i32x8 operand(u32x4 c) {
+  return {static_cast<int>(c[0]), static_cast<int>(c[1]), static_cast<int>(c[2]),
+          static_cast<int>(c[3]), 0, 0, 0, 0};
+}
+
+// 16 x 16 outputs, 128 of K; scales in byte 0
+__device__ __forceinline__ f32x4 product16(u32x4 a, unsigned sa, u32x4 b, unsigned sb, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, 4, 4, 0,
+                                                          static_cast<int>(sa), 0,
+                                                          static_cast<int>(sb));
+}
+
+// 32 x 32 outputs, 64 of K; scales in byte 0 (STEP 0) or 2 (STEP 1)
+template <int STEP>
+__device__ __forceinline__ f32x16 product(u32x4 a, unsigned sa, u32x4 b, unsigned sb, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 4, 2 * STEP,
+                                                         static_cast<int>(sa), 2 * STEP,
+                                                         static_cast<int>(sb));
+}
+
+// ---------------------------------------------------------------------------
+// Streaming kernel: one operand (L) of at most 64 rows, the other (S) read once.
+//
+// A workgroup of NW waves takes SF 16 rows of S and all of L (LF 16 rows), the
+// waves a part of K each.  Operands go from memory straight to registers: a
+// wave has the loads of up to eight k-steps (128 of K) in flight at once, for K
+// up to 8192 mostly all that it needs, and L comes from L2.  The waves' sums meet in
+// LDS and are added in a fixed order.  What bounds it is the latency of one
+// round of loads and the reduction behind it.
+//
+// Lane l of a k-step has row l % 16 and block l / 16 of the four; its scale byte
+// comes with those of its row, four k-steps in one load, or (RAGGED: k no
+// multiple of 128) by itself.  Rows past the last read the last; blocks past k
+// lie beyond the resource's range and are zeros.
+template <int F, int STEPS, bool RAGGED>
+struct StreamOperand {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  unsigned code_off[F], scale_off[F];
+  u32x4 code[F][STEPS];
+  u32x4 scale[F][RAGGED ? STEPS : STEPS / 4];    // RAGGED: one byte each
+
+  __device__ __forceinline__ void init(const uint8_t* c, const uint8_t* s, int64_t row0,
+                                       int64_t rows, int64_t k, int lane) {
+    const unsigned kbytes = static_cast<unsigned>(k / 2), blocks = static_cast<unsigned>(k / 32);
+    const int last = static_cast<int>(rows - 1 - row0 < F * 16 - 1 ? rows - 1 - row0 : F * 16 - 1);
+    codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(c + row0 * kbytes), 0,
+                                              static_cast<int>((last + 1) * kbytes), 0x00020000);
+    scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(s + row0 * blocks), 0,
+                                               static_cast<int>((last + 1) * blocks), 0x00020000);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        av[i] = static_cast<int>(a[i]);
-        bv[i] = static_cast<int>(c[i]);
+    for (int f = 0; f < F; ++f) {
+      const int row = f * 16 + (lane & 15);
+      code_off[f] = static_cast<unsigned>(row < last ? row : last) * kbytes + (lane >> 4) * 16;
+      scale_off[f] = static_cast<unsigned>(row < last ? row : last) * blocks;
+    }
+  }
+
+  // k-steps [first, first + n), n <= STEPS
+  __device__ __forceinline__ void load(int first, int n, int blocks, int lane) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int block = 4 * (first + i) + (lane >> 4);
+      const bool in = i < n && (!RAGGED || block < blocks);
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        code[f][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+            codes, in ? code_off[f] + (first + i) * 64 : 0x80000000u, 0, 0));
+        if constexpr (RAGGED)
+          scale[f][i][0] = __builtin_amdgcn_raw_buffer_load_b8(
+              scales, in ? scale_off[f] + block : 0x80000000u, 0, 0);
       }
     }
-    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, 0, static_cast<int>(as),
-                                                          0, static_cast<int>(bs));
-  }
+    if constexpr (!RAGGED) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int64_t row = m0 + 8 * (e >> 2) + 4 * h + (e & 3), col = n0 + r;
-    if (row < m && col < n) {
+      for (int i = 0; i < STEPS / 4; ++i)
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          scale[f][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              scales, 4 * i < n ? scale_off[f] + (first + 4 * i) * 4 : 0x80000000u, 0, 0));
+    }
+  }
+
+  __device__ __forceinline__ unsigned scale_of(int f, int i, int lane) const {
+    if constexpr (RAGGED) return scale[f][i][0];
+    else return scale[f][i / 4][i % 4] >> (8 * (lane >> 4));
+  }
+};
+
+template <int NW, int SF, int LF, bool RAGGED, bool S_IS_B, int OUT>
+__global__ void __launch_bounds__(NW * 64)
+mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict__ s_scales,
+                  int64_t s_rows, const uint8_t* __restrict__ l_codes,
+                  const uint8_t* __restrict__ l_scales, int64_t l_rows, int64_t k,
+                  void* __restrict__ out, int64_t ldo) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (SF * 16);
+  const int blocks = static_cast<int>(k / 32), steps = (blocks + 3) >> 2;
+  const int from = steps * wave / NW, to = steps * (wave + 1) / NW;
+
+  // k-steps in flight: what the registers hold
+  constexpr int STEPS = SF + LF > 5 || NW < 8 ? 4 : 8;
+  StreamOperand<SF, STEPS, RAGGED> so;
+  StreamOperand<LF, STEPS, RAGGED> lo;
+  so.init(s_codes, s_scales, row0, s_rows, k, lane);
+  lo.init(l_codes, l_scales, 0, l_rows, k, lane);
+  f32x4 acc[SF][LF] = {};
+  for (int st = from; st < to; st += STEPS) {
+    const int n = to - st < STEPS ? to - st : STEPS;
+    so.load(st, n, blocks, lane);
+    lo.load(st, n, blocks, lane);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+      if (i < n) {
+#pragma unroll
+        for (int a = 0; a < SF; ++a)
+#pragma unroll
+          for (int b = 0; b < LF; ++b) {
+            const unsigned ss = so.scale_of(a, i, lane), ls = lo.scale_of(b, i, lane);
+            // B's rows down, A's across
+            acc[a][b] = S_IS_B ? product16(so.code[a][i], ss, lo.code[b][i], ls, acc[a][b])
+                               : product16(lo.code[b][i], ls, so.code[a][i], ss, acc[a][b]);
+          }
+      }
+  }
+
+  __shared__ f32x4 sums[NW][SF * LF][64];
+#pragma unroll
+  for (int a = 0; a < SF; ++a)
+#pragma unroll
+    for (int b = 0; b < LF; ++b) sums[wave][a * LF + b][lane] = acc[a][b];
+  __syncthreads();
+  const bool whole = reinterpret_cast<uintptr_t>(out) % (OUT == kOutF32 ? 16 : 8) == 0 &&
+                     ldo % 4 == 0;
+  for (int q = threadIdx.x; q < SF * LF * 64; q += NW * 64) {
+    const int tile = q >> 6, l = q & 63;
+    f32x4 y = sums[0][tile][l];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) y += sums[w][tile][l];
+    // lane l of a tile: column of A's rows l % 16, four of B's from 4 (l / 16)
+    const int64_t sr = row0 + tile / LF * 16, lr = tile % LF * 16;
+    const int64_t m = (S_IS_B ? lr : sr) + (l & 15), n = (S_IS_B ? sr : lr) + (l >> 4) * 4;
+    const int64_t rows_m = S_IS_B ? l_rows : s_rows, rows_n = S_IS_B ? s_rows : l_rows;
+    if (m >= rows_m) continue;
+    if (whole && n + 4 <= rows_n) {
       if constexpr (OUT == kOutF32)
-        static_cast<float*>(out)[row * ldo + col] = acc[e];
+        *reinterpret_cast<f32x4*>(static_cast<float*>(out) + m * ldo + n) = y;
       else
-        static_cast<unsigned short*>(out)[row * ldo + col] = bf16_bits(acc[e]);
+        *reinterpret_cast<u32x2*>(static_cast<unsigned short*>(out) + m * ldo + n) =
+            u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < rows_n) {
+          if constexpr (OUT == kOutF32) static_cast<float*>(out)[m * ldo + n + i] = y[i];
+          else static_cast<unsigned short*>(out)[m * ldo + n + i] = bf16_bits(y[i]);
+        }
     }
   }
 }
@@ -80,37 +194,38 @@ mxfp4_gemm_simple(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict
 // Tiled kernel.
 //
 // A workgroup of WM x WN waves computes a tile of WM TM 32 rows of A by WN TN
-// 32 rows of B, 128 of K a stage.  Stages go from memory straight to a ring of
-// NS slots in LDS; a wave reads its operands one k-step (64 of K) ahead of the
-// products that use them.  One wait and one barrier a stage, between its two
-// k-steps: stage kt + 1 has landed for everybody before its first operands are
-// read, and the slot of stage kt - 1, whose last reads came before the barrier
-// of that stage, takes stage kt + NS - 1.
+// 32 rows of B, 256 of K a stage: 128 bytes of a row, a whole line, because L2
+// answers a request of half a line in the time of a whole one (stages of 128 of
+// K: the loads alone took 734 us of 32768 x 10240 x 5120's 926).  Stages go from
+// memory straight to one of two slots in LDS.  A stage is four k-steps of 64; a
+// wave reads the operands of a k-step while the products of the one before it
+// run, so the last reads of a slot are behind the third k-step's products, and
+// one wait and one barrier there free it: the stage after next goes into it
+// while the fourth k-step and the next stage run.
 //
-// A row's 64 bytes of a stage are four 16-byte pieces (the four blocks),
-// exchanged by an exclusive or with the row number so that the operand reads of
-// consecutive rows fall on different banks.  Its scales are 4 bytes of a line of
-// their own, so they come for four stages at once: read stage by stage they made
-// as many requests to L2 as the codes did.  Every wave takes the scales of its
-// rows to registers at the start of the four stages, which frees their place in
-// LDS for the next four.  Where k is no multiple of 128 a row's scales begin at
-// any byte: five dwords hold them, joined by the row's shift, and blocks past k
-// are read as zeros (codes beyond the resource's range, scales masked).
+// A row's eight 16-byte pieces of a stage (the eight blocks) are exchanged by an
+// exclusive or with the row number, so that the operand reads of a wave fall on
+// different banks.  Its scales are 8 bytes of a line of their own, so they come
+// for two stages at once; every wave takes those of its rows to registers at the
+// start of the two, which frees their place in LDS for the next.  Where k is no
+// multiple of 128 (RAGGED) a row's scales begin at any byte: five dwords hold
+// them, joined by the row's shift.  Blocks past k are read as zeros: codes
+// beyond the resource's range, scales masked.
 //
 // The products are computed transposed (B's rows down, A's across), so that a
 // lane holds four consecutive columns of one row of Y.  Tiles leave through LDS
 // in whole 16-byte pieces.
-constexpr int kBK = 128;
+constexpr int kBK = 256;
 constexpr int kRowBytes = kBK / 2;
 
-__device__ __forceinline__ int piece_xor(int row) { return (row >> 2) & 3; }
+__device__ __forceinline__ int piece_xor(int row) { return (row >> 1) & 7; }
 
-// One operand's loads of a wave: ROWS x 64 bytes of codes a stage, and 16 bytes
-// of scales a row every four stages (a dword more if RAGGED).  Offsets are
+// One operand's loads of a wave: ROWS x 128 bytes of codes a stage, and 16 bytes
+// of scales a row every two stages (a dword more if RAGGED).  Offsets are
 // 32-bit, from the tile's first row; rows past the last read the last.
 template <int ROWS, int NW, bool RAGGED>
 struct Loads {
-  static constexpr int kCodes = ROWS / 16 / NW;
+  static constexpr int kCodes = ROWS / 8 / NW;
   static constexpr int kPerWave = (ROWS + 64 * NW - 1) / (64 * NW);    // rows / 64 of scales
   static constexpr int kScales = kPerWave * (RAGGED ? 2 : 1);
   static constexpr int kRows = kPerWave * NW * 64;                     // places in LDS
@@ -134,9 +249,9 @@ struct Loads {
         0x00020000);
 #pragma unroll
     for (int i = 0; i < kCodes; ++i) {
-      const int q = (wave * kCodes + i) * 64 + lane, row = q >> 2;
+      const int q = (wave * kCodes + i) * 64 + lane, row = q >> 3;
       code_off[i] = static_cast<unsigned>(row < last ? row : last) * kbytes +
-                    ((q & 3) ^ piece_xor(row)) * 16;
+                    ((q & 7) ^ piece_xor(row)) * 16;
     }
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
@@ -146,22 +261,19 @@ struct Loads {
     }
   }
 
-  // `left`: blocks from this stage's first to the end of K (below 4 only in
-  // the last stage of a ragged K)
+  // `left`: blocks from this stage's first to the end of K (below 8 in a last
+  // stage, or past it)
   __device__ __forceinline__ void issue_codes(int stage, int left, uint8_t* lds, int wave,
                                               int lane) const {
 #pragma unroll
     for (int i = 0; i < kCodes; ++i) {
-      unsigned off = code_off[i];
-      if constexpr (RAGGED) {
-        const int q = (wave * kCodes + i) * 64 + lane;
-        if (((q & 3) ^ piece_xor(q >> 2)) >= left) off = 0x80000000u;
-      }
+      const int q = (wave * kCodes + i) * 64 + lane;
+      const unsigned off = ((q & 7) ^ piece_xor(q >> 3)) < left ? code_off[i] : 0x80000000u;
       lds_buf16(codes, lds + (wave * kCodes + i) * 1024, off, stage * kRowBytes);
     }
   }
 
-  // the scales of stages 4 window .. 4 window + 3
+  // the scales of stages 2 window and 2 window + 1
   __device__ __forceinline__ void issue_scales(int window, uint8_t* lds, int wave) const {
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
@@ -188,9 +300,9 @@ __device__ __forceinline__ void read_codes(Operand<T>& o, const uint8_t* lds, in
     o.code[t] = *reinterpret_cast<const u32x4*>(lds + at + t * 32 * kRowBytes);
 }
 
-// The scales of four stages of T tiles of rows, and of them those of one stage
-// as the products take them: byte 0 and byte 2 are this half-wave's blocks of
-// the two k-steps.
+// The scales of two stages of T tiles of rows, and of them those of the U-th
+// pair of k-steps as the products take them: byte 0 and byte 2 are this
+// half-wave's blocks of the two.
 template <int T, bool RAGGED, int ROWS>
 struct Scales {
   u32x4 w[T];
@@ -210,8 +322,8 @@ struct Scales {
     for (int t = 0; t < T; ++t) {
       s[t] = w[t][U];
       if constexpr (RAGGED)
-        s[t] = __builtin_amdgcn_alignbyte(U == 3 ? more[t] : w[t][(U + 1) & 3], s[t], shift[t]) & mask;
-      s[t] >>= half * 8;
+        s[t] = __builtin_amdgcn_alignbyte(U == 3 ? more[t] : w[t][(U + 1) & 3], s[t], shift[t]);
+      s[t] = (s[t] & mask) >> (half * 8);
     }
   }
 };
@@ -220,17 +332,6 @@ template <int I>
 struct Index {
   static constexpr int value = I;
 };
-
-template <int STEP>
-__device__ __forceinline__ f32x16 product(u32x4 a, unsigned sa, u32x4 b, unsigned sb, f32x16 c) {
-  const i32x8 x = {static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]),
-                   static_cast<int>(a[3]), 0, 0, 0, 0};
-  const i32x8 y = {static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]),
-                   static_cast<int>(b[3]), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 2 * STEP,
-                                                         static_cast<int>(sa), 2 * STEP,
-                                                         static_cast<int>(sb));
-}
 
 // One scheduling region of products: the next operands' reads go out behind the
 // first products, one by one (left to itself the compiler puts them behind all,
@@ -250,13 +351,11 @@ __device__ __forceinline__ void interleave() {
 
 template <int WM, int WN, int TM, int TN, bool RAGGED>
 struct TileShape {
-  static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32, NS = 4;
+  static constexpr int NW = WM * WN, BM = WM * TM * 32, BN = WN * TN * 32;
   using LoadsA = Loads<BM, NW, RAGGED>;
   using LoadsB = Loads<BN, NW, RAGGED>;
   static constexpr int kSlotBytes = (BM + BN) * kRowBytes;
   static constexpr int kScaleBytes = LoadsA::kScaleBytes + LoadsB::kScaleBytes;
-  static constexpr int kCodes = LoadsA::kCodes + LoadsB::kCodes;      // loads of a wave
-  static constexpr int kScales = LoadsA::kScales + LoadsB::kScales;
 };
 
 template <int WM, int WN, int TM, int TN, bool RAGGED, int OUT>
@@ -266,11 +365,10 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
                  const uint8_t* __restrict__ b_scales, int64_t n, int64_t k,
                  void* __restrict__ out, int64_t ldo, int tiles_m, int tiles_n) {
   using S = TileShape<WM, WN, TM, TN, RAGGED>;
-  constexpr int NS = S::NS;
   // an object of its own for each slot: a fill of one slot then does not look
-  // like a write to what the reads of another wait for
+  // like a write to what the reads of the other wait for
   __shared__ __attribute__((aligned(1024))) uint8_t s0[S::kSlotBytes], s1[S::kSlotBytes],
-      s2[S::kSlotBytes], s3[S::kSlotBytes], scale_lds[S::kScaleBytes];
+      scale_lds[S::kScaleBytes];
 
   // workgroups are dealt to the 8 XCDs in turn: each XCD takes a contiguous
   // range of tiles, in groups of 4 tiles of rows, so that those that run
@@ -287,7 +385,7 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int arow = wave / WN * TM * 32, brow = wave % WN * TN * 32;
-  const int blocks = static_cast<int>(k / 32), nk = (blocks + 3) >> 2;
+  const int blocks = static_cast<int>(k / 32), nk = (blocks + 7) >> 3;
 
   typename S::LoadsA la;
   typename S::LoadsB lb;
@@ -306,7 +404,6 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
       bshift[t] = static_cast<unsigned>(((row < n ? row : n - 1) * blocks) & 3);
     }
   }
-  const unsigned tail_mask = (blocks & 3) ? (1u << (8 * (blocks & 3))) - 1u : ~0u;
 
   f32x16 acc[TM][TN];
 #pragma unroll
@@ -317,14 +414,9 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
   constexpr int kB = S::BM * kRowBytes, kSB = S::LoadsA::kScaleBytes;
-  // past the end: the last stage again
-  auto issue_a = [&](int stage, uint8_t* slot) {
-    const int st = stage < nk ? stage : nk - 1;
-    la.issue_codes(st, blocks - 4 * st, slot, wave, lane);
-  };
-  auto issue_b = [&](int stage, uint8_t* slot) {
-    const int st = stage < nk ? stage : nk - 1;
-    lb.issue_codes(st, blocks - 4 * st, slot + kB, wave, lane);
+  auto issue_a = [&](int st, uint8_t* slot) { la.issue_codes(st, blocks - 8 * st, slot, wave, lane); };
+  auto issue_b = [&](int st, uint8_t* slot) {
+    lb.issue_codes(st, blocks - 8 * st, slot + kB, wave, lane);
   };
   auto issue_scales = [&](int window) {
     la.issue_scales(window, scale_lds, wave);
@@ -334,18 +426,14 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
   issue_a(0, s0);
   issue_b(0, s0);
   issue_a(1, s1);
-  issue_b(1, s1);
-  issue_a(2, s2);
-  issue_b(2, s2);
-  __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kCodes));
+  __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(S::LoadsA::kCodes));
   stage_barrier();
 
-  // places of the lane's first piece (k-step 0; that of k-step 1 is 32 bytes
-  // off, exchanged) and first row
+  // places of the lane's first piece (those of the other k-steps are 32, 64
+  // and 96 bytes off, exchanged) and first row
   const int h = lane >> 5, r = lane & 31;
   const int lane_at = r * kRowBytes + (h ^ piece_xor(r)) * 16;
-  const int a0 = arow * kRowBytes + lane_at, a1 = a0 ^ 32;
-  const int b0 = kB + brow * kRowBytes + lane_at, b1 = b0 ^ 32;
+  const int a0 = arow * kRowBytes + lane_at, b0 = kB + brow * kRowBytes + lane_at;
   Operand<TM> ca, na;
   Operand<TN> cb, nb;
   Scales<TM, RAGGED, S::LoadsA::kRows> wa;
@@ -355,61 +443,60 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
   wa.read(scale_lds, arow + r);
   wb.read(scale_lds + kSB, brow + r);
 
-  auto stage = [&](auto index, int kt, uint8_t* slot, uint8_t* next, uint8_t* fill) {
-    constexpr int U = decltype(index)::value;
-    // The scales of the next four stages go to the place that every wave has
-    // read before the barrier of the stage before this one.
-    if constexpr (U == 1) issue_scales((kt >> 2) + 1);
-    issue_a(kt + NS - 1, fill);
-    const unsigned mask = kt + 1 >= nk ? tail_mask : ~0u;
-    unsigned sa[TM], sb[TN];
-    wa.template take<U>(sa, h, ashift, mask);
-    wb.template take<U>(sb, h, bshift, mask);
-    read_codes(na, slot, a1);
-    read_codes(nb, slot, b1);
+  unsigned sa[TM], sb[TN];
+  auto take = [&](auto index, int first) {
+    // scales of blocks past k are zeros: a next row's may be a NaN
+    const int left = blocks - first;
+    const unsigned mask = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1u : 0u;
+    wa.template take<decltype(index)::value>(sa, h, ashift, mask);
+    wb.template take<decltype(index)::value>(sb, h, bshift, mask);
+  };
+  auto products = [&](auto step, const Operand<TM>& oa, const Operand<TN>& ob) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = product<0>(cb.code[j], sb[j], ca.code[i], sa[i], acc[i][j]);
-    interleave<TM * TN, TM + TN, S::LoadsA::kCodes + (U == 1 ? S::kScales : 0)>();
-    // this wave's loads of stage kt + 1 (and of its scales) have landed: those
-    // of stage kt + 2 and A's of stage kt + 3 may be in flight, with the scales
-    // that were issued between them
-    __builtin_amdgcn_s_waitcnt(kVmcntKeepOf((NS - 2) * S::kCodes - S::LoadsB::kCodes +
-                                            (U == 1 || U == 2 ? S::kScales : 0)));
+        acc[i][j] = product<decltype(step)::value>(ob.code[j], sb[j], oa.code[i], sa[i], acc[i][j]);
+  };
+  // Stage kt, in `slot`; P: the first or second of the two that share scales.
+  auto stage = [&](auto index, int kt, uint8_t* slot, uint8_t* other) {
+    constexpr int P = decltype(index)::value;
+    take(Index<2 * P>(), 8 * kt);
+    issue_b(kt + 1, other);
+    read_codes(na, slot, a0 ^ 32);
+    read_codes(nb, slot, b0 ^ 32);
+    products(Index<0>(), ca, cb);
+    interleave<TM * TN, TM + TN, S::LoadsB::kCodes>();
+    read_codes(ca, slot, a0 ^ 64);
+    read_codes(cb, slot, b0 ^ 64);
+    products(Index<1>(), na, nb);
+    interleave<TM * TN, TM + TN, 0>();
+    take(Index<2 * P + 1>(), 8 * kt + 4);
+    read_codes(na, slot, a0 ^ 96);
+    read_codes(nb, slot, b0 ^ 96);
+    products(Index<0>(), ca, cb);
+    interleave<TM * TN, TM + TN, 0>();
+    // this wave has read all of this slot, and its loads of the next stage
+    // have landed
+    __builtin_amdgcn_s_waitcnt(0);
     stage_barrier();
-    issue_b(kt + NS - 1, fill);
-    read_codes(ca, next, a0);
-    read_codes(cb, next, b0);
-    if constexpr (U == 3) {
+    if constexpr (P == 0) issue_scales((kt >> 1) + 1);
+    issue_a(kt + 2, slot);
+    read_codes(ca, other, a0);
+    read_codes(cb, other, b0);
+    if constexpr (P == 1) {
       wa.read(scale_lds, arow + r);
       wb.read(scale_lds + kSB, brow + r);
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        acc[i][j] = product<1>(nb.code[j], sb[j], na.code[i], sa[i], acc[i][j]);
-    interleave<TM * TN, TM + TN, S::LoadsB::kCodes>();
+    products(Index<1>(), na, nb);
+    interleave<TM * TN, TM + TN, S::LoadsA::kCodes>();
   };
-  // whole rounds of four stages, then the one to three that are left: with a
-  // condition on a stage inside the loop, the compiler waits for loads that may
-  // stay in flight where the paths join
   int kt = 0;
-  for (; kt + NS <= nk; kt += NS) {
-    stage(Index<0>(), kt, s0, s1, s3);
-    stage(Index<1>(), kt + 1, s1, s2, s0);
-    stage(Index<2>(), kt + 2, s2, s3, s1);
-    stage(Index<3>(), kt + 3, s3, s0, s2);
+  for (; kt + 2 <= nk; kt += 2) {
+    stage(Index<0>(), kt, s0, s1);
+    stage(Index<1>(), kt + 1, s1, s0);
   }
-  if (kt < nk) {
-    stage(Index<0>(), kt, s0, s1, s3);
-    if (kt + 1 < nk) {
-      stage(Index<1>(), kt + 1, s1, s2, s0);
-      if (kt + 2 < nk) stage(Index<2>(), kt + 2, s2, s3, s1);
-    }
-  }
+  if (kt < nk) stage(Index<0>(), kt, s0, s1);
   // no fill may still be writing LDS when it is used again or released
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
@@ -497,29 +584,95 @@ hipError_t launch_tiled(const uint8_t* a_codes, const uint8_t* a_scales, int64_t
   return hipGetLastError();
 }
 
+template <int NW, int SF, int LF, bool RAGGED, bool S_IS_B>
+hipError_t launch_stream(const uint8_t* s_codes, const uint8_t* s_scales, int64_t s_rows,
+                         const uint8_t* l_codes, const uint8_t* l_scales, int64_t l_rows,
+                         int64_t k, void* out, int out_dtype, int64_t ldo, hipStream_t stream) {
+  const int64_t groups = (s_rows + SF * 16 - 1) / (SF * 16);
+  if (groups > 0x7FFFFF) return hipErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(groups);
+  if (out_dtype == kOutF32)
+    mxfp4_gemm_stream<NW, SF, LF, RAGGED, S_IS_B, 0><<<grid, NW * 64, 0, stream>>>(
+        s_codes, s_scales, s_rows, l_codes, l_scales, l_rows, k, out, ldo);
+  else
+    mxfp4_gemm_stream<NW, SF, LF, RAGGED, S_IS_B, 1><<<grid, NW * 64, 0, stream>>>(
+        s_codes, s_scales, s_rows, l_codes, l_scales, l_rows, k, out, ldo);
+  return hipGetLastError();
+}
+
+// One round of workgroups of eight waves, one a CU, where some SF gives it (the
+// smallest does: 32 x 10240 x 5120 10.7 us with 214 workgroups of 48 rows, 15.8
+// with 320 of 32 and 17.5 with 640 of 16; 32 x 5120 x 5120 8.3 with 32 rows, 9.9
+// with 48); otherwise many of four waves with few loads in flight, several a CU
+// (32768 x 64 x 5120 39 us against 47 with eight waves, 64 x 10240 x 5120 19
+// against 23).
+template <int LF, bool RAGGED, bool S_IS_B>
+hipError_t stream_rows(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
+                       const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt,
+                       int64_t ldo, hipStream_t st) {
+  constexpr int kMost = LF == 1 ? 4 : LF == 2 ? 3 : 2;      // what the registers hold
+  const int64_t sf = (s_rows + 16 * 256 - 1) / (16 * 256);
+  if (sf <= 1)
+    return launch_stream<8, 1, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  if (sf <= 2)
+    return launch_stream<8, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  if constexpr (kMost >= 3)
+    if (sf <= 3)
+      return launch_stream<8, 3, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  if constexpr (kMost >= 4)
+    if (sf <= 4)
+      return launch_stream<8, 4, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  return launch_stream<4, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+}
+
+template <bool RAGGED, bool S_IS_B>
+hipError_t stream_of(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
+                     const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt, int64_t ldo,
+                     hipStream_t st) {
+  if (l_rows <= 16)
+    return stream_rows<1, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  if (l_rows <= 32)
+    return stream_rows<2, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  return stream_rows<4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+}
+
+// Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two).  Times of a round
+// of 256 CUs at K = 5120, full and partly filled: 42 and 30 us for the large
+// tile, 27 and, for at most one workgroup a CU, 16.5 for the small one; the
+// sums over a call's rounds choose.  (1003 x 17536 76 us with large, 69 with
+// small tiles; 300 x 5120 28 and 16; 1024 x 10240 32 and 41; 4096 x 12288 122
+// and 160.)
+bool large_tiles(int64_t m, int64_t n) {
+  const double large = static_cast<double>((m + 255) / 256) * ((n + 255) / 256);
+  const double small = static_cast<double>((m + 127) / 128) * ((n + 127) / 128);
+  const double fl = __builtin_floor(large / 256), fs = __builtin_floor(small / 512);
+  const double rl = large - 256 * fl, rs = small - 512 * fs;
+  return 42.0 * fl + (rl > 0 ? 30.0 : 0.0) <=
+         27.0 * fs + (rs > 256 ? 27.0 : rs > 0 ? 16.5 : 0.0);
+}
+
+template <bool RAGGED>
+hipError_t gemm_of(const uint8_t* ac, const uint8_t* as, int64_t m, const uint8_t* bc,
+                   const uint8_t* bs, int64_t n, int64_t k, void* out, int dt, int64_t ldo,
+                   hipStream_t st) {
+  if (m <= 64 && (n > 64 || m <= n))
+    return stream_of<RAGGED, true>(bc, bs, n, ac, as, m, k, out, dt, ldo, st);
+  if (n <= 64)
+    return stream_of<RAGGED, false>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  return large_tiles(m, n)
+             ? launch_tiled<2, 4, 4, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st)
+             : launch_tiled<2, 2, 2, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+}
+
 }  // namespace
 
 hipError_t launch_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                              const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
                              void* out, int out_dtype, int64_t ldo, hipStream_t stream) {
-  // 32-bit offsets within a tile
-  if (k <= (int64_t(1) << 22) && m > 64 && n > 64) {
-    if (k % kBK == 0)
-      return launch_tiled<2, 2, 4, 4, false>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
-                                             out_dtype, ldo, stream);
-    return launch_tiled<2, 2, 4, 4, true>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
-                                          out_dtype, ldo, stream);
-  }
-  const int64_t tm = (m + 63) / 64, tn = (n + 63) / 64;
-  if (tm > 0xFFFFFF / tn) return hipErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(tm * tn);
-  if (out_dtype == kOutF32)
-    mxfp4_gemm_simple<0><<<grid, 256, 0, stream>>>(a_codes, a_scales, m, b_codes, b_scales, n, k,
-                                                   out, ldo, tn);
-  else
-    mxfp4_gemm_simple<1><<<grid, 256, 0, stream>>>(a_codes, a_scales, m, b_codes, b_scales, n, k,
-                                                   out, ldo, tn);
-  return hipGetLastError();
+  return k % 128 == 0 ? gemm_of<false>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
+                                       out_dtype, ldo, stream)
+                      : gemm_of<true>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
+                                      out_dtype, ldo, stream);
 }
 
 }  // namespace nvfp4

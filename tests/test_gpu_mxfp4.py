@@ -134,7 +134,14 @@ GEMMS = [(1, 1, 32), (1, 5, 64), (2, 3, 96), (7, 33, 160), (16, 16, 128), (17, 3
          (256, 256, 1280), (257, 255, 1056), (300, 520, 2048), (513, 300, 5152)]
 
 
-@pytest.mark.parametrize("m,n,k", GEMMS)
+# one operand of few rows against each number of rows that a workgroup takes,
+# both ways round, one and several rounds of loads
+STREAMS = [(1, 4097, 96), (9, 8200, 128), (16, 13000, 160), (3, 16500, 64), (20, 4100, 256),
+           (31, 9000, 288), (32, 12400, 128), (50, 5000, 1024), (64, 9000, 96), (5, 100, 9216),
+           (40, 33, 12320), (4100, 7, 224), (13000, 32, 128), (9001, 64, 160), (70, 17, 640)]
+
+
+@pytest.mark.parametrize("m,n,k", GEMMS + STREAMS)
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_gemm(m, n, k, dt):
     _say("gemm", m, n, k, dt)

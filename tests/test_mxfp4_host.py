@@ -147,6 +147,7 @@ def test_gemm_validation(lib):
             assert gemm(lib, **{kw: v}) != OK, (kw, v)
     assert gemm(lib, k=48) == INVALID
     assert gemm(lib, ldo=6) == INVALID
+    assert gemm(lib, k=(1 << 22) + 32) == UNSUPPORTED
     assert gemm(lib, dt=2) == UNSUPPORTED
     assert gemm(lib, out=at(4) + 2) == MISALIGNED
     for on in (0, 1, 2, 3):
