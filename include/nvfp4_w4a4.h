@@ -487,10 +487,11 @@ int64_t prompt_attention_workspace(int64_t n_tokens, int64_t n_heads,
  *
  * mxfp4_gemm -- Y = A B^T for A [m][k] and B [n][k] (K-major weights) in the
  *   layout above; codes and scale arrays 16-byte aligned (else MISALIGNED).
- *   m, n >= 1, k >= 32, k % 32 == 0, k <= 2^22 (else UNSUPPORTED).  out [m][ldo] of out_dtype (F32 or BF16), ldo >= n, 4-byte
- *   aligned, no overlap with the inputs.  Products and scales are exact, sums
- *   are binary32, BF16 is rounded to nearest even from that.  A row with a
- *   scale byte of 0xFF gives NaN.
+ *   m, n >= 1, k >= 32, k % 32 == 0, k <= 2^22 (else UNSUPPORTED).  out
+ *   [m][ldo] of out_dtype (F32 or BF16), ldo >= n, 4-byte aligned, no overlap
+ *   with the inputs.  Products and scales are exact, sums are binary32, BF16 is
+ *   rounded to nearest even from that.  A row with a scale byte of 0xFF gives
+ *   NaN.
  */
 int mxfp4_quantize(const void* x, int x_dtype, int64_t rows, int64_t k, int64_t ldx,
                    uint8_t* codes, uint8_t* scales, void* stream);
@@ -512,7 +513,7 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  *   q, k         device, BF16 [n_tokens][n_k_heads][dk]; v BF16 [n_tokens]
  *                [n_heads][dv]; each with token and head strides in elements
  *                (columns of a fused projection's output, say), 16-byte
- *                aligned, strides multiples of 8.
+ *                aligned, strides multiples of 8, token strides below 2^24.
  *   n_heads      a multiple of n_k_heads; head h reads query and key head
  *                h / (n_heads / n_k_heads).  n_tokens * n_heads <= 2^27,
  *                n_requests * n_heads <= 2^20.
@@ -547,8 +548,11 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  *                0); calls in flight together need one each.
  * out, state and workspace must not overlap each other or an input.
  *
- * The state, its sums and the gates' products are binary32; out is rounded
- * once.
+ * The state, its sums and the gates' products are binary32.  Requests of few
+ * tokens are computed in binary32 throughout, with one rounding of out; longer
+ * ones in chunks, whose matrix products take the state and the corrected values
+ * as sums of two or three bf16 numbers (state: relative error of some 2^-19)
+ * and, for out, the state and the scores as bf16 numbers.
  */
 int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                   const void* k, int64_t k_token_stride, int64_t k_head_stride,

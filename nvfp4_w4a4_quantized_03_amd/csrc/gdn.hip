@@ -16,6 +16,7 @@
 
 #include <stdint.h>
 
+#include "gemm_common.h"
 #include "internal.h"
 
 namespace nvfp4 {
@@ -45,6 +46,10 @@ struct GdnArgs {
   int n_tokens, n_requests, n_heads, group, dv;
   float scale;
   int normalize;
+  int least;                          // tokens that a request of the launch has at least
+  int most;                           // and at most
+  uint8_t* records;                   // of chunks and heads
+  float* decays;                      // of whole chunks
 };
 
 __device__ __forceinline__ float bf16_value(unsigned short x) {
@@ -94,7 +99,7 @@ gdn_tokens_kernel(const GdnArgs a) {
   const int rh = blockIdx.x / slices;
   const int r = rh / a.n_heads, h = rh - r * a.n_heads, hk = h / a.group;
   const Request rq = request_of(a, r);
-  if (rq.len == 0) return;
+  if (rq.len < a.least || rq.len > a.most) return;
   const int row0 = (lane >> 2) * R, col = c0 + (lane & 3) * 4;
   float* sp = a.state + rq.slot * a.slot_stride + (static_cast<int64_t>(h) * DK + row0) * a.dv + col;
   f32x4 s[R];
@@ -150,6 +155,620 @@ gdn_tokens_kernel(const GdnArgs a) {
   for (int i = 0; i < R; ++i) *reinterpret_cast<f32x4*>(sp + i * a.dv) = s[i];
 }
 
+// ---------------------------------------------------------------------------
+// Chunks of 64 tokens.
+//
+// With g_i the product of the decays up to token i of a chunk and S0 the state
+// before it,
+//   (1 + A) U = diag(beta) (V - diag(g) K S0),  A_ij = beta_i g_i/g_j k_i.k_j, j < i
+//   O = scale (diag(g) Q S0 + P U),             P_ij = g_i/g_j q_i.k_j, j <= i
+//   S = g_64 S0 + K^T diag(g_64 / g_j) U
+// (plain rule: U = V).  What does not depend on the state is made for all chunks
+// at once by prepare_kernel: T = (1 + A)^-1 diag(beta), P and the factors of rows,
+// a record of a chunk and head.  Then scan_kernel goes through a request's chunks
+// in order with the products that do: K S0, T R, Q S0, P U, K^T U.
+//
+// A wave of scan_kernel owns 16 columns of S, U and O and all their rows.  With
+// rows down and columns across lanes, the sums of one product (lane l: column
+// l % 16, four rows of a tile of 16 from 4 (l / 16)) are the right operand of
+// the next as they are, if the tiles' rows are taken in this order: tile 2 s + e,
+// row 4 g + i is row 32 s + 8 g + 4 e + i, so that a lane's eight values of two
+// tiles are the eight of a k-step of 32.  So nothing passes between lanes or
+// waves, and only left operands (K, Q, K^T, T, P) are read from LDS.
+//
+// Precision.  K, Q and V are bf16, so products with them are exact; norms,
+// decays, beta and the scale are factors of rows in binary32.  S, U, R and T are
+// binary32 and enter products as sums of bf16 numbers: S, R and T two (16 bits),
+// U into the state three (24), the diagonal of T none at all.  Outputs take S and
+// P in bf16 and U in two: roundings of the size of the output's own.  Decays are
+// added up as base-2 logarithms in binary64, so that a gate close to zero takes
+// nothing from the others.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 64;
+// A record: the lower triangles of T (high and low parts, six operands of 1 KB
+// each) and of P (six), and four factors of each row.  Operand index of the tile
+// of rows t and the k-step s <= t / 2.
+__device__ __forceinline__ constexpr int tri(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
+template <bool DELTA>
+struct Record {
+  static constexpr int kT = 0;                               // high, then low
+  static constexpr int kP = DELTA ? 12 * 1024 : 0;
+  static constexpr int kRows = kP + 6 * 1024;                // a, b, c, beta: 64 floats each
+  static constexpr int kBytes = kRows + 1024;
+};
+
+__device__ __forceinline__ unsigned pack_bf16(float x, float y) {
+  const bf16x2 p = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
+  return __builtin_bit_cast(unsigned, p);
+}
+// x and y less the two bf16 numbers that p holds
+__device__ __forceinline__ void less_bf16(float* x, float* y, unsigned p) {
+  *x -= __uint_as_float(p << 16);
+  *y -= __uint_as_float(p & 0xFFFF0000u);
+}
+
+// Eight binary32 numbers as sums of N bf16 ones.
+template <int N>
+struct Parts {
+  u32x4 p[N];
+  __device__ __forceinline__ void of(f32x4 x, f32x4 y) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const unsigned u = pack_bf16(x[2 * i], x[2 * i + 1]), w = pack_bf16(y[2 * i], y[2 * i + 1]);
+        p[n][i] = u;
+        p[n][2 + i] = w;
+        if (n + 1 < N) {
+          float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+          less_bf16(&x0, &x1, u);
+          less_bf16(&y0, &y1, w);
+          x[2 * i] = x0; x[2 * i + 1] = x1; y[2 * i] = y0; y[2 * i + 1] = y1;
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// 2^d for d <= 0 in binary64, to binary32's precision
+__device__ __forceinline__ float exp2_of(double d) {
+  const double n = __builtin_rint(d);
+  const int e = n < -1000.0 ? -1000 : static_cast<int>(n);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(static_cast<float>(d - n)), e);
+}
+
+// First chunk slot of request r: floor(rows before / 64) + r leaves every
+// request at least the chunks that it fills, without a prefix sum of its own.
+__device__ __forceinline__ int first_slot(const GdnArgs& a, int r) {
+  const int row = min(max(a.cu[r], 0), a.n_tokens);
+  return row / kChunk + r;
+}
+
+// The request that chunk slot t belongs to, the last r with first_slot(r) <= t;
+// -1 if there is none.  Each round the wave's 64 lanes probe 64 places.
+__device__ __forceinline__ int request_at(const GdnArgs& a, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.n_requests;
+  for (bool first = true; n > 1 || first; first = false) {
+    const int step = (n + 63) >> 6;
+    const bool ok = lane * step < n && first_slot(a, lo + lane * step) <= t;
+    const int count = __popcll(__ballot(ok));
+    if (count == 0) return -1;
+    lo += (count - 1) * step;
+    n = min(step, n - (count - 1) * step);
+  }
+  return lo;
+}
+
+// Rows of [64][DK] bf16 in LDS: 16-byte pieces exchanged by an exclusive or.
+template <int DK>
+struct Rows {
+  static constexpr int kBytes = DK * 2, kPieces = DK / 8;
+  // 16 lanes with consecutive rows, or with rows 0-3, 8-11, 16-19, 24-27
+  // (+ 4), fall on different banks
+  __device__ static __forceinline__ int natural(int row) { return row & (kPieces - 1); }
+  __device__ static __forceinline__ int paired(int row) {
+    return DK == 128 ? (row & 3) | (((row >> 3) & 3) << 2) : ((row >> 1) & 1) | (((row >> 3) & 3) << 1);
+  }
+};
+
+// One chunk and key head a workgroup: products of its keys and queries, then a
+// value head a wave.  The inverse is taken in blocks of 16: those on the diagonal
+// by substitution, a column a lane, the others by products in binary32 (T_ij = -
+// T_ii sum_m A_im T_mj), so no bit is lost to powers of A where keys resemble
+// each other.
+constexpr int kPad = 68;                 // row of 64 floats in LDS
+template <int DK>
+struct PrepareLds {
+  static constexpr int kStage = 2 * kChunk * DK * 2, kProducts = 2 * kChunk * kPad * 4;
+  static constexpr int kShared = kStage > kProducts ? kStage : kProducts;
+  static constexpr int kWave = 32 * kPad * 4;                // T's rows, 32 at a time
+  alignas(16) uint8_t shared[kShared];
+  alignas(16) uint8_t wave[4][kWave];
+  double g[4][kChunk];
+  float beta[4][kChunk];
+  float rk[kChunk], rq[kChunk];
+};
+
+template <int DK, bool DELTA>
+__global__ void __launch_bounds__(256)
+prepare_kernel(const GdnArgs a, int k_heads) {
+  using L = Rows<DK>;
+  using Rec = Record<DELTA>;
+  __shared__ PrepareLds<DK> lds;
+  const int slot = blockIdx.x / k_heads, hk = blockIdx.x - slot * k_heads;
+  const int r = request_at(a, slot);
+  if (r < 0) return;
+  const Request rq = request_of(a, r);
+  const int c = slot - first_slot(a, r);
+  if (rq.len < a.least || c < 0 || c * kChunk >= rq.len) return;
+  const int len = min(rq.len - c * kChunk, kChunk);
+  const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lr = lane & 15, g4 = lane >> 4;
+
+  // K and Q to LDS; rows past the end are zeros
+  for (int i = threadIdx.x; i < 2 * kChunk * L::kPieces; i += blockDim.x) {
+    const int row = (i / L::kPieces) & (kChunk - 1), piece = i & (L::kPieces - 1);
+    const bool is_q = i >= kChunk * L::kPieces;
+    u32x4 x = {0u, 0u, 0u, 0u};
+    if (row < len) {
+      const uint8_t* p = is_q ? a.q + (t0 + row) * a.q_token + hk * a.q_head
+                              : a.k + (t0 + row) * a.k_token + hk * a.k_head;
+      x = *reinterpret_cast<const u32x4*>(p + piece * 16);
+    }
+    *reinterpret_cast<u32x4*>(lds.shared + (is_q ? kChunk * L::kBytes : 0) + row * L::kBytes +
+                              (piece ^ L::natural(row)) * 16) = x;
+  }
+  __syncthreads();
+  auto at = [&](int is_q, int tile, int s) {
+    const int row = tile * 16 + lr;
+    return *reinterpret_cast<const u32x4*>(lds.shared + is_q * kChunk * L::kBytes + row * L::kBytes +
+                                           ((4 * s + g4) ^ L::natural(row)) * 16);
+  };
+  // products of a tile of rows with the tiles of keys up to it; the wave's
+  // results stay in registers until everybody has read K and Q
+  f32x4 kk[4][4], qk[4][4], qq[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int t = wave + n * waves;
+    if (t >= 4) continue;
+    qq[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) kk[n][u] = qk[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      const u32x4 ka = at(0, t, s), qa = at(1, t, s);
+      qq[n] = mma(qa, qa, qq[n]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u <= t) {
+          const u32x4 kb = at(0, u, s);
+          kk[n][u] = mma(ka, kb, kk[n][u]);
+          qk[n][u] = mma(qa, kb, qk[n][u]);
+        }
+    }
+  }
+  __syncthreads();
+  float* const kkp = reinterpret_cast<float*>(lds.shared);
+  float* const qkp = kkp + kChunk * kPad;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int t = wave + n * waves;
+    if (t >= 4) continue;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (u <= t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
+          qkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = qk[n][u][i];
+          if (u == t && 4 * g4 + i == lr) {
+            lds.rk[t * 16 + lr] = a.normalize ? 1.0f / __builtin_sqrtf(kk[n][u][i] + kNormEps) : 1.0f;
+            lds.rq[t * 16 + lr] = a.scale * (a.normalize ? 1.0f / __builtin_sqrtf(qq[n][i] + kNormEps) : 1.0f);
+          }
+        }
+  }
+  __syncthreads();
+
+  double* const g = lds.g[wave];
+  float* const bt = lds.beta[wave];
+  float* const buf = reinterpret_cast<float*>(lds.wave[wave]);
+  for (int hh = wave; hh < a.group; hh += waves) {
+    const int h = hk * a.group + hh;
+    // logarithms of the decays up to each token; a gate of zero is one of
+    // 2^-160, below what binary32 holds
+    double sum = 0.0;
+    float be = 0.0f;
+    if (lane < len) {
+      const float al = a.alpha[(t0 + lane) * a.ld_alpha + h];
+      sum = al > 0.0f ? log2(static_cast<double>(al)) : al == 0.0f ? -160.0 : __builtin_nan("");
+      be = DELTA ? a.beta[(t0 + lane) * a.ld_beta + h] : 1.0f;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double before = __shfl_up(sum, d);
+      if (lane >= d) sum += before;
+    }
+    g[lane] = sum;
+    bt[lane] = be;
+    const double last = __shfl(sum, 63);
+    uint8_t* const rec = a.records + (static_cast<int64_t>(slot) * a.n_heads + h) * Rec::kBytes;
+    {
+      float* const rows = reinterpret_cast<float*>(rec + Rec::kRows);
+      const float gi = exp2_of(sum), rk = lds.rk[lane];
+      rows[lane] = gi * rk;
+      rows[64 + lane] = gi * lds.rq[lane];
+      rows[128 + lane] = rk * exp2_of(last - sum);
+      rows[192 + lane] = be;
+      if (lane == 0) a.decays[static_cast<int64_t>(slot) * a.n_heads + h] = exp2_of(last);
+    }
+    __builtin_amdgcn_wave_barrier();
+
+    if constexpr (DELTA) {
+      // -A: tiles below the diagonal as left operands, those on it in LDS
+      f32x4 na[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = i * 16 + lr;
+        const double gi = g[row];
+        const float f = -bt[row] * lds.rk[row];
+#pragma unroll
+        for (int m = 0; m <= i; ++m) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(kkp + row * kPad + m * 16 + 4 * g4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = m * 16 + 4 * g4 + e;
+            na[i][m][e] = col < row ? f * lds.rk[col] * exp2_of(gi - g[col]) * x[e] : 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(buf + (i * 16 + lr) * 20 + 4 * g4) = na[i][i];
+      __builtin_amdgcn_wave_barrier();
+      // the diagonal blocks' inverses: lane l has column l % 16 of block l / 16
+      float x[16];
+#pragma unroll
+      for (int row = 0; row < 16; ++row) {
+        float sum = row == lr ? 1.0f : 0.0f;
+#pragma unroll
+        for (int m = 0; m < row; m += 4) {
+          const f32x4 w = *reinterpret_cast<const f32x4*>(buf + (g4 * 16 + row) * 20 + m);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (m + e < row) sum = __builtin_fmaf(w[e], x[m + e], sum);
+        }
+        x[row] = sum;
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int row = 0; row < 16; ++row) buf[(g4 * 16 + row) * 20 + lr] = x[row];
+      __builtin_amdgcn_wave_barrier();
+      f32x4 dl[4], t[4][4];              // as left operands; tiles of the inverse
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dl[i] = *reinterpret_cast<const f32x4*>(buf + (i * 16 + lr) * 20 + 4 * g4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[i][i][e] = buf[(i * 16 + 4 * g4 + e) * 20 + lr];
+      }
+      __builtin_amdgcn_wave_barrier();
+      auto times = [](f32x4 left, f32x4 right, f32x4 acc) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], right[e], acc, 0, 0, 0);
+        return acc;
+      };
+#pragma unroll
+      for (int d = 1; d < 4; ++d)
+#pragma unroll
+        for (int j = 0; j + d < 4; ++j) {
+          const int i = j + d;
+          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int m = j; m < i; ++m) acc = times(na[i][m], t[m][j], acc);
+          t[i][j] = times(dl[i], acc, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        }
+      // 32 rows at a time through LDS to the operands' order, times beta,
+      // below the diagonal only
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2 * half + 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              buf[(i * 16 + 4 * g4 + e) * kPad + j * 16 + lr] = j <= 2 * half + i ? t[2 * half + i][j][e] : 0.0f;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int in = 8 * (lr >> 2) + 4 * e + (lr & 3), row = 32 * half + in;
+#pragma unroll
+          for (int s = 0; s <= half; ++s) {
+            const int col = 32 * s + 8 * g4;
+            f32x4 y[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              y[p] = *reinterpret_cast<const f32x4*>(buf + in * kPad + col + 4 * p);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                y[p][q] = col + 4 * p + q < row ? y[p][q] * bt[col + 4 * p + q] : 0.0f;
+            }
+            Parts<2> w;
+            w.of(y[0], y[1]);
+            uint8_t* const dst = rec + Rec::kT + tri(2 * half + e, s) * 1024 + lane * 16;
+            *reinterpret_cast<u32x4*>(dst) = w.p[0];
+            *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    // P
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int row = 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3);
+      const double gi = g[row];
+      const float f = lds.rq[row];
+#pragma unroll
+      for (int s = 0; s <= t / 2; ++s) {
+        const int col = 32 * s + 8 * g4;
+        u32x4 p;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float y[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int j = col + e + q;
+            y[q] = j <= row ? f * lds.rk[j] * exp2_of(gi - g[j]) * qkp[row * kPad + j] : 0.0f;
+          }
+          p[e / 2] = pack_bf16(y[0], y[1]);
+        }
+        *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(t, s) * 1024 + lane * 16) = p;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Two waves a workgroup, 32 columns of a request's head.
+constexpr int kScanWaves = 2, kScanCols = 16 * kScanWaves;
+template <int DK, bool DELTA>
+struct ScanLds {
+  static constexpr int kK = 0, kQ = kChunk * DK * 2, kRec = 2 * kQ;
+  static constexpr int kV = kRec + Record<DELTA>::kBytes;
+  static constexpr int kBytes = kV + kChunk * kScanCols * 2;
+};
+
+__device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  const unsigned lo = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p));
+  const unsigned hi = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(
+      reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, 0x7FFFFFFF, 0x00020000);
+}
+
+template <int DK, bool DELTA>
+__global__ void __launch_bounds__(kScanWaves * 64, 1)
+scan_kernel(const GdnArgs a) {
+  using L = Rows<DK>;
+  using Rec = Record<DELTA>;
+  using S = ScanLds<DK, DELTA>;
+  constexpr unsigned kOut = 0x80000000u;           // beyond the resources' range
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[S::kBytes], lds1[S::kBytes];
+  const int slices = (a.dv + kScanCols - 1) / kScanCols;
+  // the slices of a head and the heads of a key head on one XCD, whose L2 they
+  // share
+  int bid = blockIdx.x;
+  if (gridDim.x % 8 == 0) bid = (bid % 8) * (gridDim.x / 8) + bid / 8;
+  const int slice = bid % slices, rh = bid / slices;
+  const int r = rh / a.n_heads, h = rh - r * a.n_heads, hk = h / a.group;
+  const Request rq = request_of(a, r);
+  if (rq.len < a.least) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, g4 = lane >> 4;
+  const int col = slice * kScanCols + wave * 16 + lr;
+  const bool mine = slice * kScanCols + wave * 16 < a.dv;      // the last slice may be half
+  const int chunks = (rq.len + kChunk - 1) / kChunk;
+  const int64_t slot0 = first_slot(a, r);
+
+  // state: tile t, element i is row 32 (t / 2) + 8 g4 + 4 (t % 2) + i
+  f32x4 st[DK / 16];
+  float* const sp = a.state + rq.slot * a.slot_stride + static_cast<int64_t>(h) * DK * a.dv;
+#pragma unroll
+  for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      st[t][i] = mine && !rq.fresh
+                     ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * static_cast<int64_t>(a.dv) + col]
+                     : 0.0f;
+
+  // a chunk's loads to LDS: keys and queries, the record, values
+  auto load = [&](int c, uint8_t* lds) {
+    const int len = min(rq.len - c * kChunk, kChunk);
+    const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
+    const __amdgpu_buffer_rsrc_t kr = resource(a.k + t0 * a.k_token + hk * a.k_head);
+    const __amdgpu_buffer_rsrc_t qr = resource(a.q + t0 * a.q_token + hk * a.q_head);
+    const __amdgpu_buffer_rsrc_t vr = resource(a.v + t0 * a.v_token + h * a.v_head);
+    const __amdgpu_buffer_rsrc_t rr =
+        resource(a.records + ((slot0 + c) * a.n_heads + h) * Rec::kBytes);
+    constexpr int kTile = kChunk * DK * 2 / 1024;              // loads of 1 KB
+#pragma unroll
+    for (int i = 0; i < kTile / kScanWaves; ++i) {
+      const int n = i * kScanWaves + wave, at = n * 64 + lane;
+      const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
+      lds_buf16(kr, lds + S::kK + n * 1024,
+                row < len ? static_cast<unsigned>(row * a.k_token) + piece * 16 : kOut, 0);
+      lds_buf16(qr, lds + S::kQ + n * 1024,
+                row < len ? static_cast<unsigned>(row * a.q_token) + piece * 16 : kOut, 0);
+    }
+    constexpr int kRecs = Rec::kBytes / 1024;
+#pragma unroll
+    for (int i = 0; i < (kRecs + kScanWaves - 1) / kScanWaves; ++i) {
+      const int n = i * kScanWaves + wave;
+      if (n < kRecs) lds_buf16(rr, lds + S::kRec + n * 1024, n * 1024 + lane * 16, 0);
+    }
+    constexpr int kVs = kChunk * kScanCols * 2 / 1024, kVp = kScanCols / 8;
+#pragma unroll
+    for (int i = 0; i < kVs / kScanWaves; ++i) {
+      const int n = i * kScanWaves + wave, at = n * 64 + lane;
+      const int row = at / kVp, c8 = slice * kScanCols + at % kVp * 8;
+      lds_buf16(vr, lds + S::kV + n * 1024,
+                row < len && c8 < a.dv ? static_cast<unsigned>(row * a.v_token) + c8 * 2 : kOut, 0);
+    }
+  };
+
+  f32x4 o[4];
+  int held = -1;                                   // chunk whose outputs o has
+  auto store = [&]() {
+    if (held < 0 || !mine) return;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = held * kChunk + 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
+        if (row < rq.len)
+          *reinterpret_cast<unsigned short*>(a.out + (rq.first + static_cast<int64_t>(row)) * a.out_token +
+                                             h * a.out_head + col * 2) = bf16_bits(o[t][i]);
+      }
+  };
+
+  // rows of left operands: tile t, lane's row lr
+  const int prow = 8 * (lr >> 2) + (lr & 3);
+  auto chunk = [&](int c, uint8_t* lds, uint8_t* next) {
+    // this wave's loads have landed and, behind the barrier, the other's; and
+    // nobody reads the other place any more
+    __builtin_amdgcn_s_waitcnt(0);
+    stage_barrier();
+    if (c + 1 < chunks) load(c + 1, next);
+    store();                                       // of the chunk before
+    const float decay = a.decays[(slot0 + c) * a.n_heads + h];
+    const float* const rows = reinterpret_cast<const float*>(lds + S::kRec + Rec::kRows);
+    auto of_rows = [&](int which, int t) {
+      return *reinterpret_cast<const f32x4*>(rows + 64 * which + 32 * (t / 2) + 8 * g4 + 4 * (t % 2));
+    };
+    auto left = [&](int base, int t, int s) {      // of [64][DK] rows
+      const int row = 32 * (t / 2) + 4 * (t % 2) + prow;
+      return *reinterpret_cast<const u32x4*>(lds + base + row * L::kBytes +
+                                             ((4 * s + g4) ^ L::paired(row)) * 16);
+    };
+    auto triangle = [&](int base, int t, int s) {
+      return *reinterpret_cast<const u32x4*>(lds + S::kRec + base + tri(t, s) * 1024 + lane * 16);
+    };
+    f32x4 u[4], qs[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) u[t] = qs[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      Parts<2> x;
+      x.of(st[2 * s], st[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (DELTA) {
+          const u32x4 k = left(S::kK, t, s);
+          u[t] = mma(k, x.p[0], u[t]);
+          u[t] = mma(k, x.p[1], u[t]);
+        }
+        qs[t] = mma(left(S::kQ, t, s), x.p[0], qs[t]);
+      }
+    }
+    // V, and R = V - g K S0
+    f32x4 v[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const s16x4 x = read_tr(lds + S::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
+                              wave * 32 + (lr & 3) * 8);
+      const f32x4 f = of_rows(0, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[t][i] = bf16_value(static_cast<unsigned short>(x[i]));
+        if constexpr (DELTA) v[t][i] = __builtin_fmaf(-f[i], u[t][i], v[t][i]);
+      }
+    }
+    if constexpr (DELTA) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = of_rows(3, t) * v[t];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Parts<2> x;
+        x.of(v[2 * s], v[2 * s + 1]);
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) {
+          const u32x4 hi = triangle(Rec::kT, t, s), lo = triangle(Rec::kT + 6 * 1024, t, s);
+          u[t] = mma(hi, x.p[0], u[t]);
+          u[t] = mma(hi, x.p[1], u[t]);
+          u[t] = mma(lo, x.p[0], u[t]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = v[t];
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = of_rows(1, t) * qs[t];
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t) st[t] *= decay;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Parts<DELTA ? 2 : 1> x;                      // the plain rule's U is bf16
+      x.of(u[2 * s], u[2 * s + 1]);
+#pragma unroll
+      for (int t = 2 * s; t < 4; ++t) {
+        const u32x4 p = triangle(Rec::kP, t, s);
+        o[t] = mma(p, x.p[0], o[t]);
+        if constexpr (DELTA) o[t] = mma(p, x.p[1], o[t]);
+      }
+      Parts<3> y;
+      y.of(u[2 * s] * of_rows(2, 2 * s), u[2 * s + 1] * of_rows(2, 2 * s + 1));
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t) {
+        // K^T: rows of tile t, tokens 32 s + 8 g4 + 0 .. 7
+        const int piece = 4 * (t / 2) + (lr & 3);
+        s16x4 w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 32 * s + 8 * g4 + 4 * e + (lr >> 2);
+          w[e] = read_tr(lds + S::kK + row * L::kBytes + (piece ^ L::paired(row)) * 16 + 8 * (t % 2));
+        }
+        const u32x4 k = __builtin_bit_cast(u32x4, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) st[t] = mma(k, y.p[n], st[t]);
+      }
+    }
+    held = c;
+  };
+  load(0, lds0);
+  int c = 0;
+  for (; c + 2 <= chunks; c += 2) {
+    chunk(c, lds0, lds1);
+    chunk(c + 1, lds1, lds0);
+  }
+  if (c < chunks) chunk(c, lds0, lds1);
+  store();
+  if (mine)
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * static_cast<int64_t>(a.dv) + col] = st[t][i];
+}
+
 GdnArgs args_of(const GdnCall& c) {
   GdnArgs a = {};
   a.q = static_cast<const uint8_t*>(c.q.p);
@@ -169,23 +788,46 @@ GdnArgs args_of(const GdnCall& c) {
   return a;
 }
 
-template <int DK>
-void launch_tokens(const GdnArgs& a, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.n_requests) * a.n_heads *
-                                              ((a.dv + 63) / 64));
-  if (a.beta) gdn_tokens_kernel<DK, true><<<grid, 256, 0, stream>>>(a);
-  else gdn_tokens_kernel<DK, false><<<grid, 256, 0, stream>>>(a);
+// Requests of at most this many tokens are taken token after token.
+constexpr int kFewTokens = 16;
+
+// Chunk slots of a call (first_slot), and bytes of a slot's records and decay
+int64_t chunk_slots(const GdnCall& c) { return c.n_tokens / kChunk + c.n_requests; }
+int64_t record_bytes(bool delta) {
+  return delta ? Record<true>::kBytes : Record<false>::kBytes;
+}
+
+template <int DK, bool DELTA>
+void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
+  const int64_t rh = c.n_requests * c.n_heads;
+  a.least = 1;
+  a.most = c.max_len > kFewTokens ? kFewTokens : 0x7FFFFFFF;
+  gdn_tokens_kernel<DK, DELTA>
+      <<<static_cast<unsigned>(rh * ((c.dv + 63) / 64)), 256, 0, stream>>>(a);
+  if (c.max_len <= kFewTokens) return;
+  a.least = kFewTokens + 1;
+  a.records = static_cast<uint8_t*>(c.workspace);
+  a.decays = reinterpret_cast<float*>(a.records + chunk_slots(c) * c.n_heads * record_bytes(DELTA));
+  const unsigned waves = a.group < 4 ? a.group : 4;
+  prepare_kernel<DK, DELTA>
+      <<<static_cast<unsigned>(chunk_slots(c) * c.n_k_heads), waves * 64, 0, stream>>>(
+          a, static_cast<int>(c.n_k_heads));
+  scan_kernel<DK, DELTA>
+      <<<static_cast<unsigned>(rh * ((c.dv + kScanCols - 1) / kScanCols)), kScanWaves * 64, 0, stream>>>(a);
 }
 
 }  // namespace
 
-int64_t gdn_workspace(const GdnCall&) { return 0; }
+int64_t gdn_workspace(const GdnCall& c) {
+  if (c.max_len <= kFewTokens) return 0;
+  return chunk_slots(c) * c.n_heads * (record_bytes(c.beta != nullptr) + 4);
+}
 
 hipError_t launch_gdn(const GdnCall& c, hipStream_t stream) {
   if (c.n_tokens == 0) return hipSuccess;
   const GdnArgs a = args_of(c);
-  if (c.dk == 64) launch_tokens<64>(a, stream);
-  else launch_tokens<128>(a, stream);
+  if (c.dk == 64) c.beta ? launch_dk<64, true>(a, c, stream) : launch_dk<64, false>(a, c, stream);
+  else c.beta ? launch_dk<128, true>(a, c, stream) : launch_dk<128, false>(a, c, stream);
   return hipGetLastError();
 }
 

@@ -16,7 +16,8 @@ def gdn(q, k, v, alpha, beta, state, scale, normalize=False):
     roundings, each a sum of norms without cancellation.  Per head and column,
     n_t = alpha n_{t-1} + |k_t| |u_t| bounds the state's column norm, w_t =
     alpha w_{t-1} + n_t + |k_t| |beta v_t| sums what every step rounds; size =
-    scale |q_t| n_t [tokens, heads, dv], reach = (scale |q_t| w_t, last w)."""
+    scale |q_t| n_t [tokens, heads, dv], reach = (scale |q_t| w_t, the last w,
+    the last n)."""
     q, k, v, alpha, S = (np.array(t, dtype=np.float64) for t in (q, k, v, alpha, state))
     tokens, heads, dv = v.shape
     group = heads // k.shape[1]
@@ -42,4 +43,4 @@ def gdn(q, k, v, alpha, beta, state, scale, normalize=False):
         n = a * n + kn * np.abs(u)
         w = a * w + n + kn * wrote
         size[t], reach[t] = scale * qn * n, scale * qn * w
-    return o, S, size, (reach, w)
+    return o, S, size, (reach, w, n)

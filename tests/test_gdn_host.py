@@ -81,9 +81,9 @@ def test_normalize_divides_by_norms():
 def test_bounds_hold_the_values():
     """size bounds the outputs and the last n the state, by Cauchy-Schwarz."""
     q, k, v, alpha, beta, s0 = case(np.random.default_rng(5), 20, 2, 4, 8, 6)
-    o, s, size, (reach, w) = oracle.gdn(q, k, v, alpha, beta, s0, 0.5, True)
+    o, s, size, (reach, w, n) = oracle.gdn(q, k, v, alpha, beta, s0, 0.5, True)
     assert (np.abs(o) <= size * (1 + 1e-12)).all() and (size <= reach * (1 + 1e-12)).all()
-    assert (np.abs(s).max(1) <= w).all()
+    assert (np.sqrt((s * s).sum(1)) <= n * (1 + 1e-12)).all() and (n <= w).all()
 
 
 # ---------------------------------------------------------------- refusals
@@ -120,6 +120,8 @@ def test_validation(lib):
         assert call(lib, dv=dv, vh=528, vt=2112, oh=528, ot=2112, ss=1 << 20) == UNSUPPORTED
     assert call(lib, q=at(0) + 8) == MISALIGNED
     assert call(lib, kt=132) == MISALIGNED
+    for kw in ("qt", "kt", "vt"):
+        assert call(lib, **{kw: 1 << 24}) == INVALID, kw
     assert call(lib, v=at(2) + 4) == MISALIGNED
     assert call(lib, out=at(9) + 4) == MISALIGNED
     assert call(lib, state=at(5) + 8) == MISALIGNED
@@ -136,6 +138,14 @@ def test_validation(lib):
 def test_workspace(lib):
     f = lib.gdn_attention_workspace
     assert f(5, 2, 4, 64, 32, 2, 1, 1) == 0                # single tokens need none
+    need = f(100, 2, 4, 64, 32, 2, 90, 1)
+    assert need > f(100, 2, 4, 64, 32, 2, 90, 0) > 0       # the plain rule needs less
+    big = dict(tokens=100, most=90)
+    assert call(lib, ws=None, wn=need, **big) == INVALID
+    assert call(lib, wn=need - 1, **big) == INVALID
+    assert call(lib, ws=at(10) + 8, wn=need, **big) == MISALIGNED
+    for on in range(10):
+        assert call(lib, ws=at(on), wn=need, **big) == INVALID, on
     assert f(5, 2, 3, 64, 32, 2, 4, 1) == -1
     assert f(5, 2, 4, 65, 32, 2, 4, 1) == -1
     assert f(5, 2, 4, 64, 33, 2, 4, 1) == -1
