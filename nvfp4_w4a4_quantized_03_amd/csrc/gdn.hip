@@ -543,17 +543,47 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   }
 }
 
-// Two waves a workgroup, 32 columns of a request's head.
-constexpr int kScanWaves = 2, kScanCols = 16 * kScanWaves;
+// The scan: 32 columns of a request's head a workgroup, 16 a pair of waves.
+//
+// What the next chunk waits for is the way from one state to the next, so that
+// is all that a state wave does: K S0, R, U, K^T U.  An output wave takes Q S0 +
+// P U of the chunk before, from operands that the state wave leaves in LDS as it
+// makes them, and brings the next chunks' K, T, V and Q, P from memory to LDS.
+// One barrier a chunk: behind it the state waves are at chunk c, the output waves
+// at chunk c - 1; K, T, V of c + 1 and Q, P of c arrive.
+constexpr int kScanCols = 32;
 template <int DK, bool DELTA>
 struct ScanLds {
-  static constexpr int kK = 0, kQ = kChunk * DK * 2, kRec = 2 * kQ;
-  static constexpr int kV = kRec + Record<DELTA>::kBytes;
-  static constexpr int kBytes = kV + kChunk * kScanCols * 2;
+  using Rec = Record<DELTA>;
+  // K, T, the factors of rows, V
+  static constexpr int kK = 0, kT = kChunk * DK * 2, kRows = kT + (DELTA ? 12 * 1024 : 0);
+  static constexpr int kV = kRows + 1024, kIn = kV + kChunk * kScanCols * 2;
+  // Q, P and the factors of rows
+  static constexpr int kQ = 0, kP = kChunk * DK * 2, kOut = kP + 7 * 1024;
+  // of each pair of waves: S0 (high parts), U (two parts)
+  static constexpr int kS = 0, kU = DK / 32 * 1024, kPair = kU + 4 * 1024;
 };
 
-__device__ __forceinline__ s16x4 read_tr(const uint8_t* p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+// LDS by its own address space: with generic pointers the compiler joins the
+// paths of the two places of a buffer and then tests the pointer for null.
+#define NVFP4_LDS __attribute__((address_space(3)))
+typedef NVFP4_LDS uint8_t lds_t;
+
+template <class T>
+__device__ __forceinline__ T lds_read(const lds_t* p) {
+  return *(const NVFP4_LDS T*)(p);
+}
+__device__ __forceinline__ void lds_write(lds_t* p, u32x4 x) { *(NVFP4_LDS u32x4*)(p) = x; }
+
+__device__ __forceinline__ s16x4 read_tr(const lds_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((NVFP4_LDS s16x4*)(p));
+}
+
+// 16 bytes a lane straight to LDS at lds + 16 * lane
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, lds_t* lds, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (NVFP4_LDS void*)lds, 16, off, 0, 0, 0);
+#endif
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) {
@@ -564,209 +594,301 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) 
       reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, 0x7FFFFFFF, 0x00020000);
 }
 
+// A request's head and columns, and a lane's place in them.
+struct Scan {
+  Request rq;
+  int h, hk, slice, pair, chunks;
+  int64_t slot0;
+  bool mine;                           // the last slice may have one pair's columns only
+};
+
+// Loads to LDS of one of the two output waves: of n loads of 1 KB every other.
 template <int DK, bool DELTA>
-__global__ void __launch_bounds__(kScanWaves * 64, 1)
-scan_kernel(const GdnArgs a) {
+struct ScanLoads {
   using L = Rows<DK>;
+  using Lds = ScanLds<DK, DELTA>;
   using Rec = Record<DELTA>;
-  using S = ScanLds<DK, DELTA>;
-  constexpr unsigned kOut = 0x80000000u;           // beyond the resources' range
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[S::kBytes], lds1[S::kBytes];
-  const int slices = (a.dv + kScanCols - 1) / kScanCols;
-  // the slices of a head and the heads of a key head on one XCD, whose L2 they
-  // share
-  int bid = blockIdx.x;
-  if (gridDim.x % 8 == 0) bid = (bid % 8) * (gridDim.x / 8) + bid / 8;
-  const int slice = bid % slices, rh = bid / slices;
-  const int r = rh / a.n_heads, h = rh - r * a.n_heads, hk = h / a.group;
-  const Request rq = request_of(a, r);
-  if (rq.len < a.least) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 15, g4 = lane >> 4;
-  const int col = slice * kScanCols + wave * 16 + lr;
-  const bool mine = slice * kScanCols + wave * 16 < a.dv;      // the last slice may be half
-  const int chunks = (rq.len + kChunk - 1) / kChunk;
-  const int64_t slot0 = first_slot(a, r);
+  static constexpr unsigned kOutside = 0x80000000u;            // of the resources' range
 
-  // state: tile t, element i is row 32 (t / 2) + 8 g4 + 4 (t % 2) + i
-  f32x4 st[DK / 16];
-  float* const sp = a.state + rq.slot * a.slot_stride + static_cast<int64_t>(h) * DK * a.dv;
+  // keys or queries of a chunk
+  static __device__ __forceinline__ void rows(const uint8_t* base, int64_t stride, int len, int odd,
+                                              lds_t* lds) {
+    const __amdgpu_buffer_rsrc_t rsrc = resource(base);
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      st[t][i] = mine && !rq.fresh
-                     ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * static_cast<int64_t>(a.dv) + col]
-                     : 0.0f;
-
-  // a chunk's loads to LDS: keys and queries, the record, values
-  auto load = [&](int c, uint8_t* lds) {
-    const int len = min(rq.len - c * kChunk, kChunk);
-    const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
-    const __amdgpu_buffer_rsrc_t kr = resource(a.k + t0 * a.k_token + hk * a.k_head);
-    const __amdgpu_buffer_rsrc_t qr = resource(a.q + t0 * a.q_token + hk * a.q_head);
-    const __amdgpu_buffer_rsrc_t vr = resource(a.v + t0 * a.v_token + h * a.v_head);
-    const __amdgpu_buffer_rsrc_t rr =
-        resource(a.records + ((slot0 + c) * a.n_heads + h) * Rec::kBytes);
-    constexpr int kTile = kChunk * DK * 2 / 1024;              // loads of 1 KB
-#pragma unroll
-    for (int i = 0; i < kTile / kScanWaves; ++i) {
-      const int n = i * kScanWaves + wave, at = n * 64 + lane;
+    for (int i = 0; i < kChunk * DK * 2 / 2048; ++i) {
+      const int n = 2 * i + odd, at = n * 64 + lane;
       const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
-      lds_buf16(kr, lds + S::kK + n * 1024,
-                row < len ? static_cast<unsigned>(row * a.k_token) + piece * 16 : kOut, 0);
-      lds_buf16(qr, lds + S::kQ + n * 1024,
-                row < len ? static_cast<unsigned>(row * a.q_token) + piece * 16 : kOut, 0);
+      load_lds(rsrc, lds + n * 1024,
+                row < len ? static_cast<unsigned>(row * stride) + piece * 16 : kOutside);
     }
-    constexpr int kRecs = Rec::kBytes / 1024;
+  }
+  template <int KB>
+  static __device__ __forceinline__ void linear(__amdgpu_buffer_rsrc_t rsrc, int from, int odd,
+                                                lds_t* lds) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i < (kRecs + kScanWaves - 1) / kScanWaves; ++i) {
-      const int n = i * kScanWaves + wave;
-      if (n < kRecs) lds_buf16(rr, lds + S::kRec + n * 1024, n * 1024 + lane * 16, 0);
+    for (int i = 0; i < (KB + 1) / 2; ++i) {
+      const int n = 2 * i + odd;
+      if (n < KB) load_lds(rsrc, lds + n * 1024, from + n * 1024 + lane * 16);
     }
-    constexpr int kVs = kChunk * kScanCols * 2 / 1024, kVp = kScanCols / 8;
+  }
+  static __device__ __forceinline__ void in(const GdnArgs& a, const Scan& w, int c, int odd,
+                                            lds_t* lds) {
+    if (c >= w.chunks) return;
+    const int len = min(w.rq.len - c * kChunk, kChunk), lane = threadIdx.x & 63;
+    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
+    rows(a.k + t0 * a.k_token + w.hk * a.k_head, a.k_token, len, odd, lds + Lds::kK);
+    const __amdgpu_buffer_rsrc_t rec =
+        resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes);
+    if constexpr (DELTA) linear<12>(rec, Rec::kT, odd, lds + Lds::kT);
+    if (odd) load_lds(rec, lds + Lds::kRows, Rec::kRows + lane * 16);
+    const __amdgpu_buffer_rsrc_t vr = resource(a.v + t0 * a.v_token + w.h * a.v_head);
+    constexpr int kPieces = kScanCols / 8;
 #pragma unroll
-    for (int i = 0; i < kVs / kScanWaves; ++i) {
-      const int n = i * kScanWaves + wave, at = n * 64 + lane;
-      const int row = at / kVp, c8 = slice * kScanCols + at % kVp * 8;
-      lds_buf16(vr, lds + S::kV + n * 1024,
-                row < len && c8 < a.dv ? static_cast<unsigned>(row * a.v_token) + c8 * 2 : kOut, 0);
+    for (int i = 0; i < kChunk * kScanCols * 2 / 2048; ++i) {
+      const int n = 2 * i + odd, at = n * 64 + lane;
+      const int row = at / kPieces, col = w.slice * kScanCols + at % kPieces * 8;
+      load_lds(vr, lds + Lds::kV + n * 1024,
+                row < len && col < a.dv ? static_cast<unsigned>(row * a.v_token) + col * 2 : kOutside);
     }
-  };
+  }
+  static __device__ __forceinline__ void out(const GdnArgs& a, const Scan& w, int c, int odd,
+                                             lds_t* lds) {
+    if (c >= w.chunks) return;
+    const int len = min(w.rq.len - c * kChunk, kChunk);
+    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
+    rows(a.q + t0 * a.q_token + w.hk * a.q_head, a.q_token, len, odd, lds + Lds::kQ);
+    linear<7>(resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes), Rec::kP, odd,
+              lds + Lds::kP);
+  }
+};
 
-  f32x4 o[4];
-  int held = -1;                                   // chunk whose outputs o has
-  auto store = [&]() {
-    if (held < 0 || !mine) return;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = held * kChunk + 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
-        if (row < rq.len)
-          *reinterpret_cast<unsigned short*>(a.out + (rq.first + static_cast<int64_t>(row)) * a.out_token +
-                                             h * a.out_head + col * 2) = bf16_bits(o[t][i]);
-      }
-  };
+// Four factors of the rows of tile t, the `which`-th of each
+__device__ __forceinline__ f32x4 row_factors(const lds_t* lds, int which, int t) {
+  const int g4 = (threadIdx.x & 63) >> 4;
+  return lds_read<f32x4>(lds + 256 * which + (32 * (t / 2) + 8 * g4 + 4 * (t % 2)) * 4);
+}
 
-  // rows of left operands: tile t, lane's row lr
-  const int prow = 8 * (lr >> 2) + (lr & 3);
-  auto chunk = [&](int c, uint8_t* lds, uint8_t* next) {
-    // this wave's loads have landed and, behind the barrier, the other's; and
-    // nobody reads the other place any more
-    __builtin_amdgcn_s_waitcnt(0);
-    stage_barrier();
-    if (c + 1 < chunks) load(c + 1, next);
-    store();                                       // of the chunk before
-    const float decay = a.decays[(slot0 + c) * a.n_heads + h];
-    const float* const rows = reinterpret_cast<const float*>(lds + S::kRec + Rec::kRows);
-    auto of_rows = [&](int which, int t) {
-      return *reinterpret_cast<const f32x4*>(rows + 64 * which + 32 * (t / 2) + 8 * g4 + 4 * (t % 2));
-    };
-    auto left = [&](int base, int t, int s) {      // of [64][DK] rows
-      const int row = 32 * (t / 2) + 4 * (t % 2) + prow;
-      return *reinterpret_cast<const u32x4*>(lds + base + row * L::kBytes +
-                                             ((4 * s + g4) ^ L::paired(row)) * 16);
-    };
-    auto triangle = [&](int base, int t, int s) {
-      return *reinterpret_cast<const u32x4*>(lds + S::kRec + base + tri(t, s) * 1024 + lane * 16);
-    };
-    f32x4 u[4], qs[4];
+// Left operand of tile t, k-step s, of [64][DK] rows
+template <int DK>
+__device__ __forceinline__ u32x4 left_rows(const lds_t* lds, int t, int s) {
+  const int lr = threadIdx.x & 15, g4 = (threadIdx.x & 63) >> 4;
+  const int row = 32 * (t / 2) + 4 * (t % 2) + 8 * (lr >> 2) + (lr & 3);
+  return lds_read<u32x4>(lds + row * Rows<DK>::kBytes + ((4 * s + g4) ^ Rows<DK>::paired(row)) * 16);
+}
+
+__device__ __forceinline__ u32x4 operand_at(const lds_t* lds, int n) {
+  return lds_read<u32x4>(lds + n * 1024 + (threadIdx.x & 63) * 16);
+}
+
+// A state wave's chunk: the state to the next, what the outputs take of it to
+// `xc`.  State tile t, element i is row 32 (t / 2) + 8 g4 + 4 (t % 2) + i.
+template <int DK, bool DELTA>
+__device__ __forceinline__ void state_chunk(f32x4 (&st)[DK / 16], float decay, int pair,
+                                            const lds_t* in, lds_t* xc) {
+  using Lds = ScanLds<DK, DELTA>;
+  using L = Rows<DK>;
+  const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
+  f32x4 u[4], v[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) u[t] = qs[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < 4; ++t) u[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      Parts<2> x;
-      x.of(st[2 * s], st[2 * s + 1]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if constexpr (DELTA) {
-          const u32x4 k = left(S::kK, t, s);
-          u[t] = mma(k, x.p[0], u[t]);
-          u[t] = mma(k, x.p[1], u[t]);
-        }
-        qs[t] = mma(left(S::kQ, t, s), x.p[0], qs[t]);
-      }
-    }
-    // V, and R = V - g K S0
-    f32x4 v[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const s16x4 x = read_tr(lds + S::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
-                              wave * 32 + (lr & 3) * 8);
-      const f32x4 f = of_rows(0, t);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[t][i] = bf16_value(static_cast<unsigned short>(x[i]));
-        if constexpr (DELTA) v[t][i] = __builtin_fmaf(-f[i], u[t][i], v[t][i]);
-      }
-    }
+  for (int s = 0; s < DK / 32; ++s) {
+    Parts<DELTA ? 2 : 1> x;
+    x.of(st[2 * s], st[2 * s + 1]);
+    lds_write(xc + Lds::kS + s * 1024 + lane * 16, x.p[0]);
     if constexpr (DELTA) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] = of_rows(3, t) * v[t];
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Parts<2> x;
-        x.of(v[2 * s], v[2 * s + 1]);
-#pragma unroll
-        for (int t = 2 * s; t < 4; ++t) {
-          const u32x4 hi = triangle(Rec::kT, t, s), lo = triangle(Rec::kT + 6 * 1024, t, s);
-          u[t] = mma(hi, x.p[0], u[t]);
-          u[t] = mma(hi, x.p[1], u[t]);
-          u[t] = mma(lo, x.p[0], u[t]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] = v[t];
+        for (int t = 0; t < 4; ++t) u[t] = mma(left_rows<DK>(in + Lds::kK, t, s), x.p[n], u[t]);
     }
+  }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = of_rows(1, t) * qs[t];
+  for (int t = 0; t < 4; ++t) {
+    const s16x4 x = read_tr(in + Lds::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
+                            pair * 32 + (lr & 3) * 8);
+    const f32x4 f = row_factors(in + Lds::kRows, 0, t);
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t) st[t] *= decay;
+    for (int i = 0; i < 4; ++i) {
+      v[t][i] = bf16_value(static_cast<unsigned short>(x[i]));
+      if constexpr (DELTA) v[t][i] = __builtin_fmaf(-f[i], u[t][i], v[t][i]);   // R
+    }
+  }
+  if constexpr (DELTA) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) u[t] = row_factors(in + Lds::kRows, 3, t) * v[t];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      Parts<DELTA ? 2 : 1> x;                      // the plain rule's U is bf16
-      x.of(u[2 * s], u[2 * s + 1]);
+      Parts<2> x;
+      x.of(v[2 * s], v[2 * s + 1]);
 #pragma unroll
       for (int t = 2 * s; t < 4; ++t) {
-        const u32x4 p = triangle(Rec::kP, t, s);
-        o[t] = mma(p, x.p[0], o[t]);
-        if constexpr (DELTA) o[t] = mma(p, x.p[1], o[t]);
-      }
-      Parts<3> y;
-      y.of(u[2 * s] * of_rows(2, 2 * s), u[2 * s + 1] * of_rows(2, 2 * s + 1));
-#pragma unroll
-      for (int t = 0; t < DK / 16; ++t) {
-        // K^T: rows of tile t, tokens 32 s + 8 g4 + 0 .. 7
-        const int piece = 4 * (t / 2) + (lr & 3);
-        s16x4 w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 32 * s + 8 * g4 + 4 * e + (lr >> 2);
-          w[e] = read_tr(lds + S::kK + row * L::kBytes + (piece ^ L::paired(row)) * 16 + 8 * (t % 2));
-        }
-        const u32x4 k = __builtin_bit_cast(u32x4, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-        for (int n = 0; n < 3; ++n) st[t] = mma(k, y.p[n], st[t]);
+        const u32x4 hi = operand_at(in + Lds::kT, tri(t, s)), lo = operand_at(in + Lds::kT, 6 + tri(t, s));
+        u[t] = mma(hi, x.p[0], u[t]);
+        u[t] = mma(hi, x.p[1], u[t]);
+        u[t] = mma(lo, x.p[0], u[t]);
       }
     }
-    held = c;
-  };
-  load(0, lds0);
-  int c = 0;
-  for (; c + 2 <= chunks; c += 2) {
-    chunk(c, lds0, lds1);
-    chunk(c + 1, lds1, lds0);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) u[t] = v[t];
   }
-  if (c < chunks) chunk(c, lds0, lds1);
-  store();
-  if (mine)
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
+  for (int t = 0; t < DK / 16; ++t) st[t] *= decay;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * static_cast<int64_t>(a.dv) + col] = st[t][i];
+  for (int s = 0; s < 2; ++s) {
+    Parts<3> y;
+    y.of(u[2 * s] * row_factors(in + Lds::kRows, 2, 2 * s),
+         u[2 * s + 1] * row_factors(in + Lds::kRows, 2, 2 * s + 1));
+    u32x4 k[DK / 16];
+#pragma unroll
+    for (int t = 0; t < DK / 16; ++t) {
+      // K^T: rows of tile t, tokens 32 s + 8 g4 + 0 .. 7
+      const int piece = 4 * (t / 2) + (lr & 3);
+      s16x4 w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 32 * s + 8 * g4 + 4 * e + (lr >> 2);
+        w[e] = read_tr(in + Lds::kK + row * L::kBytes + (piece ^ L::paired(row)) * 16 + 8 * (t % 2));
+      }
+      k[t] = __builtin_bit_cast(u32x4, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t) st[t] = mma(k[t], y.p[n], st[t]);
+    Parts<DELTA ? 2 : 1> x;                        // the plain rule's U is bf16
+    x.of(u[2 * s], u[2 * s + 1]);
+#pragma unroll
+    for (int n = 0; n < (DELTA ? 2 : 1); ++n)
+      lds_write(xc + Lds::kU + (2 * s + n) * 1024 + lane * 16, x.p[n]);
+  }
+}
+
+// An output wave's chunk.
+template <int DK, bool DELTA>
+__device__ __forceinline__ void output_chunk(f32x4 (&o)[4], const lds_t* out, const lds_t* xc) {
+  using Lds = ScanLds<DK, DELTA>;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < DK / 32; ++s) {
+    const u32x4 x = operand_at(xc + Lds::kS, s);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(out + Lds::kQ, t, s), x, o[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] *= row_factors(out + Lds::kP + 6 * 1024, 1, t);
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int n = 0; n < (DELTA ? 2 : 1); ++n) {
+      const u32x4 x = operand_at(xc + Lds::kU, 2 * s + n);
+#pragma unroll
+      for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(out + Lds::kP, tri(t, s)), x, o[t]);
+    }
+}
+
+template <int DK, bool DELTA>
+__global__ void __launch_bounds__(256, 1)
+scan_kernel(const GdnArgs a, int items) {
+  using Lds = ScanLds<DK, DELTA>;
+  using Loads = ScanLoads<DK, DELTA>;
+  __shared__ __attribute__((aligned(1024))) uint8_t in0_[Lds::kIn], in1_[Lds::kIn], out0_[Lds::kOut],
+      out1_[Lds::kOut], xc0_[2 * Lds::kPair], xc1_[2 * Lds::kPair];
+  lds_t *const in0 = (lds_t*)in0_, *const in1 = (lds_t*)in1_, *const out0 = (lds_t*)out0_,
+        *const out1 = (lds_t*)out1_, *const xc0 = (lds_t*)xc0_, *const xc1 = (lds_t*)xc1_;
+  const int slices = (a.dv + kScanCols - 1) / kScanCols;
+  const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the slices of a head and the heads of a key head on one XCD, whose L2 they
+  // share; requests of few tokens are passed over
+  int first = blockIdx.x;
+  if (gridDim.x % 8 == 0) first = (first % 8) * (gridDim.x / 8) + first / 8;
+  for (int item = first; item < items; item += gridDim.x) {
+    Scan w;
+    const int rh = item / slices, r = rh / a.n_heads;
+    w.rq = request_of(a, r);
+    if (w.rq.len < a.least) continue;
+    w.slice = item - rh * slices;
+    w.h = rh - r * a.n_heads;
+    w.hk = w.h / a.group;
+    w.pair = wave & 1;
+    w.chunks = (w.rq.len + kChunk - 1) / kChunk;
+    w.slot0 = first_slot(a, r);
+    const int col = w.slice * kScanCols + w.pair * 16 + lr;
+    w.mine = w.slice * kScanCols + w.pair * 16 < a.dv;
+
+    if (wave < 2) {
+      float* const sp = a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv + col;
+      const float* const decays = a.decays + w.slot0 * a.n_heads + w.h;
+      f32x4 st[DK / 16];
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st[t][i] = w.mine && !w.rq.fresh ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] : 0.0f;
+      auto step = [&](int c, const lds_t* in, lds_t* xc) __attribute__((always_inline)) {
+        const float decay = decays[static_cast<int64_t>(c) * a.n_heads];
+        // what the outputs take is in LDS before the barrier
+        __builtin_amdgcn_s_waitcnt(0);
+        stage_barrier();
+        state_chunk<DK, DELTA>(st, decay, w.pair, in, xc + w.pair * Lds::kPair);
+      };
+      int c = 0;
+      for (; c + 2 <= w.chunks; c += 2) {
+        step(c, in0, xc0);
+        step(c + 1, in1, xc1);
+      }
+      if (c < w.chunks) step(c, in0, xc0);
+      if (w.mine)
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] = st[t][i];
+      __builtin_amdgcn_s_waitcnt(0);
+      stage_barrier();
+    } else {
+      uint8_t* const op = a.out + w.rq.first * a.out_token + w.h * a.out_head + col * 2;
+      f32x4 o[4];
+      // outputs of chunk c, behind the barrier after theirs, so that nobody
+      // waits for them
+      auto store = [&](int c) {
+        if (c < 0 || !w.mine) return;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = c * kChunk + 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
+            if (row < w.rq.len)
+              *reinterpret_cast<unsigned short*>(op + row * a.out_token) = bf16_bits(o[t][i]);
+          }
+      };
+      Loads::in(a, w, 0, w.pair, in0);
+      // behind the barrier the state waves are at chunk c
+      auto step = [&](int c, lds_t* in_next, const lds_t* out, lds_t* out_next,
+                      const lds_t* xc) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt(0);
+        stage_barrier();
+        store(c - 2);
+        Loads::in(a, w, c + 1, w.pair, in_next);
+        Loads::out(a, w, c, w.pair, out_next);
+        if (c > 0) output_chunk<DK, DELTA>(o, out, xc + w.pair * Lds::kPair);
+      };
+      int c = 0;
+      for (; c + 2 <= w.chunks + 1; c += 2) {
+        step(c, in1, out1, out0, xc1);
+        step(c + 1, in0, out0, out1, xc0);
+      }
+      if (c <= w.chunks) step(c, in1, out1, out0, xc1);
+      store(w.chunks - 1);
+    }
+    // the next item's loads and operands find LDS free
+    __syncthreads();
+  }
 }
 
 GdnArgs args_of(const GdnCall& c) {
@@ -787,6 +909,10 @@ GdnArgs args_of(const GdnCall& c) {
   a.dv = static_cast<int>(c.dv); a.scale = c.scale; a.normalize = c.normalize;
   return a;
 }
+
+// Workgroups of the scan, which go on to further items: passing over a request of
+// few tokens costs less there than starting a workgroup for it does.
+constexpr int kScanGrid = 1024;
 
 // Requests of at most this many tokens are taken token after token.
 constexpr int kFewTokens = 16;
@@ -812,8 +938,9 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   prepare_kernel<DK, DELTA>
       <<<static_cast<unsigned>(chunk_slots(c) * c.n_k_heads), waves * 64, 0, stream>>>(
           a, static_cast<int>(c.n_k_heads));
+  const int items = static_cast<int>(rh * ((c.dv + kScanCols - 1) / kScanCols));
   scan_kernel<DK, DELTA>
-      <<<static_cast<unsigned>(rh * ((c.dv + kScanCols - 1) / kScanCols)), kScanWaves * 64, 0, stream>>>(a);
+      <<<items < kScanGrid ? items : kScanGrid, 256, 0, stream>>>(a, items);
 }
 
 }  // namespace
