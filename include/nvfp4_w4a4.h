@@ -542,7 +542,8 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  *   normalize    nonzero: q and k are divided by sqrt(sum x^2 + 1e-6) over
  *                their dk elements first (the delta rule wants unit keys).
  *   out          device, out, BF16 [n_tokens][n_heads][dv] with its own
- *                strides, multiples of 4, 8-byte aligned.
+ *                strides, multiples of 4 (token stride below 2^24), 8-byte
+ *                aligned.
  *   workspace    device, 16-byte aligned, of the bytes that
  *                gdn_attention_workspace returns for the same sizes (NULL if
  *                0); calls in flight together need one each.

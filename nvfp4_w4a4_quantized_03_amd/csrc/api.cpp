@@ -724,7 +724,8 @@ int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
   if (st != NVFP4_OK) return st;
   // 32-bit offsets within the 64 rows of a chunk
   constexpr int64_t kStride = int64_t(1) << 24;
-  if (q_token_stride >= kStride || k_token_stride >= kStride || v_token_stride >= kStride)
+  if (q_token_stride >= kStride || k_token_stride >= kStride || v_token_stride >= kStride ||
+      out_token_stride >= kStride)
     return NVFP4_ERR_INVALID_VALUE;
   const int64_t need = nvfp4::gdn_workspace(c);
   if (need < 0 || workspace_bytes < need || (need > 0 && !workspace))

@@ -207,8 +207,10 @@ __device__ __forceinline__ unsigned pack_bf16(float x, float y) {
   const bf16x2 p = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
   return __builtin_bit_cast(unsigned, p);
 }
-// x and y less the two bf16 numbers that p holds
+// x and y less the two bf16 numbers that p holds (opaque, or the compiler rounds
+// x and y again, one by one)
 __device__ __forceinline__ void less_bf16(float* x, float* y, unsigned p) {
+  asm("" : "+v"(p));
   *x -= __uint_as_float(p << 16);
   *y -= __uint_as_float(p & 0xFFFF0000u);
 }
@@ -284,29 +286,56 @@ struct Rows {
 };
 
 // One chunk and key head a workgroup: products of its keys and queries, then a
-// value head a wave.  The inverse is taken in blocks of 16: those on the diagonal
-// by substitution, a column a lane, the others by products in binary32 (T_ij = -
-// T_ii sum_m A_im T_mj), so no bit is lost to powers of A where keys resemble
-// each other.
+// value head a wave.
+//
+// Decays between tokens of different blocks of 16 are products of two factors,
+// from the one to the start of the other's block and from there: both at most 1,
+// so neither overflows, and few exponentials are left (D_ij = e_i f_j; within a
+// block each has its own).  The inverse is taken in blocks of 16: those on the
+// diagonal by substitution, a column a lane, the others by products in binary32
+// (T_ij = - T_ii sum_m A_im T_mj), so no bit is lost to powers of A where keys
+// resemble each other.
 constexpr int kPad = 68;                 // row of 64 floats in LDS
-template <int DK>
+template <int DK, int WAVES>
 struct PrepareLds {
   static constexpr int kStage = 2 * kChunk * DK * 2, kProducts = 2 * kChunk * kPad * 4;
   static constexpr int kShared = kStage > kProducts ? kStage : kProducts;
-  static constexpr int kWave = 32 * kPad * 4;                // T's rows, 32 at a time
+  struct Wave {
+    float rows[32 * kPad];               // T's or P's, 32 at a time
+    double g[kChunk];                    // logarithms of the decays up to each token
+    float e[kChunk], f[3][kChunk];       // factors of rows; of columns, for blocks 1 to 3
+    float beta[kChunk];
+  };
   alignas(16) uint8_t shared[kShared];
-  alignas(16) uint8_t wave[4][kWave];
-  double g[4][kChunk];
-  float beta[4][kChunk];
-  float rk[kChunk], rq[kChunk];
+  alignas(16) Wave wave[WAVES];
+  alignas(16) float rk[kChunk], rq[kChunk];
 };
 
-template <int DK, bool DELTA>
-__global__ void __launch_bounds__(256)
+// 32 rows of T or P from LDS (buf, of tiles 2 half and 2 half + 1) as left
+// operands
+template <class F>
+__device__ __forceinline__ void operand_rows(const float* buf, int half, F&& put) {
+  const int lr = threadIdx.x & 15, g4 = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int in = 8 * (lr >> 2) + 4 * e + (lr & 3);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s > half) continue;
+      const int col = 32 * s + 8 * g4;
+      put(2 * half + e, s, 32 * half + in, col,
+          *reinterpret_cast<const f32x4*>(buf + in * kPad + col),
+          *reinterpret_cast<const f32x4*>(buf + in * kPad + col + 4));
+    }
+  }
+}
+
+template <int DK, bool DELTA, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 2)
 prepare_kernel(const GdnArgs a, int k_heads) {
   using L = Rows<DK>;
   using Rec = Record<DELTA>;
-  __shared__ PrepareLds<DK> lds;
+  __shared__ PrepareLds<DK, WAVES> lds;
   const int slot = blockIdx.x / k_heads, hk = blockIdx.x - slot * k_heads;
   const int r = request_at(a, slot);
   if (r < 0) return;
@@ -315,11 +344,13 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   if (rq.len < a.least || c < 0 || c * kChunk >= rq.len) return;
   const int len = min(rq.len - c * kChunk, kChunk);
   const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, g4 = lane >> 4;
 
   // K and Q to LDS; rows past the end are zeros
-  for (int i = threadIdx.x; i < 2 * kChunk * L::kPieces; i += blockDim.x) {
+#pragma unroll
+  for (int n = 0; n < 2 * kChunk * L::kPieces / (WAVES * 64); ++n) {
+    const int i = n * WAVES * 64 + threadIdx.x;
     const int row = (i / L::kPieces) & (kChunk - 1), piece = i & (L::kPieces - 1);
     const bool is_q = i >= kChunk * L::kPieces;
     u32x4 x = {0u, 0u, 0u, 0u};
@@ -337,13 +368,13 @@ prepare_kernel(const GdnArgs a, int k_heads) {
     return *reinterpret_cast<const u32x4*>(lds.shared + is_q * kChunk * L::kBytes + row * L::kBytes +
                                            ((4 * s + g4) ^ L::natural(row)) * 16);
   };
-  // products of a tile of rows with the tiles of keys up to it; the wave's
-  // results stay in registers until everybody has read K and Q
-  f32x4 kk[4][4], qk[4][4], qq[4];
+  // products of a tile of rows with the tiles of keys up to it; they stay in
+  // registers until everybody has read K and Q
+  constexpr int kTiles = 4 / WAVES;
+  f32x4 kk[kTiles][4], qk[kTiles][4], qq[kTiles];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int t = wave + n * waves;
-    if (t >= 4) continue;
+  for (int n = 0; n < kTiles; ++n) {
+    const int t = wave + n * WAVES;
     qq[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < 4; ++u) kk[n][u] = qk[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -364,9 +395,8 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   float* const kkp = reinterpret_cast<float*>(lds.shared);
   float* const qkp = kkp + kChunk * kPad;
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int t = wave + n * waves;
-    if (t >= 4) continue;
+  for (int n = 0; n < kTiles; ++n) {
+    const int t = wave + n * WAVES;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (u <= t)
@@ -382,13 +412,11 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   }
   __syncthreads();
 
-  double* const g = lds.g[wave];
-  float* const bt = lds.beta[wave];
-  float* const buf = reinterpret_cast<float*>(lds.wave[wave]);
-  for (int hh = wave; hh < a.group; hh += waves) {
+  auto& own = lds.wave[wave];
+  float* const buf = own.rows;
+  for (int hh = wave; hh < a.group; hh += WAVES) {
     const int h = hk * a.group + hh;
-    // logarithms of the decays up to each token; a gate of zero is one of
-    // 2^-160, below what binary32 holds
+    // a gate of zero counts as 2^-160, below what binary32 holds
     double sum = 0.0;
     float be = 0.0f;
     if (lane < len) {
@@ -401,20 +429,42 @@ prepare_kernel(const GdnArgs a, int k_heads) {
       const double before = __shfl_up(sum, d);
       if (lane >= d) sum += before;
     }
-    g[lane] = sum;
-    bt[lane] = be;
     const double last = __shfl(sum, 63);
     uint8_t* const rec = a.records + (static_cast<int64_t>(slot) * a.n_heads + h) * Rec::kBytes;
     {
+      const float rk = lds.rk[lane], gi = exp2_of(sum);
       float* const rows = reinterpret_cast<float*>(rec + Rec::kRows);
-      const float gi = exp2_of(sum), rk = lds.rk[lane];
       rows[lane] = gi * rk;
       rows[64 + lane] = gi * lds.rq[lane];
       rows[128 + lane] = rk * exp2_of(last - sum);
       rows[192 + lane] = be;
       if (lane == 0) a.decays[static_cast<int64_t>(slot) * a.n_heads + h] = exp2_of(last);
+      own.g[lane] = sum;
+      own.beta[lane] = be;
+      own.e[lane] = exp2_of(sum - __shfl(sum, lane & 48));
+#pragma unroll
+      for (int b = 1; b < 4; ++b) {
+        const double start = __shfl(sum, 16 * b);
+        own.f[b - 1][lane] = lane < 16 * b ? rk * exp2_of(start - sum) : 0.0f;
+      }
     }
     __builtin_amdgcn_wave_barrier();
+
+    // decays times the columns' norms of tile (i, m), of row i 16 + lr, columns
+    // m 16 + 4 g4 + 0 .. 3
+    f32x4 within[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double gi = own.g[i * 16 + lr];
+      const f32x4 rk = *reinterpret_cast<const f32x4*>(lds.rk + i * 16 + 4 * g4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        within[i][e] = 4 * g4 + e <= lr ? rk[e] * exp2_of(gi - own.g[i * 16 + 4 * g4 + e]) : 0.0f;
+    }
+    auto decay = [&](int i, int m) {
+      if (i == m) return within[i];
+      return own.e[i * 16 + lr] * *reinterpret_cast<const f32x4*>(&own.f[i - 1][m * 16 + 4 * g4]);
+    };
 
     if constexpr (DELTA) {
       // -A: tiles below the diagonal as left operands, those on it in LDS
@@ -422,35 +472,30 @@ prepare_kernel(const GdnArgs a, int k_heads) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = i * 16 + lr;
-        const double gi = g[row];
-        const float f = -bt[row] * lds.rk[row];
+        const float f = -own.beta[row] * lds.rk[row];
 #pragma unroll
         for (int m = 0; m <= i; ++m) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(kkp + row * kPad + m * 16 + 4 * g4);
+          na[i][m] = f * decay(i, m) * *reinterpret_cast<const f32x4*>(kkp + row * kPad + m * 16 + 4 * g4);
+          if (m == i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = m * 16 + 4 * g4 + e;
-            na[i][m][e] = col < row ? f * lds.rk[col] * exp2_of(gi - g[col]) * x[e] : 0.0f;
-          }
+            for (int e = 0; e < 4; ++e) na[i][i][e] = 4 * g4 + e < lr ? na[i][i][e] : 0.0f;
         }
+        *reinterpret_cast<f32x4*>(buf + row * 20 + 4 * g4) = na[i][i];
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f32x4*>(buf + (i * 16 + lr) * 20 + 4 * g4) = na[i][i];
       __builtin_amdgcn_wave_barrier();
       // the diagonal blocks' inverses: lane l has column l % 16 of block l / 16
       float x[16];
 #pragma unroll
       for (int row = 0; row < 16; ++row) {
-        float sum = row == lr ? 1.0f : 0.0f;
+        float y = row == lr ? 1.0f : 0.0f;
 #pragma unroll
         for (int m = 0; m < row; m += 4) {
           const f32x4 w = *reinterpret_cast<const f32x4*>(buf + (g4 * 16 + row) * 20 + m);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (m + e < row) sum = __builtin_fmaf(w[e], x[m + e], sum);
+            if (m + e < row) y = __builtin_fmaf(w[e], x[m + e], y);
         }
-        x[row] = sum;
+        x[row] = y;
       }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -492,76 +537,67 @@ prepare_kernel(const GdnArgs a, int k_heads) {
             for (int e = 0; e < 4; ++e)
               buf[(i * 16 + 4 * g4 + e) * kPad + j * 16 + lr] = j <= 2 * half + i ? t[2 * half + i][j][e] : 0.0f;
         __builtin_amdgcn_wave_barrier();
+        operand_rows(buf, half, [&](int tile, int s, int row, int col, f32x4 y0, f32x4 y1) {
+          y0 *= *reinterpret_cast<const f32x4*>(own.beta + col);
+          y1 *= *reinterpret_cast<const f32x4*>(own.beta + col + 4);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int in = 8 * (lr >> 2) + 4 * e + (lr & 3), row = 32 * half + in;
-#pragma unroll
-          for (int s = 0; s <= half; ++s) {
-            const int col = 32 * s + 8 * g4;
-            f32x4 y[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              y[p] = *reinterpret_cast<const f32x4*>(buf + in * kPad + col + 4 * p);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                y[p][q] = col + 4 * p + q < row ? y[p][q] * bt[col + 4 * p + q] : 0.0f;
-            }
-            Parts<2> w;
-            w.of(y[0], y[1]);
-            uint8_t* const dst = rec + Rec::kT + tri(2 * half + e, s) * 1024 + lane * 16;
-            *reinterpret_cast<u32x4*>(dst) = w.p[0];
-            *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
+          for (int q = 0; q < 4; ++q) {
+            y0[q] = col + q < row ? y0[q] : 0.0f;
+            y1[q] = col + 4 + q < row ? y1[q] : 0.0f;
           }
-        }
+          Parts<2> w;
+          w.of(y0, y1);
+          uint8_t* const dst = rec + Rec::kT + tri(tile, s) * 1024 + lane * 16;
+          *reinterpret_cast<u32x4*>(dst) = w.p[0];
+          *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
+        });
         __builtin_amdgcn_wave_barrier();
       }
     }
-    // P
+    // P, the same way
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int row = 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3);
-      const double gi = g[row];
-      const float f = lds.rq[row];
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int s = 0; s <= t / 2; ++s) {
-        const int col = 32 * s + 8 * g4;
-        u32x4 p;
+      for (int i = 0; i < 2; ++i) {
+        const int row = (2 * half + i) * 16 + lr;
+        const float f = lds.rq[row];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float y[2];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int j = col + e + q;
-            y[q] = j <= row ? f * lds.rk[j] * exp2_of(gi - g[j]) * qkp[row * kPad + j] : 0.0f;
-          }
-          p[e / 2] = pack_bf16(y[0], y[1]);
+        for (int m = 0; m < 2 * half + 2; ++m) {
+          f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (m <= 2 * half + i)
+            y = f * decay(2 * half + i, m) * *reinterpret_cast<const f32x4*>(qkp + row * kPad + m * 16 + 4 * g4);
+          *reinterpret_cast<f32x4*>(buf + (i * 16 + lr) * kPad + m * 16 + 4 * g4) = y;
         }
-        *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(t, s) * 1024 + lane * 16) = p;
       }
+      __builtin_amdgcn_wave_barrier();
+      operand_rows(buf, half, [&](int tile, int s, int, int, f32x4 y0, f32x4 y1) {
+        *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(tile, s) * 1024 + lane * 16) =
+            u32x4{pack_bf16(y0[0], y0[1]), pack_bf16(y0[2], y0[3]), pack_bf16(y1[0], y1[1]),
+                  pack_bf16(y1[2], y1[3])};
+      });
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
-// The scan: 32 columns of a request's head a workgroup, 16 a pair of waves.
+// The scan: 32 columns of a request's head a workgroup of four waves.
 //
 // What the next chunk waits for is the way from one state to the next, so that
-// is all that a state wave does: K S0, R, U, K^T U.  An output wave takes Q S0 +
-// P U of the chunk before, from operands that the state wave leaves in LDS as it
-// makes them, and brings the next chunks' K, T, V and Q, P from memory to LDS.
-// One barrier a chunk: behind it the state waves are at chunk c, the output waves
-// at chunk c - 1; K, T, V of c + 1 and Q, P of c arrive.
-constexpr int kScanCols = 32;
+// is all that the two state waves do, 16 columns each: K S0, R, U, K^T U.  The
+// output wave takes Q S0 + P U of the chunk before for both, from operands that
+// they leave in LDS as they make them, with Q and P from memory to its registers.
+// The loader brings K, T and V from memory to LDS.  One barrier a chunk: behind it
+// the state waves are at chunk c, the output wave at chunk c - 1, and K, T and V
+// of c + 1 and c + 2 arrive.
+constexpr int kScanCols = 32, kRing = 3;
 template <int DK, bool DELTA>
 struct ScanLds {
   using Rec = Record<DELTA>;
   // K, T, the factors of rows, V
   static constexpr int kK = 0, kT = kChunk * DK * 2, kRows = kT + (DELTA ? 12 * 1024 : 0);
   static constexpr int kV = kRows + 1024, kIn = kV + kChunk * kScanCols * 2;
-  // Q, P and the factors of rows
-  static constexpr int kQ = 0, kP = kChunk * DK * 2, kOut = kP + 7 * 1024;
-  // of each pair of waves: S0 (high parts), U (two parts)
-  static constexpr int kS = 0, kU = DK / 32 * 1024, kPair = kU + 4 * 1024;
+  // of each state wave: S0 (high parts, as operands), U (binary32, by tiles)
+  static constexpr int kS = 0, kU = DK / 32 * 1024, kWave = kU + 4 * 1024;
 };
 
 // LDS by its own address space: with generic pointers the compiler joins the
@@ -597,70 +633,52 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) 
 // A request's head and columns, and a lane's place in them.
 struct Scan {
   Request rq;
-  int h, hk, slice, pair, chunks;
+  int h, hk, slice, chunks;
   int64_t slot0;
   bool mine;                           // the last slice may have one pair's columns only
 };
 
-// Loads to LDS of one of the two output waves: of n loads of 1 KB every other.
+constexpr unsigned kOutside = 0x80000000u;         // of the resources' range
+
+// The loader's loads of K, T, the factors of rows and V of chunk c to LDS.  It
+// always makes kIssues of them (rows and chunks past the end read as zeros),
+// which its waits count.
 template <int DK, bool DELTA>
 struct ScanLoads {
   using L = Rows<DK>;
   using Lds = ScanLds<DK, DELTA>;
   using Rec = Record<DELTA>;
-  static constexpr unsigned kOutside = 0x80000000u;            // of the resources' range
+  static constexpr int kKeys = kChunk * DK * 2 / 1024, kValues = kChunk * kScanCols * 2 / 1024;
+  static constexpr int kIssues = kKeys + (DELTA ? 12 : 0) + 1 + kValues;
 
-  // keys or queries of a chunk
-  static __device__ __forceinline__ void rows(const uint8_t* base, int64_t stride, int len, int odd,
-                                              lds_t* lds) {
-    const __amdgpu_buffer_rsrc_t rsrc = resource(base);
+  static __device__ __forceinline__ void issue(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < kChunk * DK * 2 / 2048; ++i) {
-      const int n = 2 * i + odd, at = n * 64 + lane;
-      const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
-      load_lds(rsrc, lds + n * 1024,
-                row < len ? static_cast<unsigned>(row * stride) + piece * 16 : kOutside);
-    }
-  }
-  template <int KB>
-  static __device__ __forceinline__ void linear(__amdgpu_buffer_rsrc_t rsrc, int from, int odd,
-                                                lds_t* lds) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < (KB + 1) / 2; ++i) {
-      const int n = 2 * i + odd;
-      if (n < KB) load_lds(rsrc, lds + n * 1024, from + n * 1024 + lane * 16);
-    }
-  }
-  static __device__ __forceinline__ void in(const GdnArgs& a, const Scan& w, int c, int odd,
-                                            lds_t* lds) {
-    if (c >= w.chunks) return;
-    const int len = min(w.rq.len - c * kChunk, kChunk), lane = threadIdx.x & 63;
-    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
-    rows(a.k + t0 * a.k_token + w.hk * a.k_head, a.k_token, len, odd, lds + Lds::kK);
-    const __amdgpu_buffer_rsrc_t rec =
-        resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes);
-    if constexpr (DELTA) linear<12>(rec, Rec::kT, odd, lds + Lds::kT);
-    if (odd) load_lds(rec, lds + Lds::kRows, Rec::kRows + lane * 16);
+    const bool real = c < w.chunks;
+    const int len = real ? min(w.rq.len - c * kChunk, kChunk) : 0;
+    const int64_t t0 = w.rq.first + static_cast<int64_t>(real ? c : 0) * kChunk;
+    const __amdgpu_buffer_rsrc_t kr = resource(a.k + t0 * a.k_token + w.hk * a.k_head);
     const __amdgpu_buffer_rsrc_t vr = resource(a.v + t0 * a.v_token + w.h * a.v_head);
-    constexpr int kPieces = kScanCols / 8;
+    const __amdgpu_buffer_rsrc_t rec =
+        resource(a.records + ((w.slot0 + (real ? c : 0)) * a.n_heads + w.h) * Rec::kBytes);
 #pragma unroll
-    for (int i = 0; i < kChunk * kScanCols * 2 / 2048; ++i) {
-      const int n = 2 * i + odd, at = n * 64 + lane;
-      const int row = at / kPieces, col = w.slice * kScanCols + at % kPieces * 8;
-      load_lds(vr, lds + Lds::kV + n * 1024,
-                row < len && col < a.dv ? static_cast<unsigned>(row * a.v_token) + col * 2 : kOutside);
+    for (int n = 0; n < kKeys; ++n) {
+      const int at = n * 64 + lane;
+      const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
+      load_lds(kr, lds + Lds::kK + n * 1024,
+               row < len ? static_cast<unsigned>(row * a.k_token) + piece * 16 : kOutside);
     }
-  }
-  static __device__ __forceinline__ void out(const GdnArgs& a, const Scan& w, int c, int odd,
-                                             lds_t* lds) {
-    if (c >= w.chunks) return;
-    const int len = min(w.rq.len - c * kChunk, kChunk);
-    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
-    rows(a.q + t0 * a.q_token + w.hk * a.q_head, a.q_token, len, odd, lds + Lds::kQ);
-    linear<7>(resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes), Rec::kP, odd,
-              lds + Lds::kP);
+    if constexpr (DELTA)
+#pragma unroll
+      for (int n = 0; n < 12; ++n)
+        load_lds(rec, lds + Lds::kT + n * 1024, real ? Rec::kT + n * 1024 + lane * 16 : kOutside);
+    load_lds(rec, lds + Lds::kRows, real ? Rec::kRows + lane * 16 : kOutside);
+#pragma unroll
+    for (int n = 0; n < kValues; ++n) {
+      const int at = n * 64 + lane;
+      const int row = at / (kScanCols / 8), col = w.slice * kScanCols + at % (kScanCols / 8) * 8;
+      load_lds(vr, lds + Lds::kV + n * 1024,
+               row < len && col < a.dv ? static_cast<unsigned>(row * a.v_token) + col * 2 : kOutside);
+    }
   }
 };
 
@@ -736,6 +754,9 @@ __device__ __forceinline__ void state_chunk(f32x4 (&st)[DK / 16], float decay, i
     for (int t = 0; t < 4; ++t) u[t] = v[t];
   }
 #pragma unroll
+  for (int t = 0; t < 4; ++t)
+    lds_write(xc + Lds::kU + t * 1024 + lane * 16, __builtin_bit_cast(u32x4, u[t]));
+#pragma unroll
   for (int t = 0; t < DK / 16; ++t) st[t] *= decay;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
@@ -759,50 +780,77 @@ __device__ __forceinline__ void state_chunk(f32x4 (&st)[DK / 16], float decay, i
     for (int n = 0; n < 3; ++n)
 #pragma unroll
       for (int t = 0; t < DK / 16; ++t) st[t] = mma(k[t], y.p[n], st[t]);
-    Parts<DELTA ? 2 : 1> x;                        // the plain rule's U is bf16
-    x.of(u[2 * s], u[2 * s + 1]);
-#pragma unroll
-    for (int n = 0; n < (DELTA ? 2 : 1); ++n)
-      lds_write(xc + Lds::kU + (2 * s + n) * 1024 + lane * 16, x.p[n]);
   }
 }
 
-// An output wave's chunk.
+// What the output wave takes from memory for a chunk: rows of Q as left operands,
+// P and the rows' factors.
 template <int DK, bool DELTA>
-__device__ __forceinline__ void output_chunk(f32x4 (&o)[4], const lds_t* out, const lds_t* xc) {
-  using Lds = ScanLds<DK, DELTA>;
+struct ScanQuery {
+  using Rec = Record<DELTA>;
+  u32x4 q[4][DK / 32], p[6];
+  f32x4 rows[4];
+  __device__ __forceinline__ void load(const GdnArgs& a, const Scan& w, int c) {
+    const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
+    const int len = min(w.rq.len - c * kChunk, kChunk);
+    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
+    const __amdgpu_buffer_rsrc_t qr = resource(a.q + t0 * a.q_token + w.hk * a.q_head);
+    const __amdgpu_buffer_rsrc_t rec =
+        resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes);
+    auto get = [](__amdgpu_buffer_rsrc_t rsrc, unsigned off) {
+      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+    };
 #pragma unroll
-  for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < 4; ++t) {
+      const int row = 32 * (t / 2) + 4 * (t % 2) + 8 * (lr >> 2) + (lr & 3);
+      const unsigned at = static_cast<unsigned>(row * a.q_token) + g4 * 16;
 #pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    const u32x4 x = operand_at(xc + Lds::kS, s);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(out + Lds::kQ, t, s), x, o[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < 4; ++t) o[t] *= row_factors(out + Lds::kP + 6 * 1024, 1, t);
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int n = 0; n < (DELTA ? 2 : 1); ++n) {
-      const u32x4 x = operand_at(xc + Lds::kU, 2 * s + n);
-#pragma unroll
-      for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(out + Lds::kP, tri(t, s)), x, o[t]);
+      for (int s = 0; s < DK / 32; ++s) q[t][s] = get(qr, row < len ? at + s * 64 : kOutside);
     }
-}
+#pragma unroll
+    for (int i = 0; i < 6; ++i) p[i] = get(rec, Rec::kP + i * 1024 + lane * 16);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      rows[t] = __builtin_bit_cast(f32x4, get(rec, Rec::kRows + 256 + (32 * (t / 2) + 8 * g4 + 4 * (t % 2)) * 4));
+  }
+  // O of the chunk and of a state wave's columns, with S0 and U from LDS
+  __device__ __forceinline__ void products(f32x4 (&o)[4], const lds_t* xc) const {
+    using Lds = ScanLds<DK, DELTA>;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+      const u32x4 x = operand_at(xc + Lds::kS, s);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] = mma(q[t][s], x, o[t]);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] *= rows[t];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Parts<DELTA ? 2 : 1> x;                      // the plain rule's U is bf16
+      x.of(__builtin_bit_cast(f32x4, operand_at(xc + Lds::kU, 2 * s)),
+           __builtin_bit_cast(f32x4, operand_at(xc + Lds::kU, 2 * s + 1)));
+#pragma unroll
+      for (int n = 0; n < (DELTA ? 2 : 1); ++n)
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) o[t] = mma(p[tri(t, s)], x.p[n], o[t]);
+    }
+  }
+};
 
 template <int DK, bool DELTA>
 __global__ void __launch_bounds__(256, 1)
 scan_kernel(const GdnArgs a, int items) {
   using Lds = ScanLds<DK, DELTA>;
   using Loads = ScanLoads<DK, DELTA>;
-  __shared__ __attribute__((aligned(1024))) uint8_t in0_[Lds::kIn], in1_[Lds::kIn], out0_[Lds::kOut],
-      out1_[Lds::kOut], xc0_[2 * Lds::kPair], xc1_[2 * Lds::kPair];
-  lds_t *const in0 = (lds_t*)in0_, *const in1 = (lds_t*)in1_, *const out0 = (lds_t*)out0_,
-        *const out1 = (lds_t*)out1_, *const xc0 = (lds_t*)xc0_, *const xc1 = (lds_t*)xc1_;
+  using Query = ScanQuery<DK, DELTA>;
+  __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], xc_[2][2 * Lds::kWave];
   const int slices = (a.dv + kScanCols - 1) / kScanCols;
   const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  lds_t* const in = (lds_t*)in_;
+  lds_t* const xc = (lds_t*)xc_;
   // the slices of a head and the heads of a key head on one XCD, whose L2 they
   // share; requests of few tokens are passed over
   int first = blockIdx.x;
@@ -815,35 +863,34 @@ scan_kernel(const GdnArgs a, int items) {
     w.slice = item - rh * slices;
     w.h = rh - r * a.n_heads;
     w.hk = w.h / a.group;
-    w.pair = wave & 1;
     w.chunks = (w.rq.len + kChunk - 1) / kChunk;
     w.slot0 = first_slot(a, r);
-    const int col = w.slice * kScanCols + w.pair * 16 + lr;
-    w.mine = w.slice * kScanCols + w.pair * 16 < a.dv;
+    const int col0 = w.slice * kScanCols;          // the last slice may have 16 columns
 
     if (wave < 2) {
-      float* const sp = a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv + col;
+      const bool mine = col0 + wave * 16 < a.dv;
+      float* const sp = a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv +
+                        col0 + wave * 16 + lr;
       const float* const decays = a.decays + w.slot0 * a.n_heads + w.h;
       f32x4 st[DK / 16];
 #pragma unroll
       for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          st[t][i] = w.mine && !w.rq.fresh ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] : 0.0f;
-      auto step = [&](int c, const lds_t* in, lds_t* xc) __attribute__((always_inline)) {
-        const float decay = decays[static_cast<int64_t>(c) * a.n_heads];
+          st[t][i] = mine && !w.rq.fresh ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] : 0.0f;
+      int place = 0;
+      float of_64 = 0.0f;                          // decays of 64 chunks, one a lane
+      for (int c = 0; c < w.chunks; ++c) {
+        if (c % 64 == 0 && c + lane < w.chunks) of_64 = decays[(c + lane) * static_cast<int64_t>(a.n_heads)];
+        const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of_64), c % 64));
         // what the outputs take is in LDS before the barrier
         __builtin_amdgcn_s_waitcnt(0);
         stage_barrier();
-        state_chunk<DK, DELTA>(st, decay, w.pair, in, xc + w.pair * Lds::kPair);
-      };
-      int c = 0;
-      for (; c + 2 <= w.chunks; c += 2) {
-        step(c, in0, xc0);
-        step(c + 1, in1, xc1);
+        state_chunk<DK, DELTA>(st, decay, wave, in + place * Lds::kIn,
+                               xc + ((c & 1) * 2 + wave) * Lds::kWave);
+        place = place == kRing - 1 ? 0 : place + 1;
       }
-      if (c < w.chunks) step(c, in0, xc0);
-      if (w.mine)
+      if (mine)
 #pragma unroll
         for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
@@ -851,40 +898,48 @@ scan_kernel(const GdnArgs a, int items) {
             sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] = st[t][i];
       __builtin_amdgcn_s_waitcnt(0);
       stage_barrier();
-    } else {
-      uint8_t* const op = a.out + w.rq.first * a.out_token + w.h * a.out_head + col * 2;
-      f32x4 o[4];
-      // outputs of chunk c, behind the barrier after theirs, so that nobody
-      // waits for them
-      auto store = [&](int c) {
-        if (c < 0 || !w.mine) return;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = c * kChunk + 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
-            if (row < w.rq.len)
-              *reinterpret_cast<unsigned short*>(op + row * a.out_token) = bf16_bits(o[t][i]);
-          }
-      };
-      Loads::in(a, w, 0, w.pair, in0);
+    } else if (wave == 2) {
+      Query next, now;
       // behind the barrier the state waves are at chunk c
-      auto step = [&](int c, lds_t* in_next, const lds_t* out, lds_t* out_next,
-                      const lds_t* xc) __attribute__((always_inline)) {
-        __builtin_amdgcn_s_waitcnt(0);
+      for (int c = 0; c <= w.chunks; ++c) {
         stage_barrier();
-        store(c - 2);
-        Loads::in(a, w, c + 1, w.pair, in_next);
-        Loads::out(a, w, c, w.pair, out_next);
-        if (c > 0) output_chunk<DK, DELTA>(o, out, xc + w.pair * Lds::kPair);
-      };
-      int c = 0;
-      for (; c + 2 <= w.chunks + 1; c += 2) {
-        step(c, in1, out1, out0, xc1);
-        step(c + 1, in0, out0, out1, xc0);
+        now = next;
+        if (c < w.chunks) next.load(a, w, c);
+        if (c == 0) continue;
+        const int64_t t0 = w.rq.first + static_cast<int64_t>(c - 1) * kChunk;
+        const int len = min(w.rq.len - (c - 1) * kChunk, kChunk);
+        const __amdgpu_buffer_rsrc_t rsrc =
+            resource(a.out + t0 * a.out_token + w.h * a.out_head + col0 * 2);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          f32x4 o[4];
+          now.products(o, xc + ((~c & 1) * 2 + p) * Lds::kWave);
+          const bool mine = col0 + p * 16 < a.dv;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
+              __builtin_amdgcn_raw_buffer_store_b16(
+                  bf16_bits(o[t][i]), rsrc,
+                  mine && row < len ? static_cast<unsigned>(row * a.out_token) + (p * 16 + lr) * 2 : kOutside,
+                  0, 0);
+            }
+        }
       }
-      if (c <= w.chunks) step(c, in1, out1, out0, xc1);
-      store(w.chunks - 1);
+    } else {
+      Loads::issue(a, w, 0, in);
+      Loads::issue(a, w, 1, in + Lds::kIn);
+      int place = 2;
+      for (int c = 0; c <= w.chunks; ++c) {
+        // chunk c has landed, those of c + 1 may be on their way
+        __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIssues));
+        stage_barrier();
+        Loads::issue(a, w, c + 2, in + place * Lds::kIn);
+        place = place == kRing - 1 ? 0 : place + 1;
+      }
+      // nothing is on its way to LDS when it is used again or released
+      __builtin_amdgcn_s_waitcnt(0);
     }
     // the next item's loads and operands find LDS free
     __syncthreads();
@@ -934,10 +989,11 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   a.least = kFewTokens + 1;
   a.records = static_cast<uint8_t*>(c.workspace);
   a.decays = reinterpret_cast<float*>(a.records + chunk_slots(c) * c.n_heads * record_bytes(DELTA));
-  const unsigned waves = a.group < 4 ? a.group : 4;
-  prepare_kernel<DK, DELTA>
-      <<<static_cast<unsigned>(chunk_slots(c) * c.n_k_heads), waves * 64, 0, stream>>>(
-          a, static_cast<int>(c.n_k_heads));
+  const unsigned blocks = static_cast<unsigned>(chunk_slots(c) * c.n_k_heads);
+  const int k_heads = static_cast<int>(c.n_k_heads);
+  if (a.group == 1) prepare_kernel<DK, DELTA, 1><<<blocks, 64, 0, stream>>>(a, k_heads);
+  else if (a.group == 2) prepare_kernel<DK, DELTA, 2><<<blocks, 128, 0, stream>>>(a, k_heads);
+  else prepare_kernel<DK, DELTA, 4><<<blocks, 256, 0, stream>>>(a, k_heads);
   const int items = static_cast<int>(rh * ((c.dv + kScanCols - 1) / kScanCols));
   scan_kernel<DK, DELTA>
       <<<items < kScanGrid ? items : kScanGrid, 256, 0, stream>>>(a, items);

@@ -120,7 +120,7 @@ def test_validation(lib):
         assert call(lib, dv=dv, vh=528, vt=2112, oh=528, ot=2112, ss=1 << 20) == UNSUPPORTED
     assert call(lib, q=at(0) + 8) == MISALIGNED
     assert call(lib, kt=132) == MISALIGNED
-    for kw in ("qt", "kt", "vt"):
+    for kw in ("qt", "kt", "vt", "ot"):
         assert call(lib, **{kw: 1 << 24}) == INVALID, kw
     assert call(lib, v=at(2) + 4) == MISALIGNED
     assert call(lib, out=at(9) + 4) == MISALIGNED
