@@ -207,10 +207,8 @@ __device__ __forceinline__ unsigned pack_bf16(float x, float y) {
   const bf16x2 p = {static_cast<__bf16>(x), static_cast<__bf16>(y)};
   return __builtin_bit_cast(unsigned, p);
 }
-// x and y less the two bf16 numbers that p holds (opaque, or the compiler rounds
-// x and y again, one by one)
+// x and y less the two bf16 numbers that p holds
 __device__ __forceinline__ void less_bf16(float* x, float* y, unsigned p) {
-  asm("" : "+v"(p));
   *x -= __uint_as_float(p << 16);
   *y -= __uint_as_float(p & 0xFFFF0000u);
 }
@@ -224,7 +222,9 @@ struct Parts {
     for (int n = 0; n < N; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const unsigned u = pack_bf16(x[2 * i], x[2 * i + 1]), w = pack_bf16(y[2 * i], y[2 * i + 1]);
+        unsigned u = pack_bf16(x[2 * i], x[2 * i + 1]), w = pack_bf16(y[2 * i], y[2 * i + 1]);
+        // opaque, or the compiler rounds each number again to take it off
+        if (n + 1 < N) asm("" : "+v"(u), "+v"(w));
         p[n][i] = u;
         p[n][2 + i] = w;
         if (n + 1 < N) {
@@ -580,22 +580,31 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   }
 }
 
-// The scan: 32 columns of a request's head a workgroup of four waves.
+// The scan: 32 columns of a request's head a workgroup of five waves.
 //
 // What the next chunk waits for is the way from one state to the next, so that
 // is all that the two state waves do, 16 columns each: K S0, R, U, K^T U.  The
-// output wave takes Q S0 + P U of the chunk before for both, from operands that
-// they leave in LDS as they make them, with Q and P from memory to its registers.
-// The loader brings K, T and V from memory to LDS.  One barrier a chunk: behind it
-// the state waves are at chunk c, the output wave at chunk c - 1, and K, T and V
-// of c + 1 and c + 2 arrive.
-constexpr int kScanCols = 32, kRing = 3;
+// two output waves take Q S0 and then P U, from operands that a state wave leaves
+// in LDS as it makes them.  The loader brings everything from memory to LDS, K, T
+// and V two chunks ahead.
+//
+// Barriers, two a chunk.  Behind the first of chunk c, its K, T, V and Q have
+// landed, as has P of c - 1, and S0 of c and U of c - 1 are in LDS: the output
+// waves take those to registers.  Behind the second they have, and the state
+// waves may write U of c and S0 of c + 1 over them.
+//
+// One prompt of 32768 tokens, 16 key and 64 value heads of 128 (a workgroup on
+// each CU): 1060 us, 2.1 a chunk, of which the state waves' 98 products alone
+// take 0.65; without output and loader 811, output alone 862 with one output wave
+// for both (1248 in all), loads alone 655.
+constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {
-  using Rec = Record<DELTA>;
-  // K, T, the factors of rows, V
+  // K, T, the factors of rows, V: of three chunks
   static constexpr int kK = 0, kT = kChunk * DK * 2, kRows = kT + (DELTA ? 12 * 1024 : 0);
   static constexpr int kV = kRows + 1024, kIn = kV + kChunk * kScanCols * 2;
+  // Q, P: of two
+  static constexpr int kQ = 0, kP = kChunk * DK * 2, kOut = kP + 6 * 1024;
   // of each state wave: S0 (high parts, as operands), U (binary32, by tiles)
   static constexpr int kS = 0, kU = DK / 32 * 1024, kWave = kU + 4 * 1024;
 };
@@ -622,12 +631,12 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t rsrc, lds_t* lds
 #endif
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base, unsigned bytes = 0x7FFFFFFF) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   const unsigned lo = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p));
   const unsigned hi = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(p >> 32));
   return __builtin_amdgcn_make_buffer_rsrc(
-      reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, 0x7FFFFFFF, 0x00020000);
+      reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, bytes, 0x00020000);
 }
 
 // A request's head and columns, and a lane's place in them.
@@ -640,33 +649,37 @@ struct Scan {
 
 constexpr unsigned kOutside = 0x80000000u;         // of the resources' range
 
-// The loader's loads of K, T, the factors of rows and V of chunk c to LDS.  It
-// always makes kIssues of them (rows and chunks past the end read as zeros),
-// which its waits count.
+// The loader's loads to LDS.  It always makes the same number of them (rows and
+// chunks past the end read as zeros), which its waits count.
 template <int DK, bool DELTA>
 struct ScanLoads {
   using L = Rows<DK>;
   using Lds = ScanLds<DK, DELTA>;
   using Rec = Record<DELTA>;
-  static constexpr int kKeys = kChunk * DK * 2 / 1024, kValues = kChunk * kScanCols * 2 / 1024;
-  static constexpr int kIssues = kKeys + (DELTA ? 12 : 0) + 1 + kValues;
+  static constexpr int kRowLoads = kChunk * DK * 2 / 1024, kValues = kChunk * kScanCols * 2 / 1024;
+  static constexpr int kIn = kRowLoads + (DELTA ? 12 : 0) + 1 + kValues;
 
-  static __device__ __forceinline__ void issue(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
+  static __device__ __forceinline__ void rows(const uint8_t* base, int64_t stride, int len, lds_t* lds) {
+    const __amdgpu_buffer_rsrc_t rsrc = resource(base);
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < kRowLoads; ++n) {
+      const int at = n * 64 + lane;
+      const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
+      load_lds(rsrc, lds + n * 1024,
+               row < len ? static_cast<unsigned>(row * stride) + piece * 16 : kOutside);
+    }
+  }
+  // K, T, the factors of rows and V of chunk c
+  static __device__ __forceinline__ void in(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
     const int lane = threadIdx.x & 63;
     const bool real = c < w.chunks;
     const int len = real ? min(w.rq.len - c * kChunk, kChunk) : 0;
     const int64_t t0 = w.rq.first + static_cast<int64_t>(real ? c : 0) * kChunk;
-    const __amdgpu_buffer_rsrc_t kr = resource(a.k + t0 * a.k_token + w.hk * a.k_head);
+    rows(a.k + t0 * a.k_token + w.hk * a.k_head, a.k_token, len, lds + Lds::kK);
     const __amdgpu_buffer_rsrc_t vr = resource(a.v + t0 * a.v_token + w.h * a.v_head);
     const __amdgpu_buffer_rsrc_t rec =
         resource(a.records + ((w.slot0 + (real ? c : 0)) * a.n_heads + w.h) * Rec::kBytes);
-#pragma unroll
-    for (int n = 0; n < kKeys; ++n) {
-      const int at = n * 64 + lane;
-      const int row = at / L::kPieces, piece = (at & (L::kPieces - 1)) ^ L::paired(row);
-      load_lds(kr, lds + Lds::kK + n * 1024,
-               row < len ? static_cast<unsigned>(row * a.k_token) + piece * 16 : kOutside);
-    }
     if constexpr (DELTA)
 #pragma unroll
       for (int n = 0; n < 12; ++n)
@@ -679,6 +692,21 @@ struct ScanLoads {
       load_lds(vr, lds + Lds::kV + n * 1024,
                row < len && col < a.dv ? static_cast<unsigned>(row * a.v_token) + col * 2 : kOutside);
     }
+  }
+  static __device__ __forceinline__ void q(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
+    const bool real = c < w.chunks;
+    const int len = real ? min(w.rq.len - c * kChunk, kChunk) : 0;
+    const int64_t t0 = w.rq.first + static_cast<int64_t>(real ? c : 0) * kChunk;
+    rows(a.q + t0 * a.q_token + w.hk * a.q_head, a.q_token, len, lds + Lds::kQ);
+  }
+  static __device__ __forceinline__ void p(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
+    const bool real = c < w.chunks;
+    const __amdgpu_buffer_rsrc_t rec =
+        resource(a.records + ((w.slot0 + (real ? c : 0)) * a.n_heads + w.h) * Rec::kBytes);
+#pragma unroll
+    for (int n = 0; n < 6; ++n)
+      load_lds(rec, lds + Lds::kP + n * 1024,
+               real ? Rec::kP + n * 1024 + (threadIdx.x & 63) * 16 : kOutside);
   }
 };
 
@@ -700,156 +728,200 @@ __device__ __forceinline__ u32x4 operand_at(const lds_t* lds, int n) {
   return lds_read<u32x4>(lds + n * 1024 + (threadIdx.x & 63) * 16);
 }
 
-// A state wave's chunk: the state to the next, what the outputs take of it to
-// `xc`.  State tile t, element i is row 32 (t / 2) + 8 g4 + 4 (t % 2) + i.
+// K^T operand of state tile t: its rows, tokens 32 s + 8 g4 + 0 .. 7
+template <int DK>
+__device__ __forceinline__ u32x4 left_columns(const lds_t* k, int t, int s) {
+  const int lr = threadIdx.x & 15, g4 = (threadIdx.x & 63) >> 4;
+  const int piece = 4 * (t / 2) + (lr & 3);
+  s16x4 w[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int row = 32 * s + 8 * g4 + 4 * e + (lr >> 2);
+    w[e] = read_tr(k + row * Rows<DK>::kBytes + (piece ^ Rows<DK>::paired(row)) * 16 + 8 * (t % 2));
+  }
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// End of a scheduling region of a state wave: N products, between which go VALU
+// operations and LDS reads of what comes next.  One wave a SIMD hides nothing
+// under another, so its own operations have to lie under its products.
+template <int N, int VALU, int READS>
+__device__ __forceinline__ void region() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A state wave: 16 columns of the state.  Tile t, element i is row 32 (t / 2) + 8
+// g4 + 4 (t % 2) + i.  `x`: the state as right operands.
 template <int DK, bool DELTA>
-__device__ __forceinline__ void state_chunk(f32x4 (&st)[DK / 16], float decay, int pair,
-                                            const lds_t* in, lds_t* xc) {
+struct State {
   using Lds = ScanLds<DK, DELTA>;
-  using L = Rows<DK>;
-  const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
-  f32x4 u[4], v[4];
+  static constexpr int kTiles = DK / 16, kSteps = DK / 32;
+  f32x4 st[kTiles];
+  Parts<DELTA ? 2 : 1> x[kSteps];
+
+  __device__ __forceinline__ void parts(int from, int to) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t) u[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < kSteps; ++s)
+      if (s >= from && s < to) x[s].of(st[2 * s], st[2 * s + 1]);
+  }
+  // what the output wave takes of the state
+  __device__ __forceinline__ void leave(lds_t* xc) const {
 #pragma unroll
-  for (int s = 0; s < DK / 32; ++s) {
-    Parts<DELTA ? 2 : 1> x;
-    x.of(st[2 * s], st[2 * s + 1]);
-    lds_write(xc + Lds::kS + s * 1024 + lane * 16, x.p[0]);
+    for (int s = 0; s < kSteps; ++s)
+      lds_write(xc + Lds::kS + s * 1024 + (threadIdx.x & 63) * 16, x[s].p[0]);
+  }
+
+  // From the state before a chunk to the one after it; U goes to xc behind the
+  // barrier.
+  __device__ __forceinline__ void chunk(float decay, int wave, const lds_t* in, lds_t* xc) {
+    const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
+    const lds_t* const rows = in + Lds::kRows;
+    f32x4 u[4], v[4], factor[4], last[4];
+    s16x4 vb[4];
+    u32x4 kt[2][kTiles];
+    auto values = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        vb[t] = read_tr(in + Lds::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
+                        wave * 32 + (lr & 3) * 8);
+    };
+    auto columns = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) kt[s][t] = left_columns<DK>(in + Lds::kK, t, s);
+    };
+    auto factors = [&](f32x4 (&f)[4], int which) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) f[t] = row_factors(rows, which, t);
+    };
     if constexpr (DELTA) {
+      u32x4 k[kSteps][4], hi[6], lo[6];
+      f32x4 a[4], beta[4];
+      auto keys = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int t = 0; t < 4; ++t) k[s][t] = left_rows<DK>(in + Lds::kK, t, s);
+      };
+      keys(0);
+      keys(1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] = mma(left_rows<DK>(in + Lds::kK, t, s), x.p[n], u[t]);
-    }
-  }
+      for (int t = 0; t < 4; ++t) u[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const s16x4 x = read_tr(in + Lds::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
-                            pair * 32 + (lr & 3) * 8);
-    const f32x4 f = row_factors(in + Lds::kRows, 0, t);
+      for (int s = 0; s < kSteps; ++s) {
+        if (s + 2 < kSteps) keys(s + 2);
+        if (s == kSteps - 2) {
+          values();
+          factors(a, 0);
+        }
+        if (s == kSteps - 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[t][i] = bf16_value(static_cast<unsigned short>(x[i]));
-      if constexpr (DELTA) v[t][i] = __builtin_fmaf(-f[i], u[t][i], v[t][i]);   // R
-    }
-  }
-  if constexpr (DELTA) {
+          for (int t = 0; t < 4; ++t) {
+            hi[tri(t, 0)] = operand_at(in + Lds::kT, tri(t, 0));
+            lo[tri(t, 0)] = operand_at(in + Lds::kT, 6 + tri(t, 0));
+          }
+          factors(beta, 3);
+        }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) u[t] = row_factors(in + Lds::kRows, 3, t) * v[t];
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Parts<2> x;
-      x.of(v[2 * s], v[2 * s + 1]);
-#pragma unroll
-      for (int t = 2 * s; t < 4; ++t) {
-        const u32x4 hi = operand_at(in + Lds::kT, tri(t, s)), lo = operand_at(in + Lds::kT, 6 + tri(t, s));
-        u[t] = mma(hi, x.p[0], u[t]);
-        u[t] = mma(hi, x.p[1], u[t]);
-        u[t] = mma(lo, x.p[0], u[t]);
+          for (int t = 0; t < 4; ++t) u[t] = mma(k[s][t], x[s].p[n], u[t]);
+        if (s == kSteps - 2) region<8, 0, (kSteps > 2 ? 2 : 1)>();
+        else if (s == kSteps - 1) region<8, 0, 2>();
+        else region<8, 0, 1>();
       }
-    }
-  } else {
+      // R, and beta R, to which the products with T below the diagonal go
 #pragma unroll
-    for (int t = 0; t < 4; ++t) u[t] = v[t];
-  }
+      for (int t = 0; t < 4; ++t) {
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    lds_write(xc + Lds::kU + t * 1024 + lane * 16, __builtin_bit_cast(u32x4, u[t]));
-#pragma unroll
-  for (int t = 0; t < DK / 16; ++t) st[t] *= decay;
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    Parts<3> y;
-    y.of(u[2 * s] * row_factors(in + Lds::kRows, 2, 2 * s),
-         u[2 * s + 1] * row_factors(in + Lds::kRows, 2, 2 * s + 1));
-    u32x4 k[DK / 16];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-      // K^T: rows of tile t, tokens 32 s + 8 g4 + 0 .. 7
-      const int piece = 4 * (t / 2) + (lr & 3);
-      s16x4 w[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 32 * s + 8 * g4 + 4 * e + (lr >> 2);
-        w[e] = read_tr(in + Lds::kK + row * L::kBytes + (piece ^ L::paired(row)) * 16 + 8 * (t % 2));
+        for (int i = 0; i < 4; ++i)
+          v[t][i] = __builtin_fmaf(-a[t][i], u[t][i], bf16_value(static_cast<unsigned short>(vb[t][i])));
+        u[t] = beta[t] * v[t];
       }
-      k[t] = __builtin_bit_cast(u32x4, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      Parts<2> r0, r1;
+      r0.of(v[0], v[1]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) {
+        hi[tri(t, 1)] = operand_at(in + Lds::kT, tri(t, 1));
+        lo[tri(t, 1)] = operand_at(in + Lds::kT, 6 + tri(t, 1));
+      }
+      factors(factor, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      r1.of(v[2], v[3]);
+      columns(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = mma(hi[tri(t, 0)], r0.p[0], u[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = mma(hi[tri(t, 0)], r0.p[1], u[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = mma(lo[tri(t, 0)], r0.p[0], u[t]);
+      region<12, 2, 2>();
+#pragma unroll
+      for (int t = 2; t < 4; ++t) u[t] = mma(hi[tri(t, 1)], r1.p[0], u[t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) u[t] = mma(hi[tri(t, 1)], r1.p[1], u[t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) u[t] = mma(lo[tri(t, 1)], r1.p[0], u[t]);
+    } else {
+      values();
+      factors(factor, 2);
+      columns(0);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[t][i] = bf16_value(static_cast<unsigned short>(vb[t][i]));
     }
+    Parts<3> y0, y1;
+    y0.of(u[0] * factor[0], u[1] * factor[1]);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) st[t] *= decay;
+    if constexpr (DELTA) region<6, 10, 0>();
+    // the output wave has taken S0 of this chunk and U of the one before
+    stage_barrier();
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      lds_write(xc + Lds::kU + t * 1024 + lane * 16, __builtin_bit_cast(u32x4, u[t]));
+    columns(1);
+    y1.of(u[2] * factor[2], u[3] * factor[3]);
 #pragma unroll
     for (int n = 0; n < 3; ++n)
 #pragma unroll
-      for (int t = 0; t < DK / 16; ++t) st[t] = mma(k[t], y.p[n], st[t]);
-  }
-}
-
-// What the output wave takes from memory for a chunk: rows of Q as left operands,
-// P and the rows' factors.
-template <int DK, bool DELTA>
-struct ScanQuery {
-  using Rec = Record<DELTA>;
-  u32x4 q[4][DK / 32], p[6];
-  f32x4 rows[4];
-  __device__ __forceinline__ void load(const GdnArgs& a, const Scan& w, int c) {
-    const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
-    const int len = min(w.rq.len - c * kChunk, kChunk);
-    const int64_t t0 = w.rq.first + static_cast<int64_t>(c) * kChunk;
-    const __amdgpu_buffer_rsrc_t qr = resource(a.q + t0 * a.q_token + w.hk * a.q_head);
-    const __amdgpu_buffer_rsrc_t rec =
-        resource(a.records + ((w.slot0 + c) * a.n_heads + w.h) * Rec::kBytes);
-    auto get = [](__amdgpu_buffer_rsrc_t rsrc, unsigned off) {
-      return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
-    };
+      for (int t = 0; t < kTiles; ++t) st[t] = mma(kt[0][t], y0.p[n], st[t]);
+    region<3 * kTiles, 2, 1>();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int row = 32 * (t / 2) + 4 * (t % 2) + 8 * (lr >> 2) + (lr & 3);
-      const unsigned at = static_cast<unsigned>(row * a.q_token) + g4 * 16;
+    for (int n = 0; n < 3; ++n)
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) q[t][s] = get(qr, row < len ? at + s * 64 : kOutside);
-    }
+      for (int t = 0; t < kTiles / 2; ++t) st[t] = mma(kt[1][t], y1.p[n], st[t]);
+    __builtin_amdgcn_sched_barrier(0);
+    parts(0, kSteps / 2);
 #pragma unroll
-    for (int i = 0; i < 6; ++i) p[i] = get(rec, Rec::kP + i * 1024 + lane * 16);
+    for (int n = 0; n < 3; ++n)
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      rows[t] = __builtin_bit_cast(f32x4, get(rec, Rec::kRows + 256 + (32 * (t / 2) + 8 * g4 + 4 * (t % 2)) * 4));
-  }
-  // O of the chunk and of a state wave's columns, with S0 and U from LDS
-  __device__ __forceinline__ void products(f32x4 (&o)[4], const lds_t* xc) const {
-    using Lds = ScanLds<DK, DELTA>;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      const u32x4 x = operand_at(xc + Lds::kS, s);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) o[t] = mma(q[t][s], x, o[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] *= rows[t];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Parts<DELTA ? 2 : 1> x;                      // the plain rule's U is bf16
-      x.of(__builtin_bit_cast(f32x4, operand_at(xc + Lds::kU, 2 * s)),
-           __builtin_bit_cast(f32x4, operand_at(xc + Lds::kU, 2 * s + 1)));
-#pragma unroll
-      for (int n = 0; n < (DELTA ? 2 : 1); ++n)
-#pragma unroll
-        for (int t = 2 * s; t < 4; ++t) o[t] = mma(p[tri(t, s)], x.p[n], o[t]);
-    }
+      for (int t = kTiles / 2; t < kTiles; ++t) st[t] = mma(kt[1][t], y1.p[n], st[t]);
+    region<3 * kTiles / 2, 4, 0>();
+    parts(kSteps / 2, kSteps);
+    leave(xc);
   }
 };
 
+// Bounds of 512 for its 320: at most 256 registers.  More, which LDS would leave
+// room for, lie where each use by VALU operations costs a copy (1376 -> 1248 us).
 template <int DK, bool DELTA>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(512)
 scan_kernel(const GdnArgs a, int items) {
   using Lds = ScanLds<DK, DELTA>;
   using Loads = ScanLoads<DK, DELTA>;
-  using Query = ScanQuery<DK, DELTA>;
-  __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], xc_[2][2 * Lds::kWave];
+  __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], out_[2 * Lds::kOut],
+      xc_[2 * Lds::kWave];
   const int slices = (a.dv + kScanCols - 1) / kScanCols;
   const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   lds_t* const in = (lds_t*)in_;
+  lds_t* const out = (lds_t*)out_;
   lds_t* const xc = (lds_t*)xc_;
   // the slices of a head and the heads of a key head on one XCD, whose L2 they
   // share; requests of few tokens are passed over
@@ -869,74 +941,107 @@ scan_kernel(const GdnArgs a, int items) {
 
     if (wave < 2) {
       const bool mine = col0 + wave * 16 < a.dv;
-      float* const sp = a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv +
-                        col0 + wave * 16 + lr;
+      const __amdgpu_buffer_rsrc_t state = resource(reinterpret_cast<const uint8_t*>(
+          a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv));
+      const unsigned at = mine ? (8 * g4 * a.dv + col0 + wave * 16 + lr) * 4 : kOutside;
       const float* const decays = a.decays + w.slot0 * a.n_heads + w.h;
-      f32x4 st[DK / 16];
+      State<DK, DELTA> s;
 #pragma unroll
       for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          st[t][i] = mine && !w.rq.fresh ? sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] : 0.0f;
+          s.st[t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              state, w.rq.fresh ? kOutside : at, (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0));
+      s.parts(0, DK / 32);
+      s.leave(xc + wave * Lds::kWave);
       int place = 0;
       float of_64 = 0.0f;                          // decays of 64 chunks, one a lane
       for (int c = 0; c < w.chunks; ++c) {
         if (c % 64 == 0 && c + lane < w.chunks) of_64 = decays[(c + lane) * static_cast<int64_t>(a.n_heads)];
         const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of_64), c % 64));
-        // what the outputs take is in LDS before the barrier
-        __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_waitcnt(0);             // S0 and U are in LDS
         stage_barrier();
-        state_chunk<DK, DELTA>(st, decay, wave, in + place * Lds::kIn,
-                               xc + ((c & 1) * 2 + wave) * Lds::kWave);
+        s.chunk(decay, wave, in + place * Lds::kIn, xc + wave * Lds::kWave);
         place = place == kRing - 1 ? 0 : place + 1;
       }
-      if (mine)
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sp[(32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i) * a.dv] = st[t][i];
       __builtin_amdgcn_s_waitcnt(0);
       stage_barrier();
-    } else if (wave == 2) {
-      Query next, now;
-      // behind the barrier the state waves are at chunk c
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s.st[t][i]), state, at,
+                                                (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0);
+      stage_barrier();
+    } else if (wave < 4) {
+      const lds_t* const from = xc + (wave - 2) * Lds::kWave;
+      const int col = col0 + (wave - 2) * 16;
+      const bool mine = col < a.dv;
+      f32x4 o[4];
+      int place = 0;
       for (int c = 0; c <= w.chunks; ++c) {
         stage_barrier();
-        now = next;
-        if (c < w.chunks) next.load(a, w, c);
-        if (c == 0) continue;
-        const int64_t t0 = w.rq.first + static_cast<int64_t>(c - 1) * kChunk;
-        const int len = min(w.rq.len - (c - 1) * kChunk, kChunk);
-        const __amdgpu_buffer_rsrc_t rsrc =
-            resource(a.out + t0 * a.out_token + w.h * a.out_head + col0 * 2);
+        u32x4 s0[DK / 32];
+        f32x4 u[4];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          f32x4 o[4];
-          now.products(o, xc + ((~c & 1) * 2 + p) * Lds::kWave);
-          const bool mine = col0 + p * 16 < a.dv;
+        for (int t = 0; t < 4; ++t) u[t] = __builtin_bit_cast(f32x4, operand_at(from + Lds::kU, t));
+#pragma unroll
+        for (int s = 0; s < DK / 32; ++s) s0[s] = operand_at(from + Lds::kS, s);
+        __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
+        stage_barrier();
+        if (c > 0) {
+          const lds_t* const p = out + (~c & 1) * Lds::kOut + Lds::kP;
+          const int64_t t0 = w.rq.first + static_cast<int64_t>(c - 1) * kChunk;
+          const int len = min(w.rq.len - (c - 1) * kChunk, kChunk);
+          // it ends with the rows that there are
+          const __amdgpu_buffer_rsrc_t rsrc =
+              resource(a.out + t0 * a.out_token + w.h * a.out_head + col * 2,
+                       mine ? static_cast<unsigned>(len * a.out_token) : 0);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            Parts<DELTA ? 2 : 1> y;                // the plain rule's U is bf16
+            y.of(u[2 * s], u[2 * s + 1]);
+#pragma unroll
+            for (int i = 0; i < (DELTA ? 2 : 1); ++i)
+#pragma unroll
+              for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(p, tri(t, s)), y.p[i], o[t]);
+          }
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row = 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
               __builtin_amdgcn_raw_buffer_store_b16(
-                  bf16_bits(o[t][i]), rsrc,
-                  mine && row < len ? static_cast<unsigned>(row * a.out_token) + (p * 16 + lr) * 2 : kOutside,
-                  0, 0);
+                  bf16_bits(o[t][i]), rsrc, static_cast<unsigned>(row * a.out_token) + lr * 2, 0, 0);
             }
+        }
+        if (c < w.chunks) {
+          const lds_t* const q = out + (c & 1) * Lds::kOut + Lds::kQ;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(q, t, s), s0[s], o[t]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t] *= row_factors(in + place * Lds::kIn + Lds::kRows, 1, t);
+          place = place == kRing - 1 ? 0 : place + 1;
         }
       }
     } else {
-      Loads::issue(a, w, 0, in);
-      Loads::issue(a, w, 1, in + Lds::kIn);
+      Loads::q(a, w, 0, out);
+      Loads::in(a, w, 0, in);
+      Loads::in(a, w, 1, in + Lds::kIn);
       int place = 2;
       for (int c = 0; c <= w.chunks; ++c) {
-        // chunk c has landed, those of c + 1 may be on their way
-        __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIssues));
+        // but for K, T and V of chunk c + 1, all that was asked for has landed
+        __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIn));
         stage_barrier();
-        Loads::issue(a, w, c + 2, in + place * Lds::kIn);
+        Loads::q(a, w, c + 1, out + (~c & 1) * Lds::kOut);
+        Loads::p(a, w, c, out + (c & 1) * Lds::kOut);
+        Loads::in(a, w, c + 2, in + place * Lds::kIn);
         place = place == kRing - 1 ? 0 : place + 1;
+        stage_barrier();
       }
       // nothing is on its way to LDS when it is used again or released
       __builtin_amdgcn_s_waitcnt(0);
@@ -996,7 +1101,7 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   else prepare_kernel<DK, DELTA, 4><<<blocks, 256, 0, stream>>>(a, k_heads);
   const int items = static_cast<int>(rh * ((c.dv + kScanCols - 1) / kScanCols));
   scan_kernel<DK, DELTA>
-      <<<items < kScanGrid ? items : kScanGrid, 256, 0, stream>>>(a, items);
+      <<<items < kScanGrid ? items : kScanGrid, kScanThreads, 0, stream>>>(a, items);
 }
 
 }  // namespace
