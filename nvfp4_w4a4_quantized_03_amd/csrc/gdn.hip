@@ -296,9 +296,9 @@ struct Rows {
 // (T_ij = - T_ii sum_m A_im T_mj), so no bit is lost to powers of A where keys
 // resemble each other.
 constexpr int kPad = 68;                 // row of 64 floats in LDS
-template <int DK, int WAVES>
+template <int DK, bool DELTA, int WAVES>
 struct PrepareLds {
-  static constexpr int kStage = 2 * kChunk * DK * 2, kProducts = 2 * kChunk * kPad * 4;
+  static constexpr int kStage = 2 * kChunk * DK * 2, kProducts = (DELTA ? 2 : 1) * kChunk * kPad * 4;
   static constexpr int kShared = kStage > kProducts ? kStage : kProducts;
   struct Wave {
     float rows[32 * kPad];               // T's or P's, 32 at a time
@@ -331,11 +331,11 @@ __device__ __forceinline__ void operand_rows(const float* buf, int half, F&& put
 }
 
 template <int DK, bool DELTA, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, 2)
+__global__ void __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1)
 prepare_kernel(const GdnArgs a, int k_heads) {
   using L = Rows<DK>;
   using Rec = Record<DELTA>;
-  __shared__ PrepareLds<DK, WAVES> lds;
+  __shared__ PrepareLds<DK, DELTA, WAVES> lds;
   const int slot = blockIdx.x / k_heads, hk = blockIdx.x - slot * k_heads;
   const int r = request_at(a, slot);
   if (r < 0) return;
@@ -386,14 +386,14 @@ prepare_kernel(const GdnArgs a, int k_heads) {
       for (int u = 0; u < 4; ++u)
         if (u <= t) {
           const u32x4 kb = at(0, u, s);
-          kk[n][u] = mma(ka, kb, kk[n][u]);
+          if (DELTA || u == t) kk[n][u] = mma(ka, kb, kk[n][u]);
           qk[n][u] = mma(qa, kb, qk[n][u]);
         }
     }
   }
   __syncthreads();
-  float* const kkp = reinterpret_cast<float*>(lds.shared);
-  float* const qkp = kkp + kChunk * kPad;
+  float* const qkp = reinterpret_cast<float*>(lds.shared);
+  float* const kkp = qkp + kChunk * kPad;
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
     const int t = wave + n * WAVES;
@@ -402,7 +402,7 @@ prepare_kernel(const GdnArgs a, int k_heads) {
       if (u <= t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
+          if constexpr (DELTA) kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
           qkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = qk[n][u][i];
           if (u == t && 4 * g4 + i == lr) {
             lds.rk[t * 16 + lr] = a.normalize ? 1.0f / __builtin_sqrtf(kk[n][u][i] + kNormEps) : 1.0f;
@@ -908,11 +908,25 @@ struct State {
   }
 };
 
+// The n-th request of those with at least `least` tokens; -1 if they are fewer.
+__device__ __forceinline__ int nth_request(const GdnArgs& a, int n) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.n_requests; base += 64) {
+    const bool is = base + lane < a.n_requests && request_of(a, base + lane).len >= a.least;
+    const uint64_t all = __ballot(is);
+    const int count = __popcll(all);
+    if (n < count)
+      return base + __builtin_ctzll(__ballot(is && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
+    n -= count;
+  }
+  return -1;
+}
+
 // Bounds of 512 for its 320: at most 256 registers.  More, which LDS would leave
 // room for, lie where each use by VALU operations costs a copy (1376 -> 1248 us).
 template <int DK, bool DELTA>
 __global__ void __launch_bounds__(512)
-scan_kernel(const GdnArgs a, int items) {
+scan_kernel(const GdnArgs a) {
   using Lds = ScanLds<DK, DELTA>;
   using Loads = ScanLoads<DK, DELTA>;
   __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], out_[2 * Lds::kOut],
@@ -923,18 +937,20 @@ scan_kernel(const GdnArgs a, int items) {
   lds_t* const in = (lds_t*)in_;
   lds_t* const out = (lds_t*)out_;
   lds_t* const xc = (lds_t*)xc_;
-  // the slices of a head and the heads of a key head on one XCD, whose L2 they
-  // share; requests of few tokens are passed over
-  int first = blockIdx.x;
-  if (gridDim.x % 8 == 0) first = (first % 8) * (gridDim.x / 8) + first / 8;
-  for (int item = first; item < items; item += gridDim.x) {
+  // The value heads of a key head and their slices, which share K, Q and V, run on
+  // one XCD and its L2; the key heads go over the XCDs in turn.  `n` counts the
+  // requests that are long enough, so that few of them fill the card too.
+  const int share = a.group * slices, k_heads = a.n_heads / a.group;
+  for (int item = blockIdx.x / 8;; item += gridDim.x / 8) {
     Scan w;
-    const int rh = item / slices, r = rh / a.n_heads;
+    const int at = item / share, unit = at * 8 + blockIdx.x % 8;
+    const int n = unit / k_heads, of_share = item - at * share;
+    const int r = nth_request(a, n);
+    if (r < 0) break;
     w.rq = request_of(a, r);
-    if (w.rq.len < a.least) continue;
-    w.slice = item - rh * slices;
-    w.h = rh - r * a.n_heads;
-    w.hk = w.h / a.group;
+    w.hk = unit - n * k_heads;
+    w.h = w.hk * a.group + of_share / slices;
+    w.slice = of_share % slices;
     w.chunks = (w.rq.len + kChunk - 1) / kChunk;
     w.slot0 = first_slot(a, r);
     const int col0 = w.slice * kScanCols;          // the last slice may have 16 columns
@@ -1099,9 +1115,11 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   if (a.group == 1) prepare_kernel<DK, DELTA, 1><<<blocks, 64, 0, stream>>>(a, k_heads);
   else if (a.group == 2) prepare_kernel<DK, DELTA, 2><<<blocks, 128, 0, stream>>>(a, k_heads);
   else prepare_kernel<DK, DELTA, 4><<<blocks, 256, 0, stream>>>(a, k_heads);
-  const int items = static_cast<int>(rh * ((c.dv + kScanCols - 1) / kScanCols));
-  scan_kernel<DK, DELTA>
-      <<<items < kScanGrid ? items : kScanGrid, kScanThreads, 0, stream>>>(a, items);
+  // a multiple of 8 that has every item of every key head
+  const int64_t units = (c.n_requests * c.n_k_heads + 7) / 8;
+  const int64_t blocks_of = units * 8 * a.group * ((c.dv + kScanCols - 1) / kScanCols);
+  scan_kernel<DK, DELTA><<<static_cast<unsigned>(blocks_of < kScanGrid ? blocks_of : kScanGrid),
+                           kScanThreads, 0, stream>>>(a);
 }
 
 }  // namespace
