@@ -350,6 +350,16 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, g4 = lane >> 4;
+  // a lane's gates of the wave's first head, asked for before K and Q; of a later
+  // one, before the work on the one before it
+  float gate = 1.0f, be = 0.0f;
+  auto gates = [&](int hh) __attribute__((always_inline)) {
+    if (lane < len && hh < a.group) {
+      gate = a.alpha[(t0 + lane) * a.ld_alpha + hk * a.group + hh];
+      if (DELTA) be = a.beta[(t0 + lane) * a.ld_beta + hk * a.group + hh];
+    }
+  };
+  gates(wave);
 
   // K and Q to LDS; rows past the end are zeros
 #pragma unroll
@@ -409,10 +419,15 @@ prepare_kernel(const GdnArgs a, int k_heads) {
           if constexpr (DELTA) kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
           qkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = qk[n][u][i];
           if (u == t && 4 * g4 + i == lr) {
-            lds.rk[t * 16 + lr] = a.normalize ? 1.0f / __builtin_sqrtf(kk[n][u][i] + kNormEps) : 1.0f;
-            lds.rq[t * 16 + lr] = a.scale * (a.normalize ? 1.0f / __builtin_sqrtf(qq[n][i] + kNormEps) : 1.0f);
+            lds.rk[t * 16 + lr] = kk[n][u][i];
+            lds.rq[t * 16 + lr] = qq[n][i];
           }
         }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    lds.rk[lane] = a.normalize ? 1.0f / __builtin_sqrtf(lds.rk[lane] + kNormEps) : 1.0f;
+    lds.rq[lane] = a.normalize ? a.scale / __builtin_sqrtf(lds.rq[lane] + kNormEps) : a.scale;
   }
   __syncthreads();
 
@@ -421,13 +436,7 @@ prepare_kernel(const GdnArgs a, int k_heads) {
   for (int hh = wave; hh < a.group; hh += WAVES) {
     const int h = hk * a.group + hh;
     // a gate of zero counts as 2^-160, below what binary32 holds
-    double sum = 0.0;
-    float be = 0.0f;
-    if (lane < len) {
-      const float al = a.alpha[(t0 + lane) * a.ld_alpha + h];
-      sum = al > 0.0f ? log2(static_cast<double>(al)) : al == 0.0f ? -160.0 : __builtin_nan("");
-      be = DELTA ? a.beta[(t0 + lane) * a.ld_beta + h] : 1.0f;
-    }
+    double sum = gate > 0.0f ? log2(static_cast<double>(gate)) : gate == 0.0f ? -160.0 : __builtin_nan("");
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double before = __shfl_up(sum, d);
@@ -441,10 +450,11 @@ prepare_kernel(const GdnArgs a, int k_heads) {
       rows[lane] = gi * rk;
       rows[64 + lane] = gi * lds.rq[lane];
       rows[128 + lane] = rk * exp2_of(last - sum);
-      rows[192 + lane] = be;
+      if (DELTA) rows[192 + lane] = be;
       if (lane == 0) a.decays[static_cast<int64_t>(slot) * a.n_heads + h] = exp2_of(last);
       own.g[lane] = sum;
       own.beta[lane] = be;
+      gates(hh + WAVES);
       own.e[lane] = exp2_of(sum - __shfl(sum, lane & 48));
 #pragma unroll
       for (int b = 1; b < 4; ++b) {
