@@ -299,6 +299,11 @@ struct Rows {
 // diagonal by substitution, a column a lane, the others by products in binary32
 // (T_ij = - T_ii sum_m A_im T_mj), so no bit is lost to powers of A where keys
 // resemble each other.
+//
+// What it waits for bounds it.  32768 tokens, 16 key and 64 value heads of 128
+// (890 MB read and written): 250 us, 3.6 TB/s; 324 before a workgroup brought the
+// next unit's K and Q and gates while it works on one, where the inverses took
+// 115 of it, K and Q 100 and T's stores 50.
 constexpr int kPad = 68;                 // row of 64 floats in LDS
 template <int DK, bool DELTA, int WAVES>
 struct PrepareLds {
@@ -336,262 +341,301 @@ __device__ __forceinline__ void operand_rows(const float* buf, int half, F&& put
 
 template <int DK, bool DELTA, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1)
-prepare_kernel(const GdnArgs a, int k_heads) {
+prepare_kernel(const GdnArgs a, int k_heads, int units) {
   using L = Rows<DK>;
   using Rec = Record<DELTA>;
   __shared__ PrepareLds<DK, DELTA, WAVES> lds;
-  const int slot = blockIdx.x / k_heads, hk = blockIdx.x - slot * k_heads;
-  const int r = request_at(a, slot);
-  if (r < 0) return;
-  const Request rq = request_of(a, r);
-  const int c = slot - first_slot(a, r);
-  if (rq.len < a.least || c < 0 || c * kChunk >= rq.len) return;
-  const int len = min(rq.len - c * kChunk, kChunk);
-  const int64_t t0 = rq.first + static_cast<int64_t>(c) * kChunk;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lr = lane & 15, g4 = lane >> 4;
-  // a lane's gates of the wave's first head, asked for before K and Q; of a later
-  // one, before the work on the one before it
-  float gate = 1.0f, be = 0.0f;
-  auto gates = [&](int hh) __attribute__((always_inline)) {
-    if (lane < len && hh < a.group) {
-      gate = a.alpha[(t0 + lane) * a.ld_alpha + hk * a.group + hh];
-      if (DELTA) be = a.beta[(t0 + lane) * a.ld_beta + hk * a.group + hh];
-    }
-  };
-  gates(wave);
 
-  // K and Q to LDS; rows past the end are zeros
-#pragma unroll
-  for (int n = 0; n < 2 * kChunk * L::kPieces / (WAVES * 64); ++n) {
-    const int i = n * WAVES * 64 + threadIdx.x;
-    const int row = (i / L::kPieces) & (kChunk - 1), piece = i & (L::kPieces - 1);
-    const bool is_q = i >= kChunk * L::kPieces;
-    u32x4 x = {0u, 0u, 0u, 0u};
-    if (row < len) {
-      const uint8_t* p = is_q ? a.q + (t0 + row) * a.q_token + hk * a.q_head
-                              : a.k + (t0 + row) * a.k_token + hk * a.k_head;
-      x = *reinterpret_cast<const u32x4*>(p + piece * 16);
-    }
-    *reinterpret_cast<u32x4*>(lds.shared + (is_q ? kChunk * L::kBytes : 0) + row * L::kBytes +
-                              (piece ^ L::natural(row)) * 16) = x;
-  }
-  __syncthreads();
-  auto at = [&](int is_q, int tile, int s) {
-    const int row = tile * 16 + lr;
-    return *reinterpret_cast<const u32x4*>(lds.shared + is_q * kChunk * L::kBytes + row * L::kBytes +
-                                           ((4 * s + g4) ^ L::natural(row)) * 16);
+  // Of a unit (a chunk slot and key head) a thread brings pieces of K and Q and a
+  // lane's gates of its wave's first head; len 0: nothing to do there.
+  constexpr bool kAhead = WAVES == 4;
+  constexpr int kLoads = 2 * kChunk * L::kPieces / (WAVES * 64);
+  struct Unit {
+    int slot, hk, len;
+    int64_t t0;
   };
-  // products of a tile of rows with the tiles of keys up to it; they stay in
-  // registers until everybody has read K and Q
-  constexpr int kTiles = 4 / WAVES;
-  f32x4 kk[kTiles][4], qk[kTiles][4], qq[kTiles];
+  auto unit_at = [&](int i) {
+    Unit u = {0, 0, 0, 0};
+    if (i >= units) return u;
+    u.slot = i / k_heads;
+    u.hk = i - u.slot * k_heads;
+    const int r = request_at(a, u.slot);
+    if (r < 0) return u;
+    const Request rq = request_of(a, r);
+    const int c = u.slot - first_slot(a, r);
+    if (rq.len < a.least || c < 0 || c * kChunk >= rq.len) return u;
+    u.len = min(rq.len - c * kChunk, kChunk);
+    u.t0 = rq.first + static_cast<int64_t>(c) * kChunk;
+    return u;
+  };
+  u32x4 x[kLoads];
+  float gate, be;
+  auto gates = [&](const Unit& u, int hh) __attribute__((always_inline)) {
+    gate = 1.0f;
+    be = 0.0f;
+    if (lane < u.len && hh < a.group) {
+      gate = a.alpha[(u.t0 + lane) * a.ld_alpha + u.hk * a.group + hh];
+      if (DELTA) be = a.beta[(u.t0 + lane) * a.ld_beta + u.hk * a.group + hh];
+    }
+  };
+  auto rows = [&](const Unit& u) __attribute__((always_inline)) {
 #pragma unroll
-  for (int n = 0; n < kTiles; ++n) {
-    const int t = wave + n * WAVES;
-    qq[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < kLoads; ++n) {
+      const int i = n * WAVES * 64 + threadIdx.x;
+      const int row = (i / L::kPieces) & (kChunk - 1), piece = i & (L::kPieces - 1);
+      const uint8_t* p = i >= kChunk * L::kPieces ? a.q + (u.t0 + row) * a.q_token + u.hk * a.q_head
+                                                  : a.k + (u.t0 + row) * a.k_token + u.hk * a.k_head;
+      x[n] = u32x4{0u, 0u, 0u, 0u};
+      if (row < u.len) x[n] = *reinterpret_cast<const u32x4*>(p + piece * 16);
+    }
+  };
+  Unit next = unit_at(blockIdx.x);
+  gates(next, wave);
+  rows(next);
+  int i = blockIdx.x;
+  do {
+    const Unit u = next;
+    next = unit_at(kAhead ? i + gridDim.x : units);
+    const int slot = u.slot, hk = u.hk, len = u.len;
+    const int64_t t0 = u.t0;
+    if (len == 0) {
+      if (!kAhead) return;
+      gates(next, wave);
+      rows(next);
+      continue;
+    }
+
+    // K and Q to LDS, when everybody has done with the unit before
+    __syncthreads();
 #pragma unroll
-    for (int u = 0; u < 4; ++u) kk[n][u] = qk[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < kLoads; ++n) {
+      const int i = n * WAVES * 64 + threadIdx.x;
+      const int row = (i / L::kPieces) & (kChunk - 1), piece = i & (L::kPieces - 1);
+      *reinterpret_cast<u32x4*>(lds.shared + (i >= kChunk * L::kPieces ? kChunk * L::kBytes : 0) +
+                                row * L::kBytes + (piece ^ L::natural(row)) * 16) = x[n];
+    }
+    __syncthreads();
+    if (kAhead) rows(next);
+    auto at = [&](int is_q, int tile, int s) {
+      const int row = tile * 16 + lr;
+      return *reinterpret_cast<const u32x4*>(lds.shared + is_q * kChunk * L::kBytes + row * L::kBytes +
+                                             ((4 * s + g4) ^ L::natural(row)) * 16);
+    };
+    // products of a tile of rows with the tiles of keys up to it; they stay in
+    // registers until everybody has read K and Q
+    constexpr int kTiles = 4 / WAVES;
+    f32x4 kk[kTiles][4], qk[kTiles][4], qq[kTiles];
 #pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      const u32x4 ka = at(0, t, s), qa = at(1, t, s);
-      qq[n] = mma(qa, qa, qq[n]);
+    for (int n = 0; n < kTiles; ++n) {
+      const int t = wave + n * WAVES;
+      qq[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) kk[n][u] = qk[n][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) {
+        const u32x4 ka = at(0, t, s), qa = at(1, t, s);
+        qq[n] = mma(qa, qa, qq[n]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u <= t) {
+            const u32x4 kb = at(0, u, s);
+            if (DELTA || u == t) kk[n][u] = mma(ka, kb, kk[n][u]);
+            qk[n][u] = mma(qa, kb, qk[n][u]);
+          }
+      }
+    }
+    __syncthreads();
+    float* const qkp = reinterpret_cast<float*>(lds.shared);
+    float* const kkp = qkp + kChunk * kPad;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      const int t = wave + n * WAVES;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (u <= t) {
-          const u32x4 kb = at(0, u, s);
-          if (DELTA || u == t) kk[n][u] = mma(ka, kb, kk[n][u]);
-          qk[n][u] = mma(qa, kb, qk[n][u]);
-        }
-    }
-  }
-  __syncthreads();
-  float* const qkp = reinterpret_cast<float*>(lds.shared);
-  float* const kkp = qkp + kChunk * kPad;
+        if (u <= t)
 #pragma unroll
-  for (int n = 0; n < kTiles; ++n) {
-    const int t = wave + n * WAVES;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (u <= t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (DELTA) kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
-          qkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = qk[n][u][i];
-          if (u == t && 4 * g4 + i == lr) {
-            lds.rk[t * 16 + lr] = kk[n][u][i];
-            lds.rq[t * 16 + lr] = qq[n][i];
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (DELTA) kkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = kk[n][u][i];
+            qkp[(t * 16 + 4 * g4 + i) * kPad + u * 16 + lr] = qk[n][u][i];
+            if (u == t && 4 * g4 + i == lr) {
+              lds.rk[t * 16 + lr] = kk[n][u][i];
+              lds.rq[t * 16 + lr] = qq[n][i];
+            }
           }
-        }
-  }
-  __syncthreads();
-  if (wave == 0) {
-    lds.rk[lane] = a.normalize ? 1.0f / __builtin_sqrtf(lds.rk[lane] + kNormEps) : 1.0f;
-    lds.rq[lane] = a.normalize ? a.scale / __builtin_sqrtf(lds.rq[lane] + kNormEps) : a.scale;
-  }
-  __syncthreads();
-
-  auto& own = lds.wave[wave];
-  float* const buf = own.rows;
-  for (int hh = wave; hh < a.group; hh += WAVES) {
-    const int h = hk * a.group + hh;
-    // a gate of zero counts as 2^-160, below what binary32 holds
-    double sum = gate > 0.0f ? log2(static_cast<double>(gate)) : gate == 0.0f ? -160.0 : __builtin_nan("");
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double before = __shfl_up(sum, d);
-      if (lane >= d) sum += before;
     }
-    const double last = __shfl(sum, 63);
-    uint8_t* const rec = a.records + (static_cast<int64_t>(slot) * a.n_heads + h) * Rec::kBytes;
-    {
-      const float rk = lds.rk[lane], gi = exp2_of(sum);
-      float* const rows = reinterpret_cast<float*>(rec + Rec::kRows);
-      rows[lane] = gi * rk;
-      rows[64 + lane] = gi * lds.rq[lane];
-      rows[128 + lane] = rk * exp2_of(last - sum);
-      if (DELTA) rows[192 + lane] = be;
-      if (lane == 0) a.decays[static_cast<int64_t>(slot) * a.n_heads + h] = exp2_of(last);
-      own.g[lane] = sum;
-      own.beta[lane] = be;
-      gates(hh + WAVES);
-      own.e[lane] = exp2_of(sum - __shfl(sum, lane & 48));
+    __syncthreads();
+    if (wave == 0) {
+      lds.rk[lane] = a.normalize ? 1.0f / __builtin_sqrtf(lds.rk[lane] + kNormEps) : 1.0f;
+      lds.rq[lane] = a.normalize ? a.scale / __builtin_sqrtf(lds.rq[lane] + kNormEps) : a.scale;
+    }
+    __syncthreads();
+
+    auto& own = lds.wave[wave];
+    float* const buf = own.rows;
+    for (int hh = wave; hh < a.group; hh += WAVES) {
+      const int h = hk * a.group + hh;
+      // a gate of zero counts as 2^-160, below what binary32 holds
+      double sum = gate > 0.0f ? log2(static_cast<double>(gate)) : gate == 0.0f ? -160.0 : __builtin_nan("");
 #pragma unroll
-      for (int b = 1; b < 4; ++b) {
-        const double start = __shfl(sum, 16 * b);
-        own.f[b - 1][lane] = lane < 16 * b ? rk * exp2_of(start - sum) : 0.0f;
+      for (int d = 1; d < 64; d <<= 1) {
+        const double before = __shfl_up(sum, d);
+        if (lane >= d) sum += before;
       }
-    }
-    __builtin_amdgcn_wave_barrier();
-
-    // decays times the columns' norms of tile (i, m), of row i 16 + lr, columns
-    // m 16 + 4 g4 + 0 .. 3
-    f32x4 within[4];
+      const double last = __shfl(sum, 63);
+      uint8_t* const rec = a.records + (static_cast<int64_t>(slot) * a.n_heads + h) * Rec::kBytes;
+      {
+        const float rk = lds.rk[lane], gi = exp2_of(sum);
+        float* const rows = reinterpret_cast<float*>(rec + Rec::kRows);
+        rows[lane] = gi * rk;
+        rows[64 + lane] = gi * lds.rq[lane];
+        rows[128 + lane] = rk * exp2_of(last - sum);
+        if (DELTA) rows[192 + lane] = be;
+        if (lane == 0) a.decays[static_cast<int64_t>(slot) * a.n_heads + h] = exp2_of(last);
+        own.g[lane] = sum;
+        own.beta[lane] = be;
+        // asked for before the work on this head
+        if (hh + WAVES < a.group) gates(u, hh + WAVES);
+        else if (kAhead) gates(next, wave);
+        own.e[lane] = exp2_of(sum - __shfl(sum, lane & 48));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double gi = own.g[i * 16 + lr];
-      const f32x4 rk = *reinterpret_cast<const f32x4*>(lds.rk + i * 16 + 4 * g4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        within[i][e] = 4 * g4 + e <= lr ? rk[e] * exp2_of(gi - own.g[i * 16 + 4 * g4 + e]) : 0.0f;
-    }
-    auto decay = [&](int i, int m) {
-      if (i == m) return within[i];
-      return own.e[i * 16 + lr] * *reinterpret_cast<const f32x4*>(&own.f[i - 1][m * 16 + 4 * g4]);
-    };
+        for (int b = 1; b < 4; ++b) {
+          const double start = __shfl(sum, 16 * b);
+          own.f[b - 1][lane] = lane < 16 * b ? rk * exp2_of(start - sum) : 0.0f;
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
 
-    if constexpr (DELTA) {
-      // -A: tiles below the diagonal as left operands, those on it in LDS
-      f32x4 na[4][4];
+      // decays times the columns' norms of tile (i, m), of row i 16 + lr, columns
+      // m 16 + 4 g4 + 0 .. 3
+      f32x4 within[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = i * 16 + lr;
-        const float f = -own.beta[row] * lds.rk[row];
-#pragma unroll
-        for (int m = 0; m <= i; ++m) {
-          na[i][m] = f * decay(i, m) * *reinterpret_cast<const f32x4*>(kkp + row * kPad + m * 16 + 4 * g4);
-          if (m == i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) na[i][i][e] = 4 * g4 + e < lr ? na[i][i][e] : 0.0f;
-        }
-        *reinterpret_cast<f32x4*>(buf + row * 20 + 4 * g4) = na[i][i];
-      }
-      __builtin_amdgcn_wave_barrier();
-      // the diagonal blocks' inverses: lane l has column l % 16 of block l / 16
-      float x[16];
-#pragma unroll
-      for (int row = 0; row < 16; ++row) {
-        float y = row == lr ? 1.0f : 0.0f;
-#pragma unroll
-        for (int m = 0; m < row; m += 4) {
-          const f32x4 w = *reinterpret_cast<const f32x4*>(buf + (g4 * 16 + row) * 20 + m);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e < row) y = __builtin_fmaf(w[e], x[m + e], y);
-        }
-        x[row] = y;
-      }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int row = 0; row < 16; ++row) buf[(g4 * 16 + row) * 20 + lr] = x[row];
-      __builtin_amdgcn_wave_barrier();
-      f32x4 dl[4], t[4][4];              // as left operands; tiles of the inverse
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dl[i] = *reinterpret_cast<const f32x4*>(buf + (i * 16 + lr) * 20 + 4 * g4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[i][i][e] = buf[(i * 16 + 4 * g4 + e) * 20 + lr];
-      }
-      __builtin_amdgcn_wave_barrier();
-      auto times = [](f32x4 left, f32x4 right, f32x4 acc) {
+        const double gi = own.g[i * 16 + lr];
+        const f32x4 rk = *reinterpret_cast<const f32x4*>(lds.rk + i * 16 + 4 * g4);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], right[e], acc, 0, 0, 0);
-        return acc;
+          within[i][e] = 4 * g4 + e <= lr ? rk[e] * exp2_of(gi - own.g[i * 16 + 4 * g4 + e]) : 0.0f;
+      }
+      auto decay = [&](int i, int m) {
+        if (i == m) return within[i];
+        return own.e[i * 16 + lr] * *reinterpret_cast<const f32x4*>(&own.f[i - 1][m * 16 + 4 * g4]);
       };
+
+      if constexpr (DELTA) {
+        // -A: tiles below the diagonal as left operands, those on it in LDS
+        f32x4 na[4][4];
 #pragma unroll
-      for (int d = 1; d < 4; ++d)
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 16 + lr;
+          const float f = -own.beta[row] * lds.rk[row];
 #pragma unroll
-        for (int j = 0; j + d < 4; ++j) {
-          const int i = j + d;
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int m = 0; m <= i; ++m) {
+            na[i][m] = f * decay(i, m) * *reinterpret_cast<const f32x4*>(kkp + row * kPad + m * 16 + 4 * g4);
+            if (m == i)
 #pragma unroll
-          for (int m = j; m < i; ++m) acc = times(na[i][m], t[m][j], acc);
-          t[i][j] = times(dl[i], acc, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+              for (int e = 0; e < 4; ++e) na[i][i][e] = 4 * g4 + e < lr ? na[i][i][e] : 0.0f;
+          }
+          *reinterpret_cast<f32x4*>(buf + row * 20 + 4 * g4) = na[i][i];
         }
-      // 32 rows at a time through LDS to the operands' order, times beta,
-      // below the diagonal only
+        __builtin_amdgcn_wave_barrier();
+        // the diagonal blocks' inverses: lane l has column l % 16 of block l / 16
+        float x[16];
+#pragma unroll
+        for (int row = 0; row < 16; ++row) {
+          float y = row == lr ? 1.0f : 0.0f;
+#pragma unroll
+          for (int m = 0; m < row; m += 4) {
+            const f32x4 w = *reinterpret_cast<const f32x4*>(buf + (g4 * 16 + row) * 20 + m);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (m + e < row) y = __builtin_fmaf(w[e], x[m + e], y);
+          }
+          x[row] = y;
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int row = 0; row < 16; ++row) buf[(g4 * 16 + row) * 20 + lr] = x[row];
+        __builtin_amdgcn_wave_barrier();
+        f32x4 dl[4], t[4][4];              // as left operands; tiles of the inverse
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dl[i] = *reinterpret_cast<const f32x4*>(buf + (i * 16 + lr) * 20 + 4 * g4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[i][i][e] = buf[(i * 16 + 4 * g4 + e) * 20 + lr];
+        }
+        __builtin_amdgcn_wave_barrier();
+        auto times = [](f32x4 left, f32x4 right, f32x4 acc) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[e], right[e], acc, 0, 0, 0);
+          return acc;
+        };
+#pragma unroll
+        for (int d = 1; d < 4; ++d)
+#pragma unroll
+          for (int j = 0; j + d < 4; ++j) {
+            const int i = j + d;
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int m = j; m < i; ++m) acc = times(na[i][m], t[m][j], acc);
+            t[i][j] = times(dl[i], acc, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          }
+        // 32 rows at a time through LDS to the operands' order, times beta,
+        // below the diagonal only
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2 * half + 2; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                buf[(i * 16 + 4 * g4 + e) * kPad + j * 16 + lr] = j <= 2 * half + i ? t[2 * half + i][j][e] : 0.0f;
+          __builtin_amdgcn_wave_barrier();
+          operand_rows(buf, half, [&](int tile, int s, int row, int col, f32x4 y0, f32x4 y1) {
+            y0 *= *reinterpret_cast<const f32x4*>(own.beta + col);
+            y1 *= *reinterpret_cast<const f32x4*>(own.beta + col + 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              y0[q] = col + q < row ? y0[q] : 0.0f;
+              y1[q] = col + 4 + q < row ? y1[q] : 0.0f;
+            }
+            Parts<2> w;
+            w.of(y0, y1);
+            uint8_t* const dst = rec + Rec::kT + tri(tile, s) * 1024 + lane * 16;
+            *reinterpret_cast<u32x4*>(dst) = w.p[0];
+            *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
+          });
+          __builtin_amdgcn_wave_barrier();
+        }
+      }
+      // P, the same way
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const int row = (2 * half + i) * 16 + lr;
+          const float f = lds.rq[row];
 #pragma unroll
-          for (int j = 0; j < 2 * half + 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              buf[(i * 16 + 4 * g4 + e) * kPad + j * 16 + lr] = j <= 2 * half + i ? t[2 * half + i][j][e] : 0.0f;
-        __builtin_amdgcn_wave_barrier();
-        operand_rows(buf, half, [&](int tile, int s, int row, int col, f32x4 y0, f32x4 y1) {
-          y0 *= *reinterpret_cast<const f32x4*>(own.beta + col);
-          y1 *= *reinterpret_cast<const f32x4*>(own.beta + col + 4);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            y0[q] = col + q < row ? y0[q] : 0.0f;
-            y1[q] = col + 4 + q < row ? y1[q] : 0.0f;
+          for (int m = 0; m < 2 * half + 2; ++m) {
+            f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (m <= 2 * half + i)
+              y = f * decay(2 * half + i, m) * *reinterpret_cast<const f32x4*>(qkp + row * kPad + m * 16 + 4 * g4);
+            *reinterpret_cast<f32x4*>(buf + (i * 16 + lr) * kPad + m * 16 + 4 * g4) = y;
           }
-          Parts<2> w;
-          w.of(y0, y1);
-          uint8_t* const dst = rec + Rec::kT + tri(tile, s) * 1024 + lane * 16;
-          *reinterpret_cast<u32x4*>(dst) = w.p[0];
-          *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
+        }
+        __builtin_amdgcn_wave_barrier();
+        operand_rows(buf, half, [&](int tile, int s, int, int, f32x4 y0, f32x4 y1) {
+          *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(tile, s) * 1024 + lane * 16) =
+              u32x4{pack_bf16(y0[0], y0[1]), pack_bf16(y0[2], y0[3]), pack_bf16(y1[0], y1[1]),
+                    pack_bf16(y1[2], y1[3])};
         });
         __builtin_amdgcn_wave_barrier();
       }
     }
-    // P, the same way
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = (2 * half + i) * 16 + lr;
-        const float f = lds.rq[row];
-#pragma unroll
-        for (int m = 0; m < 2 * half + 2; ++m) {
-          f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (m <= 2 * half + i)
-            y = f * decay(2 * half + i, m) * *reinterpret_cast<const f32x4*>(qkp + row * kPad + m * 16 + 4 * g4);
-          *reinterpret_cast<f32x4*>(buf + (i * 16 + lr) * kPad + m * 16 + 4 * g4) = y;
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-      operand_rows(buf, half, [&](int tile, int s, int, int, f32x4 y0, f32x4 y1) {
-        *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(tile, s) * 1024 + lane * 16) =
-            u32x4{pack_bf16(y0[0], y0[1]), pack_bf16(y0[2], y0[3]), pack_bf16(y1[0], y1[1]),
-                  pack_bf16(y1[2], y1[3])};
-      });
-      __builtin_amdgcn_wave_barrier();
-    }
-  }
+  } while (kAhead && (i += gridDim.x) < units);
 }
 
 // The scan: 32 columns of a request's head a workgroup of five waves.
@@ -1104,6 +1148,9 @@ GdnArgs args_of(const GdnCall& c) {
 // few tokens costs less there than starting a workgroup for it does.
 constexpr int kScanGrid = 1024;
 
+// Workgroups of four waves of the preparation, two a CU, which go on to further units
+constexpr int kPrepareGrid = 512;
+
 // Requests of at most this many tokens are taken token after token.
 constexpr int kFewTokens = 16;
 
@@ -1124,15 +1171,17 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   a.least = kFewTokens + 1;
   a.records = static_cast<uint8_t*>(c.workspace);
   a.decays = reinterpret_cast<float*>(a.records + chunk_slots(c) * c.n_heads * record_bytes(DELTA));
-  const unsigned blocks = static_cast<unsigned>(chunk_slots(c) * c.n_k_heads);
+  const int units = static_cast<int>(chunk_slots(c) * c.n_k_heads);
   const int k_heads = static_cast<int>(c.n_k_heads);
-  if (a.group == 1) prepare_kernel<DK, DELTA, 1><<<blocks, 64, 0, stream>>>(a, k_heads);
-  else if (a.group == 2) prepare_kernel<DK, DELTA, 2><<<blocks, 128, 0, stream>>>(a, k_heads);
-  else prepare_kernel<DK, DELTA, 4><<<blocks, 256, 0, stream>>>(a, k_heads);
+  if (a.group == 1) prepare_kernel<DK, DELTA, 1><<<units, 64, 0, stream>>>(a, k_heads, units);
+  else if (a.group == 2) prepare_kernel<DK, DELTA, 2><<<units, 128, 0, stream>>>(a, k_heads, units);
+  else
+    prepare_kernel<DK, DELTA, 4><<<units < kPrepareGrid ? units : kPrepareGrid, 256, 0, stream>>>(
+        a, k_heads, units);
   // a multiple of 8 that has every item of every key head
-  const int64_t units = (c.n_requests * c.n_k_heads + 7) / 8;
-  const int64_t blocks_of = units * 8 * a.group * ((c.dv + kScanCols - 1) / kScanCols);
-  scan_kernel<DK, DELTA><<<static_cast<unsigned>(blocks_of < kScanGrid ? blocks_of : kScanGrid),
+  const int64_t eights = (c.n_requests * c.n_k_heads + 7) / 8;
+  const int64_t blocks = eights * 8 * a.group * ((c.dv + kScanCols - 1) / kScanCols);
+  scan_kernel<DK, DELTA><<<static_cast<unsigned>(blocks < kScanGrid ? blocks : kScanGrid),
                            kScanThreads, 0, stream>>>(a);
 }
 
