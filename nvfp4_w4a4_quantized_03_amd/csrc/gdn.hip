@@ -652,9 +652,9 @@ prepare_kernel(const GdnArgs a, int k_heads, int units) {
 // waves may write U of c and S0 of c + 1 over them.
 //
 // One prompt of 32768 tokens, 16 key and 64 value heads of 128 (a workgroup on
-// each CU): 1060 us, 2.1 a chunk, of which the state waves' 98 products alone
-// take 0.65; without output and loader 811, output alone 862 with one output wave
-// for both (1248 in all), loads alone 655.
+// each CU): 1003 us, 2.0 a chunk.  The state waves bound it: 797 without output
+// and loader, of which their 98 products a chunk take 330 and the rest is what
+// each product waits for of the one before.  Output alone takes 453, the loads 631.
 constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {
@@ -991,7 +991,10 @@ scan_kernel(const GdnArgs a) {
       xc_[2 * Lds::kWave];
   const int slices = (a.dv + kScanCols - 1) / kScanCols;
   const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // 0, 1: state, 2, 3: output, 4: loader.  The first wave, with which the fifth
+  // shares a SIMD, is not a state wave (1077 -> 1004 us).
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = id == 0 ? 2 : id < 3 ? id - 1 : id;
   lds_t* const in = (lds_t*)in_;
   lds_t* const out = (lds_t*)out_;
   lds_t* const xc = (lds_t*)xc_;
