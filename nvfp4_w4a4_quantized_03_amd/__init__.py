@@ -851,7 +851,7 @@ def _gates(t, name, device, tokens, heads):
         _device_tensor(t, name, torch.float32, device=device)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != tokens or shape[1] != heads or \
-            (heads > 1 and stride[1] != 1):
+            (tokens > 0 and heads > 1 and stride[1] != 1):
         raise ValueError("%s must be float32 [n_tokens, n_heads] with unit "
                          "column stride" % name)
     return t.data_ptr(), stride[0] if tokens > 1 else heads

@@ -967,15 +967,25 @@ struct State {
 };
 
 // The n-th request of those with at least `least` tokens; -1 if they are fewer.
+// 256 at a time, whose loads do not wait for each other.
 __device__ __forceinline__ int nth_request(const GdnArgs& a, int n) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < a.n_requests; base += 64) {
-    const bool is = base + lane < a.n_requests && request_of(a, base + lane).len >= a.least;
-    const uint64_t all = __ballot(is);
-    const int count = __popcll(all);
-    if (n < count)
-      return base + __builtin_ctzll(__ballot(is && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
-    n -= count;
+  for (int base = 0; base < a.n_requests; base += 256) {
+    bool is[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = min(base + 64 * j + lane, a.n_requests - 1);
+      is[j] = request_of(a, r).len >= a.least && base + 64 * j + lane < a.n_requests;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t all = __ballot(is[j]);
+      const int count = __popcll(all);
+      if (n < count)
+        return base + 64 * j +
+               __builtin_ctzll(__ballot(is[j] && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
+      n -= count;
+    }
   }
   return -1;
 }

@@ -120,7 +120,8 @@ def check(c, out, before, want, what):
     got, state = out.double().cpu().numpy(), c["state"].double().cpu().numpy()
     for r, ref in enumerate(want):
         if cu[r + 1] == cu[r]:
-            assert torch.equal(c["state"][slots[r]], before[slots[r]]), (what, r)
+            kept = (t[slots[r]].view(torch.int32) for t in (c["state"], before))  # NaN too
+            assert torch.equal(*kept), (what, r)
         else:
             compare(got[cu[r]:cu[r + 1]], state[slots[r]], ref, (what, r))
     rest = np.setdiff1d(np.arange(len(state)), slots)
@@ -284,3 +285,75 @@ def test_scale_and_no_normalisation():
         c["k"] = (c["k"].float() / 12).to(BF16)           # |k| < 1 without the division
         c["normalize"] = False
         run(c, scale=0.7)
+
+
+@pytest.mark.parametrize("k_heads,heads,dk,dv", [(3, 3, 128, 16), (3, 3, 64, 32), (2, 4, 128, 80),
+                                                 (2, 4, 64, 64), (1, 4, 64, 16), (2, 10, 128, 64),
+                                                 (1, 8, 128, 32), (1, 9, 64, 48), (9, 9, 64, 64),
+                                                 (1, 1, 128, 512), (2, 2, 64, 272)])
+@pytest.mark.parametrize("delta", [True, False])
+def test_heads_of_prompts(k_heads, heads, dk, dv, delta):
+    _say("heads", k_heads, heads, dk, dv, delta)
+    rng = np.random.default_rng(heads * dk + dv)
+    run(build(rng, [90, 2, 64, 17], k_heads, heads, dk, dv, delta), held=[1, 1, 0, 1])
+
+
+@pytest.mark.parametrize("every", [1, 97])
+def test_many_requests(every):
+    """Of 600 requests every one or some are long: the scan finds each of them."""
+    rng = np.random.default_rng(every)
+    lens = [int(rng.integers(17, 40)) if i % every == 0 else int(rng.integers(0, 3))
+            for i in range(600)]
+    run(build(rng, lens, 1, 1, 64, 16), held=[int(rng.integers(0, 2)) for _ in lens])
+
+
+def test_more_units_than_workgroups():
+    """Records and columns that a workgroup takes after its first ones."""
+    rng = np.random.default_rng(21)
+    lens = [100] * 36 + [3] * 4 + [20] * 20
+    run(build(rng, lens, 8, 32, 64, 48))
+
+
+@pytest.mark.parametrize("lens,max_len", [([40, 3, 70], 16), ([40, 3, 70], 0), ([40, 3, 200], 17)])
+def test_longer_than_max_len(lens, max_len):
+    """max_len chooses kernels only."""
+    rng = np.random.default_rng(22)
+    c = build(rng, lens, 1, 3, 64, 48)
+    want, before = reference(c), c["state"].clone()
+    out = nv.gdn_attention(**dict(c, max_len=max_len))
+    cu, got, state = c["cu_lens"].tolist(), out.double().cpu().numpy(), c["state"].double().cpu().numpy()
+    for r, ref in enumerate(want):
+        compare(got[cu[r]:cu[r + 1]], state[int(c["slots"][r])], ref, (lens, max_len, r),
+                chunked=None if max_len > 16 else False)
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+def test_no_tokens(pad):
+    rng = np.random.default_rng(23)
+    c = build(rng, [0, 0], 1, 2, 64, 32, pad=pad)
+    before = c["state"].clone()
+    out = torch.full((pad, 2, 32), 5.0, dtype=BF16, device=DEV)
+    for max_len in (0, 1, 100):
+        nv.gdn_attention(**dict(c, max_len=max_len), out=out)
+        assert bool((out == 5).all())
+        assert torch.equal(c["state"].view(torch.int32), before.view(torch.int32))
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1], [60, 70, 100]])
+def test_what_is_not_finite_stays_with_its_request(lens):
+    """NaN and infinities of one request's inputs leave the others alone."""
+    rng = np.random.default_rng(24)
+    c = build(rng, lens, 2, 4, 128, 64)
+    clean = dict(c, state=c["state"].clone())
+    want = nv.gdn_attention(**clean)
+    lo, hi = int(c["cu_lens"][1]), int(c["cu_lens"][2])
+    bad = dict(c, **{x: c[x].clone() for x in ("q", "k", "v", "alpha", "beta")})
+    bad["q"][lo:hi], bad["k"][hi - 1] = float("inf"), float("nan")
+    bad["v"][lo], bad["alpha"][lo:hi, 1], bad["beta"][lo] = float("-inf"), float("nan"), float("nan")
+    out = nv.gdn_attention(**bad)
+    assert bool(out[lo:hi].isnan().any())
+    for rows in (slice(0, lo), slice(hi, None)):
+        assert torch.equal(out[rows], want[rows])
+    for r in (0, 2):
+        s = int(c["slots"][r])
+        assert torch.equal(bad["state"][s], clean["state"][s])
