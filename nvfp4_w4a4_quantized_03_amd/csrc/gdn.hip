@@ -638,23 +638,24 @@ prepare_kernel(const GdnArgs a, int k_heads, int units) {
   } while (kAhead && (i += gridDim.x) < units);
 }
 
-// The scan: 32 columns of a request's head a workgroup of five waves.
+// The scan: 32 columns of a request's head are an item; a workgroup of five waves
+// goes through the chunks of its items.
 //
 // What the next chunk waits for is the way from one state to the next, so that
 // is all that the two state waves do, 16 columns each: K S0, R, U, K^T U.  The
 // two output waves take Q S0 and then P U, from operands that a state wave leaves
 // in LDS as it makes them.  The loader brings everything from memory to LDS, K, T
-// and V two chunks ahead.
+// and V two chunks ahead, also those of the next item.
 //
 // Barriers, two a chunk.  Behind the first of chunk c, its K, T, V and Q have
 // landed, as has P of c - 1, and S0 of c and U of c - 1 are in LDS: the output
 // waves take those to registers.  Behind the second they have, and the state
 // waves may write U of c and S0 of c + 1 over them.
 //
-// One prompt of 32768 tokens, 16 key and 64 value heads of 128 (a workgroup on
-// each CU): 1003 us, 2.0 a chunk.  The state waves bound it: 797 without output
-// and loader, of which their 98 products a chunk take 330 and the rest is what
-// each product waits for of the one before.  Output alone takes 453, the loads 631.
+// One prompt of 32768 tokens, 16 key and 64 value heads of 128 (an item on each
+// CU): 962 us, 1.9 a chunk.  The state waves bound it: 782 without output and
+// loader, of which their 98 products a chunk take 330 and the rest is what each
+// product waits for of the one before.  Output alone takes 401, the loads 629.
 constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {
@@ -697,12 +698,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* base, 
       reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, bytes, 0x00020000);
 }
 
-// A request's head and columns, and a lane's place in them.
+// A request's head and columns; chunks 0: none.
 struct Scan {
   Request rq;
   int h, hk, slice, chunks;
   int64_t slot0;
-  bool mine;                           // the last slice may have one pair's columns only
 };
 
 constexpr unsigned kOutside = 0x80000000u;         // of the resources' range
@@ -966,28 +966,79 @@ struct State {
   }
 };
 
-// The n-th request of those with at least `least` tokens; -1 if they are fewer.
-// 256 at a time, whose loads do not wait for each other.
-__device__ __forceinline__ int nth_request(const GdnArgs& a, int n) {
+// The n-th request of those with at least `least` tokens and its number; len 0 if
+// they are fewer.  256 at a time, whose loads do not wait for each other.
+__device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* number) {
   const int lane = threadIdx.x & 63;
   for (int base = 0; base < a.n_requests; base += 256) {
-    bool is[4];
+    Request rq[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rq[j] = request_of(a, min(base + 64 * j + lane, a.n_requests - 1));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = min(base + 64 * j + lane, a.n_requests - 1);
-      is[j] = request_of(a, r).len >= a.least && base + 64 * j + lane < a.n_requests;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t all = __ballot(is[j]);
+      const bool is = rq[j].len >= a.least && base + 64 * j + lane < a.n_requests;
+      const uint64_t all = __ballot(is);
       const int count = __popcll(all);
-      if (n < count)
-        return base + 64 * j +
-               __builtin_ctzll(__ballot(is[j] && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
+      if (n < count) {
+        const int at =
+            __builtin_ctzll(__ballot(is && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
+        *number = base + 64 * j + at;
+        return {__builtin_amdgcn_readlane(rq[j].first, at), __builtin_amdgcn_readlane(rq[j].len, at),
+                __builtin_amdgcn_readlane(static_cast<int>(rq[j].slot), at),
+                __builtin_amdgcn_readlane(rq[j].fresh, at) != 0};
+      }
       n -= count;
     }
   }
-  return -1;
+  return {0, 0, 0, false};
+}
+
+// A wave's place in the chunks of its workgroup's items, one item behind the
+// other: chunk c of `w`, `next` the item behind.
+//
+// The value heads of a key head and their slices, which share K, Q and V, run on
+// one XCD and its L2; the key heads go over the XCDs in turn.  Only requests that
+// are long enough count, so that few of them fill the card too.
+struct Cursor {
+  Scan w, next;
+  int c, item;
+
+  __device__ __forceinline__ void look(const GdnArgs& a) {
+    const int slices = (a.dv + kScanCols - 1) / kScanCols;
+    const int share = a.group * slices, k_heads = a.n_heads / a.group;
+    const int at = item / share, unit = at * 8 + blockIdx.x % 8;
+    const int n = unit / k_heads, of_share = item - at * share;
+    int r = 0;
+    next.rq = nth_request(a, n, &r);
+    next.hk = unit - n * k_heads;
+    next.h = next.hk * a.group + of_share / slices;
+    next.slice = of_share % slices;
+    next.chunks = (next.rq.len + kChunk - 1) / kChunk;
+    next.slot0 = next.rq.first / kChunk + r;
+    item += gridDim.x / 8;
+  }
+  __device__ __forceinline__ void start(const GdnArgs& a) {
+    item = blockIdx.x / 8;
+    look(a);
+    w = next;
+    c = 0;
+  }
+  __device__ __forceinline__ bool valid() const { return c < w.chunks; }
+  // To the next chunk; true if that is another item's.  The item behind it is
+  // looked for before the step that leaves it, where that holds up nobody.
+  __device__ __forceinline__ bool step() {
+    if (++c < w.chunks) return false;
+    if (w.chunks == 0) return false;
+    w = next;
+    c = 0;
+    return true;
+  }
+};
+
+template <int DK>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t state_of(const GdnArgs& a, const Scan& w) {
+  return resource(reinterpret_cast<const uint8_t*>(a.state + w.rq.slot * a.slot_stride +
+                                                   static_cast<int64_t>(w.h) * DK * a.dv));
 }
 
 // Bounds of 512 for its 320: at most 256 registers.  More, which LDS would leave
@@ -999,7 +1050,6 @@ scan_kernel(const GdnArgs a) {
   using Loads = ScanLoads<DK, DELTA>;
   __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], out_[2 * Lds::kOut],
       xc_[2 * Lds::kWave];
-  const int slices = (a.dv + kScanCols - 1) / kScanCols;
   const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
   // 0, 1: state, 2, 3: output, 4: loader.  The first wave, with which the fifth
   // shares a SIMD, is not a state wave (1077 -> 1004 us).
@@ -1008,133 +1058,143 @@ scan_kernel(const GdnArgs a) {
   lds_t* const in = (lds_t*)in_;
   lds_t* const out = (lds_t*)out_;
   lds_t* const xc = (lds_t*)xc_;
-  // The value heads of a key head and their slices, which share K, Q and V, run on
-  // one XCD and its L2; the key heads go over the XCDs in turn.  `n` counts the
-  // requests that are long enough, so that few of them fill the card too.
-  const int share = a.group * slices, k_heads = a.n_heads / a.group;
-  for (int item = blockIdx.x / 8;; item += gridDim.x / 8) {
-    Scan w;
-    const int at = item / share, unit = at * 8 + blockIdx.x % 8;
-    const int n = unit / k_heads, of_share = item - at * share;
-    const int r = nth_request(a, n);
-    if (r < 0) break;
-    w.rq = request_of(a, r);
-    w.hk = unit - n * k_heads;
-    w.h = w.hk * a.group + of_share / slices;
-    w.slice = of_share % slices;
-    w.chunks = (w.rq.len + kChunk - 1) / kChunk;
-    w.slot0 = first_slot(a, r);
-    const int col0 = w.slice * kScanCols;          // the last slice may have 16 columns
-
-    if (wave < 2) {
-      const bool mine = col0 + wave * 16 < a.dv;
-      const __amdgpu_buffer_rsrc_t state = resource(reinterpret_cast<const uint8_t*>(
-          a.state + w.rq.slot * a.slot_stride + static_cast<int64_t>(w.h) * DK * a.dv));
-      const unsigned at = mine ? (8 * g4 * a.dv + col0 + wave * 16 + lr) * 4 : kOutside;
-      const float* const decays = a.decays + w.slot0 * a.n_heads + w.h;
-      State<DK, DELTA> s;
-#pragma unroll
-      for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s.st[t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-              state, w.rq.fresh ? kOutside : at, (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0));
-      s.parts(0, DK / 32);
-      s.leave(xc + wave * Lds::kWave);
-      int place = 0;
-      float of_64 = 0.0f;                          // decays of 64 chunks, one a lane
-      for (int c = 0; c < w.chunks; ++c) {
-        if (c % 64 == 0 && c + lane < w.chunks) of_64 = decays[(c + lane) * static_cast<int64_t>(a.n_heads)];
-        const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of_64), c % 64));
-        __builtin_amdgcn_s_waitcnt(0);             // S0 and U are in LDS
-        stage_barrier();
-        s.chunk(decay, wave, in + place * Lds::kIn, xc + wave * Lds::kWave);
-        place = place == kRing - 1 ? 0 : place + 1;
+  Cursor at;
+  at.start(a);
+  int place = 0;
+  if (wave < 2) {
+    State<DK, DELTA> s;
+    float of_64 = 0.0f;                            // decays of 64 chunks, one a lane
+    for (;;) {
+      // the last slice may have one wave's columns only
+      const int col = at.w.slice * kScanCols + wave * 16;
+      const unsigned place_in = col < a.dv ? (8 * g4 * a.dv + col + lr) * 4 : kOutside;
+      if (at.valid() && (at.c & 63) == 0) {
+        const float* const decays = a.decays + at.w.slot0 * a.n_heads + at.w.h;
+        if (at.c + lane < at.w.chunks) of_64 = decays[(at.c + lane) * static_cast<int64_t>(a.n_heads)];
       }
-      __builtin_amdgcn_s_waitcnt(0);
+      if (at.valid() && at.c == 0) {
+        const __amdgpu_buffer_rsrc_t state = state_of<DK>(a, at.w);
+#pragma unroll
+        for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s.st[t][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                state, at.w.rq.fresh ? kOutside : place_in, (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0));
+        at.look(a);
+        s.parts(0, DK / 32);
+        s.leave(xc + wave * Lds::kWave);
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0): S0 and U are in LDS
       stage_barrier();
+      if (!at.valid()) break;
+      const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of_64), at.c & 63));
+      s.chunk(decay, wave, in + place * Lds::kIn, xc + wave * Lds::kWave);
+      place = place == kRing - 1 ? 0 : place + 1;
+      if (at.c == at.w.chunks - 1) {
+        const __amdgpu_buffer_rsrc_t state = state_of<DK>(a, at.w);
 #pragma unroll
-      for (int t = 0; t < DK / 16; ++t)
+        for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s.st[t][i]), state, at,
-                                                (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0);
-      stage_barrier();
-    } else if (wave < 4) {
-      const lds_t* const from = xc + (wave - 2) * Lds::kWave;
-      const int col = col0 + (wave - 2) * 16;
-      const bool mine = col < a.dv;
-      f32x4 o[4];
-      int place = 0;
-      for (int c = 0; c <= w.chunks; ++c) {
-        stage_barrier();
-        u32x4 s0[DK / 32];
-        f32x4 u[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) u[t] = __builtin_bit_cast(f32x4, operand_at(from + Lds::kU, t));
-#pragma unroll
-        for (int s = 0; s < DK / 32; ++s) s0[s] = operand_at(from + Lds::kS, s);
-        __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
-        stage_barrier();
-        if (c > 0) {
-          const lds_t* const p = out + (~c & 1) * Lds::kOut + Lds::kP;
-          const int64_t t0 = w.rq.first + static_cast<int64_t>(c - 1) * kChunk;
-          const int len = min(w.rq.len - (c - 1) * kChunk, kChunk);
-          // it ends with the rows that there are
-          const __amdgpu_buffer_rsrc_t rsrc =
-              resource(a.out + t0 * a.out_token + w.h * a.out_head + col * 2,
-                       mine ? static_cast<unsigned>(len * a.out_token) : 0);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            Parts<DELTA ? 2 : 1> y;                // the plain rule's U is bf16
-            y.of(u[2 * s], u[2 * s + 1]);
-#pragma unroll
-            for (int i = 0; i < (DELTA ? 2 : 1); ++i)
-#pragma unroll
-              for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(p, tri(t, s)), y.p[i], o[t]);
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
-              __builtin_amdgcn_raw_buffer_store_b16(
-                  bf16_bits(o[t][i]), rsrc, static_cast<unsigned>(row * a.out_token) + lr * 2, 0, 0);
-            }
-        }
-        if (c < w.chunks) {
-          const lds_t* const q = out + (c & 1) * Lds::kOut + Lds::kQ;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int s = 0; s < DK / 32; ++s)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(q, t, s), s0[s], o[t]);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) o[t] *= row_factors(in + place * Lds::kIn + Lds::kRows, 1, t);
-          place = place == kRing - 1 ? 0 : place + 1;
-        }
+          for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s.st[t][i]), state, place_in,
+                                                  (32 * (t / 2) + 4 * (t % 2) + i) * a.dv * 4, 0);
       }
-    } else {
-      Loads::q(a, w, 0, out);
-      Loads::in(a, w, 0, in);
-      Loads::in(a, w, 1, in + Lds::kIn);
-      int place = 2;
-      for (int c = 0; c <= w.chunks; ++c) {
-        // but for K, T and V of chunk c + 1, all that was asked for has landed
-        __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIn));
-        stage_barrier();
-        Loads::q(a, w, c + 1, out + (~c & 1) * Lds::kOut);
-        Loads::p(a, w, c, out + (c & 1) * Lds::kOut);
-        Loads::in(a, w, c + 2, in + place * Lds::kIn);
-        place = place == kRing - 1 ? 0 : place + 1;
-        stage_barrier();
-      }
-      // nothing is on its way to LDS when it is used again or released
-      __builtin_amdgcn_s_waitcnt(0);
+      at.step();
     }
-    // the next item's loads and operands find LDS free
-    __syncthreads();
+    stage_barrier();
+  } else if (wave < 4) {
+    const lds_t* const from = xc + (wave - 2) * Lds::kWave;
+    f32x4 o[4];
+    int len = 0;                                   // rows of the chunk whose outputs o is
+    const uint8_t* rows = a.out;
+    bool mine = false;
+    at.look(a);
+    for (int g = 0;; g ^= 1) {
+      stage_barrier();
+      u32x4 s0[DK / 32];
+      f32x4 u[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = __builtin_bit_cast(f32x4, operand_at(from + Lds::kU, t));
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s) s0[s] = operand_at(from + Lds::kS, s);
+      __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
+      stage_barrier();
+      if (len > 0) {
+        const lds_t* const p = out + (g ^ 1) * Lds::kOut + Lds::kP;
+        // it ends with the rows that there are
+        const __amdgpu_buffer_rsrc_t rsrc =
+            resource(rows, mine ? static_cast<unsigned>(len * a.out_token) : 0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          Parts<DELTA ? 2 : 1> y;                  // the plain rule's U is bf16
+          y.of(u[2 * s], u[2 * s + 1]);
+#pragma unroll
+          for (int i = 0; i < (DELTA ? 2 : 1); ++i)
+#pragma unroll
+            for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(p, tri(t, s)), y.p[i], o[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 32 * (t / 2) + 8 * g4 + 4 * (t % 2) + i;
+            __builtin_amdgcn_raw_buffer_store_b16(
+                bf16_bits(o[t][i]), rsrc, static_cast<unsigned>(row * a.out_token) + lr * 2, 0, 0);
+          }
+      }
+      if (!at.valid()) break;
+      const lds_t* const q = out + g * Lds::kOut + Lds::kQ;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < DK / 32; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(q, t, s), s0[s], o[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) o[t] *= row_factors(in + place * Lds::kIn + Lds::kRows, 1, t);
+      place = place == kRing - 1 ? 0 : place + 1;
+      const int col = at.w.slice * kScanCols + (wave - 2) * 16;
+      mine = col < a.dv;
+      len = min(at.w.rq.len - at.c * kChunk, kChunk);
+      rows = a.out + (at.w.rq.first + static_cast<int64_t>(at.c) * kChunk) * a.out_token +
+             at.w.h * a.out_head + col * 2;
+      if (at.step()) at.look(a);
+    }
+  } else {
+    // two chunks, one and none behind `at`
+    Scan w0 = at.w, w1;
+    int c0 = 0, c1;
+    Loads::q(a, at.w, 0, out);
+    Loads::in(a, at.w, 0, in);
+    if (at.w.chunks == 1) at.look(a);
+    bool looked = at.w.chunks == 1;
+    if (at.step()) looked = false;
+    w1 = at.w;
+    c1 = at.c;
+    Loads::in(a, w1, c1, in + Lds::kIn);
+    if (!looked) at.look(a);
+    if (at.step()) at.look(a);
+    place = 2;
+    for (int g = 0;; g ^= 1) {
+      // but for K, T and V of the next chunk, all that was asked for has landed
+      __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIn));
+      stage_barrier();
+      Loads::q(a, w1, c1, out + (g ^ 1) * Lds::kOut);
+      Loads::p(a, w0, c0, out + g * Lds::kOut);
+      // the rest is not needed that soon, and would hold up the second barrier
+      // (plain rule, 7 prompts: 42 -> 37 us)
+      stage_barrier();
+      Loads::in(a, at.w, at.c, in + place * Lds::kIn);
+      place = place == kRing - 1 ? 0 : place + 1;
+      if (c0 >= w0.chunks) break;
+      w0 = w1;
+      c0 = c1;
+      w1 = at.w;
+      c1 = at.c;
+      if (at.step()) at.look(a);
+    }
+    // nothing is on its way to LDS when it is released
+    __builtin_amdgcn_s_waitcnt(0);
   }
 }
 
@@ -1157,14 +1217,17 @@ GdnArgs args_of(const GdnCall& c) {
   return a;
 }
 
-// Workgroups of the scan, which go on to further items: passing over a request of
-// few tokens costs less there than starting a workgroup for it does.
-constexpr int kScanGrid = 1024;
+// Workgroups of the scan, one a CU, which go on to further items without a pause.
+// 32 requests of 17 to 64 tokens, 64 heads of 128 x 128 (32 items a workgroup): 153
+// us in all; 171 with 1024 workgroups, 441 where each item began anew.
+constexpr int kScanGrid = 256;
 
 // Workgroups of four waves of the preparation, two a CU, which go on to further units
 constexpr int kPrepareGrid = 512;
 
-// Requests of at most this many tokens are taken token after token.
+// Requests of at most this many tokens are taken token after token.  Between 18 and
+// 24 both ways take as long: 1, 8 and 32 requests of 16 tokens, 64 heads of 128 x
+// 128, so 22, 42 and 117 us, of 24 31, 58 and 162; in chunks 26, 52 and 153.
 constexpr int kFewTokens = 16;
 
 // Chunk slots of a call (first_slot), and bytes of a slot's records and decay
