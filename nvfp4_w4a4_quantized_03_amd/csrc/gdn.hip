@@ -46,8 +46,7 @@ struct GdnArgs {
   int n_tokens, n_requests, n_heads, group, dv;
   float scale;
   int normalize;
-  int least;                          // tokens that a request of the launch has at least
-  int most;                           // and at most
+  int few;                            // requests of at most so many tokens go token after token
   uint8_t* records;                   // of chunks and heads
   float* decays;                      // of whole chunks
 };
@@ -93,17 +92,15 @@ __device__ __forceinline__ Request request_of(const GdnArgs& a, int r) {
 // lines: 57.3 -> 52.9 us; states written past the caches, where they would take
 // the place of what the next layer reads: 52.9 -> 44.6.
 template <int DK, bool DELTA>
-__global__ void __launch_bounds__(256)
-gdn_tokens_kernel(const GdnArgs a) {
+__device__ __forceinline__ void few_tokens(const GdnArgs& a, int wave) {
   constexpr int R = DK / 8;
   const int lane = threadIdx.x & 63;
-  const int slices = (a.dv + 127) >> 7;
-  const int col = (blockIdx.x % slices * 4 + (threadIdx.x >> 6)) * 32 + (lane & 7) * 4;
-  if (col >= a.dv) return;
-  const int rh = blockIdx.x / slices;
+  const int slices = (a.dv + 31) >> 5, rh = wave / slices;
+  const int col = (wave - rh * slices) * 32 + (lane & 7) * 4;
   const int r = rh / a.n_heads, h = rh - r * a.n_heads, hk = h / a.group;
+  if (r >= a.n_requests || col >= a.dv) return;
   const Request rq = request_of(a, r);
-  if (rq.len < a.least || rq.len > a.most) return;
+  if (rq.len < 1 || rq.len > a.few) return;
   const int row0 = (lane >> 3) * R;
   float* sp = a.state + rq.slot * a.slot_stride + (static_cast<int64_t>(h) * DK + row0) * a.dv + col;
   f32x4 s[R];
@@ -157,6 +154,12 @@ gdn_tokens_kernel(const GdnArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(sp + i * a.dv));
+}
+
+template <int DK, bool DELTA>
+__global__ void __launch_bounds__(256)
+gdn_tokens_kernel(const GdnArgs a) {
+  few_tokens<DK, DELTA>(a, __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)));
 }
 
 // ---------------------------------------------------------------------------
@@ -341,7 +344,15 @@ __device__ __forceinline__ void operand_rows(const float* buf, int half, F&& put
 
 template <int DK, bool DELTA, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1)
-prepare_kernel(const GdnArgs a, int k_heads, int units) {
+prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
+  // The workgroups behind those of the preparation take the requests of few tokens,
+  // whose states come from memory while the others compute (3 prompts and 21 single
+  // tokens, 48 heads: 29 us, one after the other 38).
+  if (static_cast<int>(blockIdx.x) >= workgroups) {
+    few_tokens<DK, DELTA>(a, __builtin_amdgcn_readfirstlane((blockIdx.x - workgroups) * WAVES +
+                                                            (threadIdx.x >> 6)));
+    return;
+  }
   using L = Rows<DK>;
   using Rec = Record<DELTA>;
   __shared__ PrepareLds<DK, DELTA, WAVES> lds;
@@ -365,7 +376,7 @@ prepare_kernel(const GdnArgs a, int k_heads, int units) {
     if (r < 0) return u;
     const Request rq = request_of(a, r);
     const int c = u.slot - first_slot(a, r);
-    if (rq.len < a.least || c < 0 || c * kChunk >= rq.len) return u;
+    if (rq.len <= a.few || c < 0 || c * kChunk >= rq.len) return u;
     u.len = min(rq.len - c * kChunk, kChunk);
     u.t0 = rq.first + static_cast<int64_t>(c) * kChunk;
     return u;
@@ -397,7 +408,7 @@ prepare_kernel(const GdnArgs a, int k_heads, int units) {
   int i = blockIdx.x;
   do {
     const Unit u = next;
-    next = unit_at(kAhead ? i + gridDim.x : units);
+    next = unit_at(kAhead ? i + workgroups : units);
     const int slot = u.slot, hk = u.hk, len = u.len;
     const int64_t t0 = u.t0;
     if (len == 0) {
@@ -635,7 +646,7 @@ prepare_kernel(const GdnArgs a, int k_heads, int units) {
         __builtin_amdgcn_wave_barrier();
       }
     }
-  } while (kAhead && (i += gridDim.x) < units);
+  } while (kAhead && (i += workgroups) < units);
 }
 
 // The scan: 32 columns of a request's head are an item; a workgroup of five waves
@@ -966,7 +977,7 @@ struct State {
   }
 };
 
-// The n-th request of those with at least `least` tokens and its number; len 0 if
+// The n-th request of those with more than `few` tokens and its number; len 0 if
 // they are fewer.  256 at a time, whose loads do not wait for each other.
 __device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* number) {
   const int lane = threadIdx.x & 63;
@@ -976,7 +987,7 @@ __device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* num
     for (int j = 0; j < 4; ++j) rq[j] = request_of(a, min(base + 64 * j + lane, a.n_requests - 1));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool is = rq[j].len >= a.least && base + 64 * j + lane < a.n_requests;
+      const bool is = rq[j].len > a.few && base + 64 * j + lane < a.n_requests;
       const uint64_t all = __ballot(is);
       const int count = __popcll(all);
       if (n < count) {
@@ -1236,24 +1247,29 @@ int64_t record_bytes(bool delta) {
   return delta ? Record<true>::kBytes : Record<false>::kBytes;
 }
 
+template <int DK, bool DELTA, int WAVES>
+void launch_prepare(const GdnArgs& a, const GdnCall& c, int waves, hipStream_t stream) {
+  const int units = static_cast<int>(chunk_slots(c) * c.n_k_heads);
+  const int workgroups = WAVES == 4 && units > kPrepareGrid ? kPrepareGrid : units;
+  prepare_kernel<DK, DELTA, WAVES>
+      <<<static_cast<unsigned>(workgroups + (waves + WAVES - 1) / WAVES), WAVES * 64, 0, stream>>>(
+          a, static_cast<int>(c.n_k_heads), units, workgroups);
+}
+
 template <int DK, bool DELTA>
 void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
-  const int64_t rh = c.n_requests * c.n_heads;
-  a.least = 1;
-  a.most = c.max_len > kFewTokens ? kFewTokens : 0x7FFFFFFF;
-  gdn_tokens_kernel<DK, DELTA>
-      <<<static_cast<unsigned>(rh * ((c.dv + 127) / 128)), 256, 0, stream>>>(a);
-  if (c.max_len <= kFewTokens) return;
-  a.least = kFewTokens + 1;
+  const int waves = static_cast<int>(c.n_requests * c.n_heads * ((c.dv + 31) / 32));
+  a.few = 0x7FFFFFFF;
+  if (c.max_len <= kFewTokens) {
+    gdn_tokens_kernel<DK, DELTA><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, stream>>>(a);
+    return;
+  }
+  a.few = kFewTokens;
   a.records = static_cast<uint8_t*>(c.workspace);
   a.decays = reinterpret_cast<float*>(a.records + chunk_slots(c) * c.n_heads * record_bytes(DELTA));
-  const int units = static_cast<int>(chunk_slots(c) * c.n_k_heads);
-  const int k_heads = static_cast<int>(c.n_k_heads);
-  if (a.group == 1) prepare_kernel<DK, DELTA, 1><<<units, 64, 0, stream>>>(a, k_heads, units);
-  else if (a.group == 2) prepare_kernel<DK, DELTA, 2><<<units, 128, 0, stream>>>(a, k_heads, units);
-  else
-    prepare_kernel<DK, DELTA, 4><<<units < kPrepareGrid ? units : kPrepareGrid, 256, 0, stream>>>(
-        a, k_heads, units);
+  if (a.group == 1) launch_prepare<DK, DELTA, 1>(a, c, waves, stream);
+  else if (a.group == 2) launch_prepare<DK, DELTA, 2>(a, c, waves, stream);
+  else launch_prepare<DK, DELTA, 4>(a, c, waves, stream);
   // a multiple of 8 that has every item of every key head
   const int64_t eights = (c.n_requests * c.n_k_heads + 7) / 8;
   const int64_t blocks = eights * 8 * a.group * ((c.dv + kScanCols - 1) / kScanCols);
