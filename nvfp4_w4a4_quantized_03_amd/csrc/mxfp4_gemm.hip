@@ -51,10 +51,11 @@ __device__ __forceinline__ f32x16 product(u32x4 a, unsigned sa, u32x4 b, unsigne
 }
 
 // ---------------------------------------------------------------------------
-// Streaming kernel: one operand (L) of at most 64 rows, the other (S) read once.
+// Streaming kernel: one operand (L) of at most 64 rows, the other (S) read once; or
+// L in groups of 64 rows, for small products of a long K.
 //
-// A workgroup of NW waves takes SF 16 rows of S and all of L (LF 16 rows), the
-// waves a part of K each.  Operands go from memory straight to registers: a
+// A workgroup of NW waves takes SF 16 rows of S and LF 16 rows of L, the waves a
+// part of K each.  Operands go from memory straight to registers: a
 // wave has the loads of up to eight k-steps (128 of K) in flight at once, for K
 // up to 8192 mostly all that it needs, and L comes from L2.  The waves' sums meet in
 // LDS and are added in a fixed order.  What bounds it is the latency of one
@@ -126,6 +127,7 @@ mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict
                   void* __restrict__ out, int64_t ldo) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (SF * 16);
+  const int64_t lrow0 = static_cast<int64_t>(blockIdx.y) * (LF * 16);
   const int blocks = static_cast<int>(k / 32), steps = (blocks + 3) >> 2;
   const int from = steps * wave / NW, to = steps * (wave + 1) / NW;
 
@@ -134,7 +136,7 @@ mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict
   StreamOperand<SF, STEPS, RAGGED> so;
   StreamOperand<LF, STEPS, RAGGED> lo;
   so.init(s_codes, s_scales, row0, s_rows, k, lane);
-  lo.init(l_codes, l_scales, 0, l_rows, k, lane);
+  lo.init(l_codes, l_scales, lrow0, l_rows, k, lane);
   f32x4 acc[SF][LF] = {};
   for (int st = from; st < to; st += STEPS) {
     const int n = to - st < STEPS ? to - st : STEPS;
@@ -169,7 +171,7 @@ mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict
 #pragma unroll
     for (int w = 1; w < NW; ++w) y += sums[w][tile][l];
     // lane l of a tile: column of A's rows l % 16, four of B's from 4 (l / 16)
-    const int64_t sr = row0 + tile / LF * 16, lr = tile % LF * 16;
+    const int64_t sr = row0 + tile / LF * 16, lr = lrow0 + tile % LF * 16;
     const int64_t m = (S_IS_B ? lr : sr) + (l & 15), n = (S_IS_B ? sr : lr) + (l >> 4) * 4;
     const int64_t rows_m = S_IS_B ? l_rows : s_rows, rows_n = S_IS_B ? s_rows : l_rows;
     if (m >= rows_m) continue;
@@ -596,7 +598,7 @@ hipError_t launch_stream(const uint8_t* s_codes, const uint8_t* s_scales, int64_
                          int64_t k, void* out, int out_dtype, int64_t ldo, hipStream_t stream) {
   const int64_t groups = (s_rows + SF * 16 - 1) / (SF * 16);
   if (groups > 0x7FFFFF) return hipErrorInvalidValue;
-  const unsigned grid = static_cast<unsigned>(groups);
+  const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>((l_rows + LF * 16 - 1) / (LF * 16)));
   if (out_dtype == kOutF32)
     mxfp4_gemm_stream<NW, SF, LF, RAGGED, S_IS_B, 0><<<grid, NW * 64, 0, stream>>>(
         s_codes, s_scales, s_rows, l_codes, l_scales, l_rows, k, out, ldo);
@@ -659,6 +661,28 @@ bool large_tiles(int64_t m, int64_t n) {
          27.0 * fs + (rs > 256 ? 27.0 : rs > 0 ? 16.5 : 0.0);
 }
 
+// Products whose tiles would leave most CUs idle while each goes through a long K:
+// one round of streaming workgroups, of 16 or 32 rows of the longer side against 64
+// of the other, whose waves share K.  K = 5120, tiles and streaming: 128 x 128 11.4
+// and 9.5 us, 457 x 312 12.1 and 9.7, 128 x 4096 17.8 and 11.9, 700 x 700 22.3 and
+// 11.9; 128 x 2048 x 17408 52 and 27.  Shorter K: 512 x 1000 x 2048 7.1 and 6.9, 512
+// x 512 x 1024 5.0 and 6.3.
+int64_t small_groups(int64_t m, int64_t n, int sf) {
+  const int64_t s = m <= n ? n : m, l = m <= n ? m : n;
+  return (s + 16 * sf - 1) / (16 * sf) * ((l + 63) / 64);
+}
+bool small_product(int64_t m, int64_t n, int64_t k) {
+  return k >= 2048 && m < (1 << 16) && n < (1 << 16) && small_groups(m, n, 2) <= 256;
+}
+template <bool RAGGED, bool S_IS_B>
+hipError_t stream_small(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
+                        const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt, int64_t ldo,
+                        hipStream_t st) {
+  return small_groups(s_rows, l_rows, 1) <= 256
+             ? launch_stream<8, 1, 4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st)
+             : launch_stream<8, 2, 4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+}
+
 template <bool RAGGED>
 hipError_t gemm_of(const uint8_t* ac, const uint8_t* as, int64_t m, const uint8_t* bc,
                    const uint8_t* bs, int64_t n, int64_t k, void* out, int dt, int64_t ldo,
@@ -667,6 +691,9 @@ hipError_t gemm_of(const uint8_t* ac, const uint8_t* as, int64_t m, const uint8_
     return stream_of<RAGGED, true>(bc, bs, n, ac, as, m, k, out, dt, ldo, st);
   if (n <= 64)
     return stream_of<RAGGED, false>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  if (small_product(m, n, k))
+    return m <= n ? stream_small<RAGGED, true>(bc, bs, n, ac, as, m, k, out, dt, ldo, st)
+                  : stream_small<RAGGED, false>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
   return large_tiles(m, n)
              ? launch_tiled<2, 4, 4, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st)
              : launch_tiled<2, 2, 2, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);

@@ -141,7 +141,13 @@ STREAMS = [(1, 4097, 96), (9, 8200, 128), (16, 13000, 160), (3, 16500, 64), (20,
            (40, 33, 12320), (4100, 7, 224), (13000, 32, 128), (9001, 64, 160), (70, 17, 640)]
 
 
-@pytest.mark.parametrize("m,n,k", GEMMS + STREAMS)
+# small products of a long K, in groups of 64 rows of the shorter side, both ways
+# round; and their neighbours in tiles
+SMALL = [(457, 312, 2048), (312, 457, 2080), (65, 65, 5152), (65, 4096, 2048), (4090, 66, 2592),
+         (700, 700, 2048), (129, 1300, 4128), (128, 128, 2016), (4097, 130, 2048)]
+
+
+@pytest.mark.parametrize("m,n,k", GEMMS + STREAMS + SMALL)
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_gemm(m, n, k, dt):
     _say("gemm", m, n, k, dt)
