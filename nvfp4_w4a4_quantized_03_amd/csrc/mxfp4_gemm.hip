@@ -273,22 +273,25 @@ struct Loads {
   // stage, or past it)
   __device__ __forceinline__ void issue_codes(int stage, int left, uint8_t* lds, int wave,
                                               int lane) const {
+    // a scalar offset within the resource, also where every lane's lies beyond it
+    const int from = left > 0 ? stage * kRowBytes : 0;
 #pragma unroll
     for (int i = 0; i < kCodes; ++i) {
       const int q = (wave * kCodes + i) * 64 + lane;
       const unsigned off = ((q & 7) ^ piece_xor(q >> 3)) < left ? code_off[i] : 0x80000000u;
-      lds_buf16(codes, lds + (wave * kCodes + i) * 1024, off, stage * kRowBytes);
+      lds_buf16(codes, lds + (wave * kCodes + i) * 1024, off, from);
     }
   }
 
-  // the scales of stages 2 window and 2 window + 1
-  __device__ __forceinline__ void issue_scales(int window, uint8_t* lds, int wave) const {
+  // the scales of stages 2 window and 2 window + 1; past the end of K any, which
+  // are not used
+  __device__ __forceinline__ void issue_scales(int window, int blocks, uint8_t* lds, int wave) const {
+    const int from = window * 16 < blocks ? window * 16 : 0;
 #pragma unroll
     for (int i = 0; i < kPerWave; ++i) {
-      lds_buf16(scales, lds + (wave * kPerWave + i) * 1024, scale_off[i], window * 16);
+      lds_buf16(scales, lds + (wave * kPerWave + i) * 1024, scale_off[i], from);
       if constexpr (RAGGED)
-        lds_buf4(scales, lds + kRows * 16 + (wave * kPerWave + i) * 256, scale_off[i] + 16,
-                 window * 16);
+        lds_buf4(scales, lds + kRows * 16 + (wave * kPerWave + i) * 256, scale_off[i] + 16, from);
     }
   }
 };
@@ -427,8 +430,8 @@ mxfp4_gemm_tiled(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict_
     lb.issue_codes(st, blocks - 8 * st, slot + kB, wave, lane);
   };
   auto issue_scales = [&](int window) {
-    la.issue_scales(window, scale_lds, wave);
-    lb.issue_scales(window, scale_lds + kSB, wave);
+    la.issue_scales(window, blocks, scale_lds, wave);
+    lb.issue_scales(window, blocks, scale_lds + kSB, wave);
   };
   issue_scales(0);
   issue_a(0, s0);
