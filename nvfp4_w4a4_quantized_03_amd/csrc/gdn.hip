@@ -59,8 +59,13 @@ __device__ __forceinline__ unsigned short bf16_bits(float f) {
   return __builtin_bit_cast(unsigned short, static_cast<__bf16>(f));
 }
 
-// Sum over the 8 lanes that share lane & 7; every one of them gets it.
+// Sum over the lanes that share lane % LC; every one of them gets it.
+template <int LC>
 __device__ __forceinline__ float sum_rows(float x) {
+  if constexpr (LC <= 2)
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x122, 0xF, 0xF, false));
+  if constexpr (LC <= 4)
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x124, 0xF, 0xF, false));
   x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x128, 0xF, 0xF, false));
   unsigned u = __float_as_uint(x);
   auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
@@ -84,35 +89,50 @@ __device__ __forceinline__ Request request_of(const GdnArgs& a, int r) {
   return {lo, held && hi > lo ? hi - lo : 0, held ? slot : 0, a.cached && a.cached[r] <= 0};
 }
 
-// Token after token.  Lane l has the dk / 8 rows from dk / 8 * (l / 8) and
-// the four columns from 4 (l % 8) of its wave's 32.
+// Token after token.  Lane l has the four columns from 4 (l % LC) of its wave's 4 LC
+// and the dk LC / 64 rows from there times l / LC.
 //
 // Bound by reading and writing the states: 32 requests of one token, 64 heads of
 // 128 x 128 (268 MB): 44.6 us, 6.0 TB/s.  Waves of 16 columns, which ask for half
 // lines: 57.3 -> 52.9 us; states written past the caches, where they would take
 // the place of what the next layer reads: 52.9 -> 44.6.
-template <int DK, bool DELTA>
+template <int DK, bool DELTA, int LC>
 __device__ __forceinline__ void few_tokens(const GdnArgs& a, int wave) {
-  constexpr int R = DK / 8;
+  constexpr int R = DK / 64 * LC;
   const int lane = threadIdx.x & 63;
-  const int slices = (a.dv + 31) >> 5, rh = wave / slices;
-  const int col = (wave - rh * slices) * 32 + (lane & 7) * 4;
+  const int slices = (a.dv + 4 * LC - 1) / (4 * LC), rh = wave / slices;
+  const int col = (wave - rh * slices) * 4 * LC + lane % LC * 4;
   const int r = rh / a.n_heads, h = rh - r * a.n_heads, hk = h / a.group;
   if (r >= a.n_requests || col >= a.dv) return;
   const Request rq = request_of(a, r);
   if (rq.len < 1 || rq.len > a.few) return;
-  const int row0 = (lane >> 3) * R;
+  const int row0 = lane / LC * R;
   float* sp = a.state + rq.slot * a.slot_stride + (static_cast<int64_t>(h) * DK + row0) * a.dv + col;
   f32x4 s[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
     s[i] = rq.fresh ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : *reinterpret_cast<const f32x4*>(sp + i * a.dv);
-  for (int t = rq.first; t < rq.first + rq.len; ++t) {
-    typedef unsigned short row_t __attribute__((ext_vector_type(R)));
-    const row_t kr = *reinterpret_cast<const row_t*>(a.k + t * a.k_token + hk * a.k_head + row0 * 2);
-    const row_t qr = *reinterpret_cast<const row_t*>(a.q + t * a.q_token + hk * a.q_head + row0 * 2);
-    const u16x4 vr = *reinterpret_cast<const u16x4*>(a.v + t * a.v_token + h * a.v_head + col * 2);
-    const float al = a.alpha[t * a.ld_alpha + h];
+  // a token's inputs, asked for while the one before is computed
+  typedef unsigned short row_t __attribute__((ext_vector_type(R)));
+  struct Token {
+    row_t k, q;
+    u16x4 v;
+    float alpha, beta;
+  };
+  auto token = [&](int t) __attribute__((always_inline)) {
+    return Token{*reinterpret_cast<const row_t*>(a.k + t * a.k_token + hk * a.k_head + row0 * 2),
+                 *reinterpret_cast<const row_t*>(a.q + t * a.q_token + hk * a.q_head + row0 * 2),
+                 *reinterpret_cast<const u16x4*>(a.v + t * a.v_token + h * a.v_head + col * 2),
+                 a.alpha[t * a.ld_alpha + h], DELTA ? a.beta[t * a.ld_beta + h] : 1.0f};
+  };
+  const int end = rq.first + rq.len;
+  Token next = token(rq.first);
+  for (int t = rq.first; t < end; ++t) {
+    const Token now = next;
+    if (t + 1 < end) next = token(t + 1);
+    const row_t kr = now.k, qr = now.q;
+    const u16x4 vr = now.v;
+    const float al = now.alpha, be = now.beta;
     float kv[R], qv[R];
     f32x4 ks = {}, qs = {};
     float kq = 0.0f, kk = 0.0f, qq = 0.0f;
@@ -129,37 +149,36 @@ __device__ __forceinline__ void few_tokens(const GdnArgs& a, int wave) {
         qs[j] = __builtin_fmaf(qv[i], s[i][j], qs[j]);
       }
     }
-    kq = sum_rows(kq);
+    kq = sum_rows<LC>(kq);
     float rk = 1.0f, rqn = a.scale;
     if (a.normalize) {
-      rk = 1.0f / __builtin_sqrtf(sum_rows(kk) + kNormEps);
-      rqn = a.scale / __builtin_sqrtf(sum_rows(qq) + kNormEps);
+      rk = 1.0f / __builtin_sqrtf(sum_rows<LC>(kk) + kNormEps);
+      rqn = a.scale / __builtin_sqrtf(sum_rows<LC>(qq) + kNormEps);
     }
-    const float be = DELTA ? a.beta[t * a.ld_beta + h] : 1.0f;
     f32x4 u;
     u16x4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       u[j] = bf16_value(vr[j]);
-      if constexpr (DELTA) u[j] = be * (u[j] - al * (rk * sum_rows(ks[j])));
+      if constexpr (DELTA) u[j] = be * (u[j] - al * (rk * sum_rows<LC>(ks[j])));
       u[j] *= rk;                     // the key's norm goes with u into k u^T
-      o[j] = bf16_bits(rqn * __builtin_fmaf(kq, u[j], al * sum_rows(qs[j])));
+      o[j] = bf16_bits(rqn * __builtin_fmaf(kq, u[j], al * sum_rows<LC>(qs[j])));
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = __builtin_fmaf(kv[i], u[j], al * s[i][j]);
-    if (lane < 8)
+    if (lane < LC)
       *reinterpret_cast<u16x4*>(a.out + t * a.out_token + h * a.out_head + col * 2) = o;
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(sp + i * a.dv));
 }
 
-template <int DK, bool DELTA>
+template <int DK, bool DELTA, int LC>
 __global__ void __launch_bounds__(256)
 gdn_tokens_kernel(const GdnArgs a) {
-  few_tokens<DK, DELTA>(a, __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  few_tokens<DK, DELTA, LC>(a, __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)));
 }
 
 // ---------------------------------------------------------------------------
@@ -349,7 +368,7 @@ prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
   // whose states come from memory while the others compute (3 prompts and 21 single
   // tokens, 48 heads: 29 us, one after the other 38).
   if (static_cast<int>(blockIdx.x) >= workgroups) {
-    few_tokens<DK, DELTA>(a, __builtin_amdgcn_readfirstlane((blockIdx.x - workgroups) * WAVES +
+    few_tokens<DK, DELTA, 8>(a, __builtin_amdgcn_readfirstlane((blockIdx.x - workgroups) * WAVES +
                                                             (threadIdx.x >> 6)));
     return;
   }
@@ -1236,10 +1255,10 @@ constexpr int kScanGrid = 256;
 // Workgroups of four waves of the preparation, two a CU, which go on to further units
 constexpr int kPrepareGrid = 512;
 
-// Requests of at most this many tokens are taken token after token.  Between 18 and
-// 24 both ways take as long: 1, 8 and 32 requests of 16 tokens, 64 heads of 128 x
-// 128, so 22, 42 and 117 us, of 24 31, 58 and 162; in chunks 26, 52 and 153.
-constexpr int kFewTokens = 16;
+// Requests of at most this many tokens are taken token after token.  Both ways take
+// as long between 21 and 36: 1, 8 and 32 requests of 64 heads of 128 x 128 17, 40 and
+// 114 us at 16 tokens and 0.5, 1.9 and 5.2 a further one; in chunks 24, 49 and 153.
+constexpr int kFewTokens = 20;
 
 // Chunk slots of a call (first_slot), and bytes of a slot's records and decay
 int64_t chunk_slots(const GdnCall& c) { return c.n_tokens / kChunk + c.n_requests; }
@@ -1261,7 +1280,15 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   const int waves = static_cast<int>(c.n_requests * c.n_heads * ((c.dv + 31) / 32));
   a.few = 0x7FFFFFFF;
   if (c.max_len <= kFewTokens) {
-    gdn_tokens_kernel<DK, DELTA><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, stream>>>(a);
+    // Few waves wait for their own operations: 16 columns each where 32 give at most
+    // one wave to every other SIMD (16 tokens, 64 heads of 128 x 128: 21 us against 17,
+    // 2 requests 22 and 17.6, 4 requests 24.6 and 27.4).
+    if (waves <= 512) {
+      const unsigned narrow = static_cast<unsigned>(c.n_requests * c.n_heads * (c.dv / 16));
+      gdn_tokens_kernel<DK, DELTA, 4><<<(narrow + 3) / 4, 256, 0, stream>>>(a);
+    } else {
+      gdn_tokens_kernel<DK, DELTA, 8><<<static_cast<unsigned>((waves + 3) / 4), 256, 0, stream>>>(a);
+    }
     return;
   }
   a.few = kFewTokens;

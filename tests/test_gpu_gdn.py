@@ -12,7 +12,7 @@ k^T does not lengthen an error, so errors are carried by alpha alone).
   out     2^-8 |o| for its own rounding; scale |q| times the state's error;
           40 2^-24 scale |q| n for its own sum.
 
-Requests of more than 16 tokens go in chunks, whose products take binary32
+Requests of more than 20 tokens go in chunks, whose products take binary32
 operands as sums of bf16 numbers:
 
   out     the state and the scores enter as one bf16 number each, 2^-8: with
@@ -96,7 +96,7 @@ def reference(c, held=None, scale=None):
 def compare(got_o, got_s, ref, what, chunked=None):
     """One request's outputs and state within what the header derives."""
     o, s, size, reach, w, n = ref
-    chunked = len(o) > 16 if chunked is None else chunked
+    chunked = len(o) > 20 if chunked is None else chunked
     assert np.isfinite(got_o).all() and np.isfinite(got_s).all(), what
     e = 40 * 2.0 ** -24
     tol = 2.0 ** -8 * np.abs(o) + ((2.0 ** -8 + 2.0 ** -14) * size if chunked
