@@ -8,8 +8,8 @@
 //
 // One pass over S a token: with a = S^T k and b = S^T q of the old state,
 //   u = beta (v - alpha a),  o = scale (alpha b + (k.q) u).
-// A column of S depends on no other column, so a wave owns 16 columns and all
-// rows, and nothing is exchanged between waves.  The state passes once in and
+// A column of S depends on no other column, so a wave owns 16 or 32 columns and
+// all rows, and nothing is exchanged between waves.  The state passes once in and
 // once out, whatever the tokens in between; for single tokens that is all there
 // is to move, and the kernel is bound by it.
 #include <hip/hip_runtime.h>
@@ -47,6 +47,7 @@ struct GdnArgs {
   float scale;
   int normalize;
   int few;                            // requests of at most so many tokens go token after token
+  int share, parts;                   // items of a part of a key head's, parts
   uint8_t* records;                   // of chunks and heads
   float* decays;                      // of whole chunks
 };
@@ -1027,22 +1028,24 @@ __device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* num
 // other: chunk c of `w`, `next` the item behind.
 //
 // The value heads of a key head and their slices, which share K, Q and V, run on
-// one XCD and its L2; the key heads go over the XCDs in turn.  Only requests that
-// are long enough count, so that few of them fill the card too.
+// one XCD and its L2; the key heads go over the XCDs in turn, in parts if there are
+// fewer than 8 of them.  Only requests that are long enough count, so that few of
+// them fill the card too.
 struct Cursor {
   Scan w, next;
   int c, item;
 
   __device__ __forceinline__ void look(const GdnArgs& a) {
     const int slices = (a.dv + kScanCols - 1) / kScanCols;
-    const int share = a.group * slices, k_heads = a.n_heads / a.group;
-    const int at = item / share, unit = at * 8 + blockIdx.x % 8;
-    const int n = unit / k_heads, of_share = item - at * share;
+    const int per_request = a.n_heads / a.group * a.parts;
+    const int at = item / a.share, unit = at * 8 + blockIdx.x % 8;
+    const int n = unit / per_request, part = unit - n * per_request;
     int r = 0;
     next.rq = nth_request(a, n, &r);
-    next.hk = unit - n * k_heads;
-    next.h = next.hk * a.group + of_share / slices;
-    next.slice = of_share % slices;
+    next.hk = part / a.parts;
+    const int of_head = part % a.parts * a.share + item - at * a.share;
+    next.h = next.hk * a.group + of_head / slices;
+    next.slice = of_head % slices;
     next.chunks = (next.rq.len + kChunk - 1) / kChunk;
     next.slot0 = next.rq.first / kChunk + r;
     item += gridDim.x / 8;
@@ -1297,9 +1300,13 @@ void launch_dk(GdnArgs a, const GdnCall& c, hipStream_t stream) {
   if (a.group == 1) launch_prepare<DK, DELTA, 1>(a, c, waves, stream);
   else if (a.group == 2) launch_prepare<DK, DELTA, 2>(a, c, waves, stream);
   else launch_prepare<DK, DELTA, 4>(a, c, waves, stream);
-  // a multiple of 8 that has every item of every key head
-  const int64_t eights = (c.n_requests * c.n_k_heads + 7) / 8;
-  const int64_t blocks = eights * 8 * a.group * ((c.dv + kScanCols - 1) / kScanCols);
+  const int items = a.group * static_cast<int>((c.dv + kScanCols - 1) / kScanCols);
+  a.parts = static_cast<int>((7 + c.n_k_heads) / c.n_k_heads);
+  while (items % a.parts != 0 && a.parts < 64) ++a.parts;
+  if (items % a.parts != 0) a.parts = 1;
+  a.share = items / a.parts;
+  // a multiple of 8 that has every part of every key head
+  const int64_t blocks = (c.n_requests * c.n_k_heads * a.parts + 7) / 8 * 8 * a.share;
   scan_kernel<DK, DELTA><<<static_cast<unsigned>(blocks < kScanGrid ? blocks : kScanGrid),
                            kScanThreads, 0, stream>>>(a);
 }
