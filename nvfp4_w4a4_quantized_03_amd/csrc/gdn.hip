@@ -997,32 +997,44 @@ struct State {
   }
 };
 
-// The n-th request of those with more than `few` tokens and its number; len 0 if
-// they are fewer.  256 at a time, whose loads do not wait for each other.
-__device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* number) {
-  const int lane = threadIdx.x & 63;
-  for (int base = 0; base < a.n_requests; base += 256) {
-    Request rq[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) rq[j] = request_of(a, min(base + 64 * j + lane, a.n_requests - 1));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool is = rq[j].len > a.few && base + 64 * j + lane < a.n_requests;
+// The requests of more than `few` tokens in their order, 64 at a time in a wave's
+// lanes, so that finding the next one mostly reads nothing: a load would wait for
+// those to LDS before it.
+struct Long {
+  Request mine;
+  int base, before;                    // of the 64: the first, and those wanted before it
+
+  __device__ __forceinline__ void start(const GdnArgs& a) {
+    base = before = 0;
+    take(a);
+  }
+  __device__ __forceinline__ void take(const GdnArgs& a) {
+    const int r = base + static_cast<int>(threadIdx.x & 63);
+    mine = request_of(a, min(r, a.n_requests - 1));
+    if (r >= a.n_requests) mine.len = 0;
+  }
+  // The n-th and its number, len 0 if they are fewer; n does not decrease.
+  __device__ __forceinline__ Request nth(const GdnArgs& a, int n, int* number) {
+    const int lane = threadIdx.x & 63;
+    for (;;) {
+      const bool is = mine.len > a.few;
       const uint64_t all = __ballot(is);
       const int count = __popcll(all);
-      if (n < count) {
-        const int at =
-            __builtin_ctzll(__ballot(is && __popcll(all & ((uint64_t(1) << lane) - 1)) == n));
-        *number = base + 64 * j + at;
-        return {__builtin_amdgcn_readlane(rq[j].first, at), __builtin_amdgcn_readlane(rq[j].len, at),
-                __builtin_amdgcn_readlane(static_cast<int>(rq[j].slot), at),
-                __builtin_amdgcn_readlane(rq[j].fresh, at) != 0};
+      if (n - before < count) {
+        const int at = __builtin_ctzll(
+            __ballot(is && __popcll(all & ((uint64_t(1) << lane) - 1)) == n - before));
+        *number = base + at;
+        return {__builtin_amdgcn_readlane(mine.first, at), __builtin_amdgcn_readlane(mine.len, at),
+                __builtin_amdgcn_readlane(static_cast<int>(mine.slot), at),
+                __builtin_amdgcn_readlane(mine.fresh, at) != 0};
       }
-      n -= count;
+      if (base + 64 >= a.n_requests) return {0, 0, 0, false};
+      before += count;
+      base += 64;
+      take(a);
     }
   }
-  return {0, 0, 0, false};
-}
+};
 
 // A wave's place in the chunks of its workgroup's items, one item behind the
 // other: chunk c of `w`, `next` the item behind.
@@ -1033,6 +1045,7 @@ __device__ __forceinline__ Request nth_request(const GdnArgs& a, int n, int* num
 // them fill the card too.
 struct Cursor {
   Scan w, next;
+  Long requests;
   int c, item;
 
   __device__ __forceinline__ void look(const GdnArgs& a) {
@@ -1041,7 +1054,7 @@ struct Cursor {
     const int at = item / a.share, unit = at * 8 + blockIdx.x % 8;
     const int n = unit / per_request, part = unit - n * per_request;
     int r = 0;
-    next.rq = nth_request(a, n, &r);
+    next.rq = requests.nth(a, n, &r);
     next.hk = part / a.parts;
     const int of_head = part % a.parts * a.share + item - at * a.share;
     next.h = next.hk * a.group + of_head / slices;
@@ -1052,6 +1065,7 @@ struct Cursor {
   }
   __device__ __forceinline__ void start(const GdnArgs& a) {
     item = blockIdx.x / 8;
+    requests.start(a);
     look(a);
     w = next;
     c = 0;
