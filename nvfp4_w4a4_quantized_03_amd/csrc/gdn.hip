@@ -1265,8 +1265,9 @@ GdnArgs args_of(const GdnCall& c) {
 }
 
 // Workgroups of the scan, one a CU, which go on to further items without a pause.
-// 32 requests of 17 to 64 tokens, 64 heads of 128 x 128 (32 items a workgroup): 153
-// us in all; 171 with 1024 workgroups, 441 where each item began anew.
+// 32 requests of 21 to 64 tokens, 64 heads of 128 x 128 (32 items a workgroup): 135
+// to 149 us in all; 441 where each item began anew (before the lengths were kept in
+// lanes: 153, with 1024 workgroups 171).
 constexpr int kScanGrid = 256;
 
 // Workgroups of four waves of the preparation, two a CU, which go on to further units
@@ -1274,7 +1275,7 @@ constexpr int kPrepareGrid = 512;
 
 // Requests of at most this many tokens are taken token after token.  Both ways take
 // as long between 21 and 36: 1, 8 and 32 requests of 64 heads of 128 x 128 17, 40 and
-// 114 us at 16 tokens and 0.5, 1.9 and 5.2 a further one; in chunks 24, 49 and 153.
+// 114 us at 16 tokens and 0.5, 1.9 and 5.2 a further one; in chunks 24, 46 and 135.
 constexpr int kFewTokens = 20;
 
 // Chunk slots of a call (first_slot), and bytes of a slot's records and decay

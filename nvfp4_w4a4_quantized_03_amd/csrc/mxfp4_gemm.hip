@@ -218,8 +218,8 @@ mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict
 // lane holds four consecutive columns of one row of Y.  Tiles leave through LDS
 // in whole 16-byte pieces.
 //
-// What bounds it is the power of the matrix cores: 32768 x 10240 x 5120 806-843 us,
-// 4.1-4.3 PFLOP/s, busy 62 % of the cycles at a clock of 1.46 GHz; a loop of the
+// What bounds it is the power of the matrix cores: 32768 x 10240 x 5120 806-889 us,
+// 3.9-4.3 PFLOP/s, busy 62 % of the cycles at a clock of 1.46 GHz; a loop of the
 // same products alone reaches 6.3-6.5 on random codes.  Rows that are no whole
 // lines (K = 5152: 2576 bytes) cost a second line for each piece: 1003 x 17536 62
 // us at K = 5120, 82 at 5152.
