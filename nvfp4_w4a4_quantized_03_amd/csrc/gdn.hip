@@ -205,11 +205,14 @@ gdn_tokens_kernel(const GdnArgs a) {
 //
 // Precision.  K, Q and V are bf16, so products with them are exact; norms,
 // decays, beta and the scale are factors of rows in binary32.  S, U, R and T are
-// binary32 and enter products as sums of bf16 numbers: S, R and T two (16 bits),
-// U into the state three (24), the diagonal of T none at all.  Outputs take S and
-// P in bf16 and U in two: roundings of the size of the output's own.  Decays are
-// added up as base-2 logarithms in binary64, so that a gate close to zero takes
-// nothing from the others.
+// binary32 and enter products as sums of bf16 numbers: S and T two (16 bits), R
+// and U into the state three (24), the diagonal of T none at all.  R in two and
+// without its second part's product with T's: scan 971 us instead of 1031 for 32768
+// tokens, the state's error 1.5 times as large (0.1 to 1.7e-6 instead of 1.1e-6);
+// S in three: 1148 and 0.7 times.  Outputs take S and P in bf16 and U in two:
+// roundings of the size of the output's own.  Decays are added up as base-2
+// logarithms in binary64, so that a gate close to zero takes nothing from the
+// others.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -684,9 +687,10 @@ prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
 // waves may write U of c and S0 of c + 1 over them.
 //
 // One prompt of 32768 tokens, 16 key and 64 value heads of 128 (an item on each
-// CU): 962 us, 1.9 a chunk.  The state waves bound it: 782 without output and
-// loader, of which their 98 products a chunk take 330 and the rest is what each
-// product waits for of the one before.  Output alone takes 401, the loads 629.
+// CU): 1031 us, 2.0 a chunk.  The state waves bound it (782 of 962 without output
+// and loader, before R had three parts): their 110 products a chunk take 370, the
+// rest is what each waits for of the one before.  Output alone takes 401, the
+// loads 629.
 constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {
@@ -931,7 +935,7 @@ struct State {
           v[t][i] = __builtin_fmaf(-a[t][i], u[t][i], bf16_value(static_cast<unsigned short>(vb[t][i])));
         u[t] = beta[t] * v[t];
       }
-      Parts<2> r0, r1;
+      Parts<3> r0, r1;
       r0.of(v[0], v[1]);
 #pragma unroll
       for (int t = 2; t < 4; ++t) {
@@ -948,13 +952,21 @@ struct State {
       for (int t = 0; t < 4; ++t) u[t] = mma(hi[tri(t, 0)], r0.p[1], u[t]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) u[t] = mma(lo[tri(t, 0)], r0.p[0], u[t]);
-      region<12, 2, 2>();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = mma(lo[tri(t, 0)], r0.p[1], u[t]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) u[t] = mma(hi[tri(t, 0)], r0.p[2], u[t]);
+      region<20, 2, 2>();
 #pragma unroll
       for (int t = 2; t < 4; ++t) u[t] = mma(hi[tri(t, 1)], r1.p[0], u[t]);
 #pragma unroll
       for (int t = 2; t < 4; ++t) u[t] = mma(hi[tri(t, 1)], r1.p[1], u[t]);
 #pragma unroll
       for (int t = 2; t < 4; ++t) u[t] = mma(lo[tri(t, 1)], r1.p[0], u[t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) u[t] = mma(lo[tri(t, 1)], r1.p[1], u[t]);
+#pragma unroll
+      for (int t = 2; t < 4; ++t) u[t] = mma(hi[tri(t, 1)], r1.p[2], u[t]);
     } else {
       values();
       factors(factor, 2);

@@ -20,10 +20,10 @@ operands as sums of bf16 numbers:
           for the other, together 2^-8 scale |q| n at most; 2^-14 of the same
           covers the binary32 and two-number roundings.
   state   two numbers leave 2^-17 of an operand at most, of either sign from
-          element to element: the state in K S, the corrected values and the
-          triangular matrix in their product, three sources whose squares add.
-          Held to sqrt(3) 2^-17 < 2^-16 of the columns' norms n, in the 2-norm
-          over a request's state.
+          element to element: the state in K S and the triangular matrix, two
+          sources whose squares add.  Held to sqrt(3) 2^-17 < 2^-16 of the
+          columns' norms n, in the 2-norm over a request's state, which leaves
+          as much for the rest.
 """
 import numpy as np
 import pytest
