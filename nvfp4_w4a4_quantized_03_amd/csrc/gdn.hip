@@ -1169,6 +1169,8 @@ scan_kernel(const GdnArgs a) {
     bool mine = false;
     at.look(a);
     for (int g = 0;; g ^= 1) {
+      // lgkmcnt(0): the loader fills the Q and P that were read last
+      __builtin_amdgcn_s_waitcnt(0xC07F);
       stage_barrier();
       u32x4 s0[DK / 32];
       f32x4 u[4];
