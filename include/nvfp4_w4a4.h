@@ -551,9 +551,9 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  *
  * The state, its sums and the gates' products are binary32.  Requests of few
  * tokens are computed in binary32 throughout, with one rounding of out; longer
- * ones in chunks, whose matrix products take the state and the corrected values
- * as sums of two or three bf16 numbers (state: relative error of some 2^-19)
- * and, for out, the state and the scores as bf16 numbers.
+ * ones in chunks, whose matrix products take binary32 operands as sums of two or
+ * three bf16 numbers (state: a relative error of some 2^-20), with one rounding of
+ * out as well.
  */
 int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                   const void* k, int64_t k_token_stride, int64_t k_head_stride,

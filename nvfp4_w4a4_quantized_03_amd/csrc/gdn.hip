@@ -207,12 +207,12 @@ gdn_tokens_kernel(const GdnArgs a) {
 // decays, beta and the scale are factors of rows in binary32.  S, U, R and T are
 // binary32 and enter products as sums of bf16 numbers: S and T two (16 bits), R
 // and U into the state three (24), the diagonal of T none at all.  R in two and
-// without its second part's product with T's: scan 971 us instead of 1031 for 32768
-// tokens, the state's error 1.5 times as large (0.1 to 1.7e-6 instead of 1.1e-6);
-// S in three: 1148 and 0.7 times.  Outputs take S and P in bf16 and U in two:
-// roundings of the size of the output's own.  Decays are added up as base-2
-// logarithms in binary64, so that a gate close to zero takes nothing from the
-// others.
+// without its second part's product with T's: the scan of 32768 tokens 6 % shorter,
+// the state's error 1.5 times as large; S in three: 11 % longer and 0.7 times.
+// Outputs take S, P and U in two, which leaves them their own rounding to bf16 (1.66e-3
+// in the 2-norm; with S and P in one number each 2.3 to 2.5e-3, and the scan of 32768
+// tokens 960 us instead of 1000).  Decays are added up as base-2 logarithms in binary64,
+// so that a gate close to zero takes nothing from the others.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -221,15 +221,15 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 64;
-// A record: the lower triangles of T (high and low parts, six operands of 1 KB
-// each) and of P (six), and four factors of each row.  Operand index of the tile
-// of rows t and the k-step s <= t / 2.
+// A record: the lower triangles of T and of P (high and low parts, six operands of
+// 1 KB each), and four factors of each row.  Operand index of the tile of rows t and
+// the k-step s <= t / 2.
 __device__ __forceinline__ constexpr int tri(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
 template <bool DELTA>
 struct Record {
   static constexpr int kT = 0;                               // high, then low
   static constexpr int kP = DELTA ? 12 * 1024 : 0;
-  static constexpr int kRows = kP + 6 * 1024;                // a, b, c, beta: 64 floats each
+  static constexpr int kRows = kP + 12 * 1024;               // a, b, c, beta: 64 floats each
   static constexpr int kBytes = kRows + 1024;
 };
 
@@ -327,9 +327,9 @@ struct Rows {
 // resemble each other.
 //
 // What it waits for bounds it.  32768 tokens, 16 key and 64 value heads of 128
-// (890 MB read and written): 250 us, 3.6 TB/s; 324 before a workgroup brought the
-// next unit's K and Q and gates while it works on one, where the inverses took
-// 115 of it, K and Q 100 and T's stores 50.
+// (1.1 GB read and written): 254 us, 4.3 TB/s (238 with P in one part).  Before a
+// workgroup brought the next unit's K and Q and gates while it works on one it took
+// 1.3 times as long: the inverses 0.35 of it, K and Q 0.31 and T's stores 0.15.
 constexpr int kPad = 68;                 // row of 64 floats in LDS
 template <int DK, bool DELTA, int WAVES>
 struct PrepareLds {
@@ -662,9 +662,11 @@ prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
         }
         __builtin_amdgcn_wave_barrier();
         operand_rows(buf, half, [&](int tile, int s, int, int, f32x4 y0, f32x4 y1) {
-          *reinterpret_cast<u32x4*>(rec + Rec::kP + tri(tile, s) * 1024 + lane * 16) =
-              u32x4{pack_bf16(y0[0], y0[1]), pack_bf16(y0[2], y0[3]), pack_bf16(y1[0], y1[1]),
-                    pack_bf16(y1[2], y1[3])};
+          Parts<2> w;
+          w.of(y0, y1);
+          uint8_t* const dst = rec + Rec::kP + tri(tile, s) * 1024 + lane * 16;
+          *reinterpret_cast<u32x4*>(dst) = w.p[0];
+          *reinterpret_cast<u32x4*>(dst + 6 * 1024) = w.p[1];
         });
         __builtin_amdgcn_wave_barrier();
       }
@@ -683,24 +685,30 @@ prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
 //
 // Barriers, two a chunk.  Behind the first of chunk c, its K, T, V and Q have
 // landed, as has P of c - 1, and S0 of c and U of c - 1 are in LDS: the output
-// waves take those to registers.  Behind the second they have, and the state
-// waves may write U of c and S0 of c + 1 over them.
+// waves take S0 to registers and finish c - 1 with P U.  Behind the second they have,
+// and the state waves may write U of c and S0 of c + 1 over them and the loader P of c
+// over that of c - 1; the state waves have read T and V of c, and the loader brings
+// those of c + 2 there.  (P of two chunks where LDS holds them, dk 64 or the plain
+// rule, and P U behind the second barrier: 1 to 4 % longer.)
 //
 // One prompt of 32768 tokens, 16 key and 64 value heads of 128 (an item on each
-// CU): 1031 us, 2.0 a chunk.  The state waves bound it (782 of 962 without output
-// and loader, before R had three parts): their 110 products a chunk take 370, the
-// rest is what each waits for of the one before.  Output alone takes 401, the
-// loads 629.
+// CU): 1000 us, 2.0 a chunk.  The state waves bound it (782 of 962 were left without
+// output and loader when S and P went to outputs, and R to U, in a part less): their
+// 110 products a chunk take 370, the rest is what each waits for of the one before.
+// The plain rule's state waves do little; there a chunk's loads bound it (one more KB
+// in ten of them took 10 % longer).
 constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {
-  // K, T, the factors of rows, V: of three chunks
-  static constexpr int kK = 0, kT = kChunk * DK * 2, kRows = kT + (DELTA ? 12 * 1024 : 0);
-  static constexpr int kV = kRows + 1024, kIn = kV + kChunk * kScanCols * 2;
-  // Q, P: of two
-  static constexpr int kQ = 0, kP = kChunk * DK * 2, kOut = kP + 6 * 1024;
-  // of each state wave: S0 (high parts, as operands), U (binary32, by tiles)
-  static constexpr int kS = 0, kU = DK / 32 * 1024, kWave = kU + 4 * 1024;
+  // of three chunks: K and the factors of rows
+  static constexpr int kK = 0, kRows = kChunk * DK * 2, kIn = kRows + 1024;
+  // of two: T and V, which a state wave has read when half a chunk is done; Q
+  static constexpr int kT = 0, kV = DELTA ? 12 * 1024 : 0, kMid = kV + kChunk * kScanCols * 2;
+  static constexpr int kQ = kChunk * DK * 2;
+  // of one: P
+  static constexpr int kP = 12 * 1024;
+  // of each state wave: S0 (two parts, as operands), U (binary32, by tiles)
+  static constexpr int kS = 0, kU = DK / 32 * 2048, kWave = kU + 4 * 1024;
 };
 
 // LDS by its own address space: with generic pointers the compiler joins the
@@ -763,8 +771,9 @@ struct ScanLoads {
                row < len ? static_cast<unsigned>(row * stride) + piece * 16 : kOutside);
     }
   }
-  // K, T, the factors of rows and V of chunk c
-  static __device__ __forceinline__ void in(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
+  // K and the factors of rows of chunk c to `lds`, T and V to `mid`
+  static __device__ __forceinline__ void in(const GdnArgs& a, const Scan& w, int c, lds_t* lds,
+                                            lds_t* mid) {
     const int lane = threadIdx.x & 63;
     const bool real = c < w.chunks;
     const int len = real ? min(w.rq.len - c * kChunk, kChunk) : 0;
@@ -776,13 +785,13 @@ struct ScanLoads {
     if constexpr (DELTA)
 #pragma unroll
       for (int n = 0; n < 12; ++n)
-        load_lds(rec, lds + Lds::kT + n * 1024, real ? Rec::kT + n * 1024 + lane * 16 : kOutside);
+        load_lds(rec, mid + Lds::kT + n * 1024, real ? Rec::kT + n * 1024 + lane * 16 : kOutside);
     load_lds(rec, lds + Lds::kRows, real ? Rec::kRows + lane * 16 : kOutside);
 #pragma unroll
     for (int n = 0; n < kValues; ++n) {
       const int at = n * 64 + lane;
       const int row = at / (kScanCols / 8), col = w.slice * kScanCols + at % (kScanCols / 8) * 8;
-      load_lds(vr, lds + Lds::kV + n * 1024,
+      load_lds(vr, mid + Lds::kV + n * 1024,
                row < len && col < a.dv ? static_cast<unsigned>(row * a.v_token) + col * 2 : kOutside);
     }
   }
@@ -790,15 +799,15 @@ struct ScanLoads {
     const bool real = c < w.chunks;
     const int len = real ? min(w.rq.len - c * kChunk, kChunk) : 0;
     const int64_t t0 = w.rq.first + static_cast<int64_t>(real ? c : 0) * kChunk;
-    rows(a.q + t0 * a.q_token + w.hk * a.q_head, a.q_token, len, lds + Lds::kQ);
+    rows(a.q + t0 * a.q_token + w.hk * a.q_head, a.q_token, len, lds);
   }
   static __device__ __forceinline__ void p(const GdnArgs& a, const Scan& w, int c, lds_t* lds) {
     const bool real = c < w.chunks;
     const __amdgpu_buffer_rsrc_t rec =
         resource(a.records + ((w.slot0 + (real ? c : 0)) * a.n_heads + w.h) * Rec::kBytes);
 #pragma unroll
-    for (int n = 0; n < 6; ++n)
-      load_lds(rec, lds + Lds::kP + n * 1024,
+    for (int n = 0; n < 12; ++n)
+      load_lds(rec, lds + n * 1024,
                real ? Rec::kP + n * 1024 + (threadIdx.x & 63) * 16 : kOutside);
   }
 };
@@ -856,7 +865,7 @@ struct State {
   using Lds = ScanLds<DK, DELTA>;
   static constexpr int kTiles = DK / 16, kSteps = DK / 32;
   f32x4 st[kTiles];
-  Parts<DELTA ? 2 : 1> x[kSteps];
+  Parts<2> x[kSteps];
 
   __device__ __forceinline__ void parts(int from, int to) {
 #pragma unroll
@@ -867,12 +876,15 @@ struct State {
   __device__ __forceinline__ void leave(lds_t* xc) const {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
-      lds_write(xc + Lds::kS + s * 1024 + (threadIdx.x & 63) * 16, x[s].p[0]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        lds_write(xc + Lds::kS + (2 * s + n) * 1024 + (threadIdx.x & 63) * 16, x[s].p[n]);
   }
 
   // From the state before a chunk to the one after it; U goes to xc behind the
   // barrier.
-  __device__ __forceinline__ void chunk(float decay, int wave, const lds_t* in, lds_t* xc) {
+  __device__ __forceinline__ void chunk(float decay, int wave, const lds_t* in, const lds_t* mid,
+                                        lds_t* xc) {
     const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
     const lds_t* const rows = in + Lds::kRows;
     f32x4 u[4], v[4], factor[4], last[4];
@@ -881,7 +893,7 @@ struct State {
     auto values = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        vb[t] = read_tr(in + Lds::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
+        vb[t] = read_tr(mid + Lds::kV + (32 * (t / 2) + 8 * g4 + 4 * (t % 2) + (lr >> 2)) * (kScanCols * 2) +
                         wave * 32 + (lr & 3) * 8);
     };
     auto columns = [&](int s) __attribute__((always_inline)) {
@@ -914,8 +926,8 @@ struct State {
         if (s == kSteps - 1) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            hi[tri(t, 0)] = operand_at(in + Lds::kT, tri(t, 0));
-            lo[tri(t, 0)] = operand_at(in + Lds::kT, 6 + tri(t, 0));
+            hi[tri(t, 0)] = operand_at(mid + Lds::kT, tri(t, 0));
+            lo[tri(t, 0)] = operand_at(mid + Lds::kT, 6 + tri(t, 0));
           }
           factors(beta, 3);
         }
@@ -939,8 +951,8 @@ struct State {
       r0.of(v[0], v[1]);
 #pragma unroll
       for (int t = 2; t < 4; ++t) {
-        hi[tri(t, 1)] = operand_at(in + Lds::kT, tri(t, 1));
-        lo[tri(t, 1)] = operand_at(in + Lds::kT, 6 + tri(t, 1));
+        hi[tri(t, 1)] = operand_at(mid + Lds::kT, tri(t, 1));
+        lo[tri(t, 1)] = operand_at(mid + Lds::kT, 6 + tri(t, 1));
       }
       factors(factor, 2);
       __builtin_amdgcn_sched_barrier(0);
@@ -981,7 +993,9 @@ struct State {
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) st[t] *= decay;
     if constexpr (DELTA) region<6, 10, 0>();
-    // the output wave has taken S0 of this chunk and U of the one before
+    // The output wave has taken S0 of this chunk and U of the one before; lgkmcnt(0):
+    // the loader fills T and V, which this wave has read.
+    __builtin_amdgcn_s_waitcnt(0xC07F);
     stage_barrier();
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -1107,15 +1121,17 @@ __global__ void __launch_bounds__(512)
 scan_kernel(const GdnArgs a) {
   using Lds = ScanLds<DK, DELTA>;
   using Loads = ScanLoads<DK, DELTA>;
-  __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], out_[2 * Lds::kOut],
-      xc_[2 * Lds::kWave];
+  __shared__ __attribute__((aligned(1024))) uint8_t in_[kRing * Lds::kIn], mid_[2 * Lds::kMid],
+      q_[2 * Lds::kQ], p_[Lds::kP], xc_[2 * Lds::kWave];
   const int lane = threadIdx.x & 63, lr = lane & 15, g4 = lane >> 4;
   // 0, 1: state, 2, 3: output, 4: loader.  The first wave, with which the fifth
   // shares a SIMD, is not a state wave (1077 -> 1004 us).
   const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wave = id == 0 ? 2 : id < 3 ? id - 1 : id;
   lds_t* const in = (lds_t*)in_;
-  lds_t* const out = (lds_t*)out_;
+  lds_t* const mid = (lds_t*)mid_;
+  lds_t* const queries = (lds_t*)q_;
+  lds_t* const scores = (lds_t*)p_;
   lds_t* const xc = (lds_t*)xc_;
   Cursor at;
   at.start(a);
@@ -1123,7 +1139,7 @@ scan_kernel(const GdnArgs a) {
   if (wave < 2) {
     State<DK, DELTA> s;
     float of_64 = 0.0f;                            // decays of 64 chunks, one a lane
-    for (;;) {
+    for (int g = 0;; g ^= 1) {
       // the last slice may have one wave's columns only
       const int col = at.w.slice * kScanCols + wave * 16;
       const unsigned place_in = col < a.dv ? (8 * g4 * a.dv + col + lr) * 4 : kOutside;
@@ -1147,7 +1163,7 @@ scan_kernel(const GdnArgs a) {
       stage_barrier();
       if (!at.valid()) break;
       const float decay = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(of_64), at.c & 63));
-      s.chunk(decay, wave, in + place * Lds::kIn, xc + wave * Lds::kWave);
+      s.chunk(decay, wave, in + place * Lds::kIn, mid + g * Lds::kMid, xc + wave * Lds::kWave);
       place = place == kRing - 1 ? 0 : place + 1;
       if (at.c == at.w.chunks - 1) {
         const __amdgpu_buffer_rsrc_t state = state_of<DK>(a, at.w);
@@ -1169,19 +1185,18 @@ scan_kernel(const GdnArgs a) {
     bool mine = false;
     at.look(a);
     for (int g = 0;; g ^= 1) {
-      // lgkmcnt(0): the loader fills the Q and P that were read last
+      // lgkmcnt(0): the loader fills the Q that was read last
       __builtin_amdgcn_s_waitcnt(0xC07F);
       stage_barrier();
-      u32x4 s0[DK / 32];
-      f32x4 u[4];
+      u32x4 s0[DK / 32][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) u[t] = __builtin_bit_cast(f32x4, operand_at(from + Lds::kU, t));
+      for (int s = 0; s < DK / 32; ++s)
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s) s0[s] = operand_at(from + Lds::kS, s);
-      __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
-      stage_barrier();
+        for (int n = 0; n < 2; ++n) s0[s][n] = operand_at(from + Lds::kS, 2 * s + n);
       if (len > 0) {
-        const lds_t* const p = out + (g ^ 1) * Lds::kOut + Lds::kP;
+        f32x4 u[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) u[t] = __builtin_bit_cast(f32x4, operand_at(from + Lds::kU, t));
         // it ends with the rows that there are
         const __amdgpu_buffer_rsrc_t rsrc =
             resource(rows, mine ? static_cast<unsigned>(len * a.out_token) : 0);
@@ -1189,10 +1204,17 @@ scan_kernel(const GdnArgs a) {
         for (int s = 0; s < 2; ++s) {
           Parts<DELTA ? 2 : 1> y;                  // the plain rule's U is bf16
           y.of(u[2 * s], u[2 * s + 1]);
+          u32x4 p[4][2];
 #pragma unroll
-          for (int i = 0; i < (DELTA ? 2 : 1); ++i)
+          for (int t = 2 * s; t < 4; ++t)
 #pragma unroll
-            for (int t = 2 * s; t < 4; ++t) o[t] = mma(operand_at(p, tri(t, s)), y.p[i], o[t]);
+            for (int n = 0; n < 2; ++n) p[t][n] = operand_at(scores, 6 * n + tri(t, s));
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < (DELTA && n == 0 ? 2 : 1); ++i)
+#pragma unroll
+              for (int t = 2 * s; t < 4; ++t) o[t] = mma(p[t][n], y.p[i], o[t]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -1203,14 +1225,24 @@ scan_kernel(const GdnArgs a) {
                 bf16_bits(o[t][i]), rsrc, static_cast<unsigned>(row * a.out_token) + lr * 2, 0, 0);
           }
       }
+      // lgkmcnt(0): S0 and U are taken, which the state waves write over, and P, which
+      // the loader fills
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      stage_barrier();
       if (!at.valid()) break;
-      const lds_t* const q = out + g * Lds::kOut + Lds::kQ;
+      const lds_t* const q = queries + g * Lds::kQ;
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int s = 0; s < DK / 32; ++s)
+      for (int s = 0; s < DK / 32; ++s) {
+        u32x4 x[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) o[t] = mma(left_rows<DK>(q, t, s), s0[s], o[t]);
+        for (int t = 0; t < 4; ++t) x[t] = left_rows<DK>(q, t, s);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) o[t] = mma(x[t], s0[s][n], o[t]);
+      }
 #pragma unroll
       for (int t = 0; t < 4; ++t) o[t] *= row_factors(in + place * Lds::kIn + Lds::kRows, 1, t);
       place = place == kRing - 1 ? 0 : place + 1;
@@ -1225,14 +1257,14 @@ scan_kernel(const GdnArgs a) {
     // two chunks, one and none behind `at`
     Scan w0 = at.w, w1;
     int c0 = 0, c1;
-    Loads::q(a, at.w, 0, out);
-    Loads::in(a, at.w, 0, in);
+    Loads::q(a, at.w, 0, queries);
+    Loads::in(a, at.w, 0, in, mid);
     if (at.w.chunks == 1) at.look(a);
     bool looked = at.w.chunks == 1;
     if (at.step()) looked = false;
     w1 = at.w;
     c1 = at.c;
-    Loads::in(a, w1, c1, in + Lds::kIn);
+    Loads::in(a, w1, c1, in + Lds::kIn, mid + Lds::kMid);
     if (!looked) at.look(a);
     if (at.step()) at.look(a);
     place = 2;
@@ -1240,12 +1272,12 @@ scan_kernel(const GdnArgs a) {
       // but for K, T and V of the next chunk, all that was asked for has landed
       __builtin_amdgcn_s_waitcnt(kVmcntKeepOf(Loads::kIn));
       stage_barrier();
-      Loads::q(a, w1, c1, out + (g ^ 1) * Lds::kOut);
-      Loads::p(a, w0, c0, out + g * Lds::kOut);
+      Loads::q(a, w1, c1, queries + (g ^ 1) * Lds::kQ);
       // the rest is not needed that soon, and would hold up the second barrier
       // (plain rule, 7 prompts: 42 -> 37 us)
       stage_barrier();
-      Loads::in(a, at.w, at.c, in + place * Lds::kIn);
+      Loads::p(a, w0, c0, scores);
+      Loads::in(a, at.w, at.c, in + place * Lds::kIn, mid + g * Lds::kMid);
       place = place == kRing - 1 ? 0 : place + 1;
       if (c0 >= w0.chunks) break;
       w0 = w1;
