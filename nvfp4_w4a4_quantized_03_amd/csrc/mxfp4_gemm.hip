@@ -10,6 +10,7 @@
 
 #include "gemm_common.h"
 #include "internal.h"
+#include "mxfp4_plan.h"
 
 namespace nvfp4 {
 namespace {
@@ -611,95 +612,39 @@ hipError_t launch_stream(const uint8_t* s_codes, const uint8_t* s_scales, int64_
   return hipGetLastError();
 }
 
-// One round of workgroups of eight waves, one a CU, where some SF gives it (the
-// smallest does: 32 x 10240 x 5120 10.7 us with 214 workgroups of 48 rows, 15.8
-// with 320 of 32 and 17.5 with 640 of 16; 32 x 5120 x 5120 8.3 with 32 rows, 9.9
-// with 48); otherwise many of four waves with few loads in flight, several a CU
-// (32768 x 64 x 5120 39 us against 47 with eight waves, 64 x 10240 x 5120 19
-// against 23).
 template <int LF, bool RAGGED, bool S_IS_B>
-hipError_t stream_rows(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
-                       const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt,
-                       int64_t ldo, hipStream_t st) {
-  constexpr int kMost = LF == 1 ? 4 : LF == 2 ? 3 : 2;      // what the registers hold
-  const int64_t sf = (s_rows + 16 * 256 - 1) / (16 * 256);
-  if (sf <= 1)
+hipError_t stream_of(const Mxfp4Plan& p, const uint8_t* sc, const uint8_t* ss, int64_t s_rows,
+                     const uint8_t* lc, const uint8_t* ls, int64_t l_rows, int64_t k, void* out,
+                     int dt, int64_t ldo, hipStream_t st) {
+  if (p.waves == 4)
+    return launch_stream<4, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  if (p.sf == 1)
     return launch_stream<8, 1, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  if (sf <= 2)
-    return launch_stream<8, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  if constexpr (kMost >= 3)
-    if (sf <= 3)
+  if constexpr (LF <= 2)
+    if (p.sf == 3)
       return launch_stream<8, 3, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  if constexpr (kMost >= 4)
-    if (sf <= 4)
+  if constexpr (LF == 1)
+    if (p.sf == 4)
       return launch_stream<8, 4, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  return launch_stream<4, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-}
-
-template <bool RAGGED, bool S_IS_B>
-hipError_t stream_of(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
-                     const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt, int64_t ldo,
-                     hipStream_t st) {
-  if (l_rows <= 16)
-    return stream_rows<1, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  if (l_rows <= 32)
-    return stream_rows<2, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-  return stream_rows<4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
-}
-
-// Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two).  Times of a round
-// of 256 CUs at K = 5120, full and partly filled: 42 and 30 us for the large
-// tile, 27 and, for at most one workgroup a CU, 16.5 for the small one; the
-// sums over a call's rounds choose.  (1003 x 17536 76 us with large, 69 with
-// small tiles; 300 x 5120 28 and 16; 1024 x 10240 32 and 41; 4096 x 12288 122
-// and 160.  Large tiles for the whole rounds and small ones for the rest in a
-// second launch: 1003 x 17536 66 us against 62, 8192 x 8448 184 against 181, 1500 x
-// 12288 59 against 63.)
-bool large_tiles(int64_t m, int64_t n) {
-  const double large = static_cast<double>((m + 255) / 256) * ((n + 255) / 256);
-  const double small = static_cast<double>((m + 127) / 128) * ((n + 127) / 128);
-  const double fl = __builtin_floor(large / 256), fs = __builtin_floor(small / 512);
-  const double rl = large - 256 * fl, rs = small - 512 * fs;
-  return 42.0 * fl + (rl > 0 ? 30.0 : 0.0) <=
-         27.0 * fs + (rs > 256 ? 27.0 : rs > 0 ? 16.5 : 0.0);
-}
-
-// Products whose tiles would leave most CUs idle while each goes through a long K:
-// one round of streaming workgroups, of 16 or 32 rows of the longer side against 64
-// of the other, whose waves share K.  K = 5120, tiles and streaming: 128 x 128 11.4
-// and 9.5 us, 457 x 312 12.1 and 9.7, 128 x 4096 17.8 and 11.9, 700 x 700 22.3 and
-// 11.9; 128 x 2048 x 17408 52 and 27.  Shorter K: 512 x 1000 x 2048 7.1 and 6.9, 512
-// x 512 x 1024 5.0 and 6.3.
-int64_t small_groups(int64_t m, int64_t n, int sf) {
-  const int64_t s = m <= n ? n : m, l = m <= n ? m : n;
-  return (s + 16 * sf - 1) / (16 * sf) * ((l + 63) / 64);
-}
-bool small_product(int64_t m, int64_t n, int64_t k) {
-  return k >= 2048 && m < (1 << 16) && n < (1 << 16) && small_groups(m, n, 2) <= 256;
-}
-template <bool RAGGED, bool S_IS_B>
-hipError_t stream_small(const uint8_t* sc, const uint8_t* ss, int64_t s_rows, const uint8_t* lc,
-                        const uint8_t* ls, int64_t l_rows, int64_t k, void* out, int dt, int64_t ldo,
-                        hipStream_t st) {
-  return small_groups(s_rows, l_rows, 1) <= 256
-             ? launch_stream<8, 1, 4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st)
-             : launch_stream<8, 2, 4, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
+  return launch_stream<8, 2, LF, RAGGED, S_IS_B>(sc, ss, s_rows, lc, ls, l_rows, k, out, dt, ldo, st);
 }
 
 template <bool RAGGED>
-hipError_t gemm_of(const uint8_t* ac, const uint8_t* as, int64_t m, const uint8_t* bc,
-                   const uint8_t* bs, int64_t n, int64_t k, void* out, int dt, int64_t ldo,
-                   hipStream_t st) {
-  if (m <= 64 && (n > 64 || m <= n))
-    return stream_of<RAGGED, true>(bc, bs, n, ac, as, m, k, out, dt, ldo, st);
-  if (n <= 64)
-    return stream_of<RAGGED, false>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
-  if (small_product(m, n, k))
-    return m <= n ? stream_small<RAGGED, true>(bc, bs, n, ac, as, m, k, out, dt, ldo, st)
-                  : stream_small<RAGGED, false>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
-  return large_tiles(m, n)
-             ? launch_tiled<2, 4, 4, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st)
-             : launch_tiled<2, 2, 2, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+hipError_t gemm_of(const Mxfp4Plan& p, const uint8_t* ac, const uint8_t* as, int64_t m,
+                   const uint8_t* bc, const uint8_t* bs, int64_t n, int64_t k, void* out, int dt,
+                   int64_t ldo, hipStream_t st) {
+  if (p.tile == 256)
+    return launch_tiled<2, 4, 4, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  if (p.tile == 128)
+    return launch_tiled<2, 2, 2, 2, RAGGED>(ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  if (p.s_is_b) {
+    if (p.lf == 1) return stream_of<1, RAGGED, true>(p, bc, bs, n, ac, as, m, k, out, dt, ldo, st);
+    if (p.lf == 2) return stream_of<2, RAGGED, true>(p, bc, bs, n, ac, as, m, k, out, dt, ldo, st);
+    return stream_of<4, RAGGED, true>(p, bc, bs, n, ac, as, m, k, out, dt, ldo, st);
+  }
+  if (p.lf == 1) return stream_of<1, RAGGED, false>(p, ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  if (p.lf == 2) return stream_of<2, RAGGED, false>(p, ac, as, m, bc, bs, n, k, out, dt, ldo, st);
+  return stream_of<4, RAGGED, false>(p, ac, as, m, bc, bs, n, k, out, dt, ldo, st);
 }
 
 }  // namespace
@@ -707,10 +652,11 @@ hipError_t gemm_of(const uint8_t* ac, const uint8_t* as, int64_t m, const uint8_
 hipError_t launch_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                              const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
                              void* out, int out_dtype, int64_t ldo, hipStream_t stream) {
-  return k % 128 == 0 ? gemm_of<false>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
-                                       out_dtype, ldo, stream)
-                      : gemm_of<true>(a_codes, a_scales, m, b_codes, b_scales, n, k, out,
-                                      out_dtype, ldo, stream);
+  const Mxfp4Plan p = mxfp4_plan(m, n, k);
+  return p.ragged ? gemm_of<true>(p, a_codes, a_scales, m, b_codes, b_scales, n, k, out, out_dtype,
+                                  ldo, stream)
+                  : gemm_of<false>(p, a_codes, a_scales, m, b_codes, b_scales, n, k, out, out_dtype,
+                                   ldo, stream);
 }
 
 }  // namespace nvfp4
