@@ -554,6 +554,10 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  * ones in chunks, whose matrix products take binary32 operands as sums of two or
  * three bf16 numbers (state: a relative error of some 2^-20), with one rounding of
  * out as well.
+ * Inputs should be finite.  Of a request that is computed in chunks (of 64 tokens
+ * each from its first), an infinity or NaN in a token's k, v or gates may make
+ * rows before it NaN, back to the start of its chunk; token after token, only rows
+ * from it on.  Other requests are not touched by it.
  */
 int gdn_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                   const void* k, int64_t k_token_stride, int64_t k_head_stride,

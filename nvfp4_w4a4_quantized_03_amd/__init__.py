@@ -877,7 +877,9 @@ def gdn_attention(q, k, v, alpha, beta, state, cu_lens, max_len, slots=None,
     one, None for the first n_requests; one outside the state leaves its
     request out; cached_lens: int32 [n_requests], a request with 0 starts from
     an empty state (None: all continue).  scale defaults to 1 / sqrt(dk);
-    normalize divides q and k by sqrt(sum x^2 + 1e-6) first.  Returns
+    normalize divides q and k by sqrt(sum x^2 + 1e-6) first.  Inputs should be
+    finite: what is not may make rows before its token NaN, back to the start
+    of its chunk of 64 tokens, and no other request's.  Returns
     [n_tokens, n_heads, dv] bfloat16 (or fills out); rows of no request are not
     written."""
     qp = _head_rows(q, "q")

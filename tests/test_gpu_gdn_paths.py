@@ -149,3 +149,39 @@ def test_state_keeps_24_bits_within_a_chunk(i, j, dk):
     got = state.to(DEV)
     nv.gdn_attention(**c, state=got, cu_lens=gdn.i32([0, tokens]), max_len=tokens, scale=1.0)
     assert np.array_equal(got[0].double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "alpha", "beta"])
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+def test_what_is_not_finite_stays_behind_its_chunk(which, value):
+    """A non-finite input of one token: token after token, earlier rows stay; in
+    chunks, those of earlier chunks (a query's reaches its own row only)."""
+    _say("finite", which, value)
+    n, at = 200, 150
+    c = gdn.build(np.random.default_rng(3), [n], 2, 4, 128, 64)
+    clean, first = nv.gdn_attention(**dict(c, state=c["state"].clone())), c["state"].clone()
+    bad = dict(c, state=first.clone())
+    bad[which] = c[which].clone()
+    bad[which][at, 1] = float(value)
+    out = nv.gdn_attention(**bad)
+    assert torch.equal(out[:at // 64 * 64], clean[:at // 64 * 64])
+    if which == "q":
+        others = [t for t in range(n) if t != at]
+        assert torch.equal(out[others], clean[others])
+        assert torch.equal(bad["state"][int(c["slots"][0])], nv_state(c))
+    else:
+        assert not bool(out[at:].isfinite().all())
+    # the same tokens before it in calls of few tokens
+    m = few()
+    head = {x: c[x][:m] for x in ("q", "k", "v", "alpha", "beta")}
+    tail = dict(head, **{which: head[which].clone()})
+    tail[which][m - 3, 1] = float(value)
+    outs = [nv.gdn_attention(state=first.clone(), cu_lens=gdn.i32([0, m]), max_len=m,
+                             slots=c["slots"], normalize=True, **x) for x in (head, tail)]
+    assert torch.equal(outs[0][:m - 3], outs[1][:m - 3])
+
+
+def nv_state(c):
+    state = c["state"].clone()
+    nv.gdn_attention(**dict(c, state=state))
+    return state[int(c["slots"][0])]
