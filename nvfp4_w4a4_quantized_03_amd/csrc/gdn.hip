@@ -23,7 +23,6 @@ namespace nvfp4 {
 namespace {
 
 typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
-typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNormEps = 1e-6f;
@@ -689,14 +688,14 @@ prepare_kernel(const GdnArgs a, int k_heads, int units, int workgroups) {
 // and the state waves may write U of c and S0 of c + 1 over them and the loader P of c
 // over that of c - 1; the state waves have read T and V of c, and the loader brings
 // those of c + 2 there.  (P of two chunks where LDS holds them, dk 64 or the plain
-// rule, and P U behind the second barrier: 1 to 4 % longer.)
+// rule, and P U behind the second barrier: 2 to 5 % longer.)
 //
 // One prompt of 32768 tokens, 16 key and 64 value heads of 128 (an item on each
 // CU): 1000 us, 2.0 a chunk.  The state waves bound it (782 of 962 were left without
 // output and loader when S and P went to outputs, and R to U, in a part less): their
 // 110 products a chunk take 370, the rest is what each waits for of the one before.
-// The plain rule's state waves do little; there a chunk's loads bound it (one more KB
-// in ten of them took 10 % longer).
+// The plain rule's state waves do little; there a chunk's loads bound it, 21 bytes a
+// cycle to LDS (with P in one part, 43 KB instead of 49, it took 12 % less).
 constexpr int kScanCols = 32, kRing = 3, kScanThreads = 320;
 template <int DK, bool DELTA>
 struct ScanLds {

@@ -219,11 +219,14 @@ mxfp4_gemm_stream(const uint8_t* __restrict__ s_codes, const uint8_t* __restrict
 // lane holds four consecutive columns of one row of Y.  Tiles leave through LDS
 // in whole 16-byte pieces.
 //
-// What bounds it is the power of the matrix cores: 32768 x 10240 x 5120 806-889 us,
-// 3.9-4.3 PFLOP/s, busy 62 % of the cycles at a clock of 1.46 GHz; a loop of the
-// same products alone reaches 6.3-6.5 on random codes.  Rows that are no whole
-// lines (K = 5152: 2576 bytes) cost a second line for each piece: 1003 x 17536 62
-// us at K = 5120, 82 at 5152.
+// What bounds it is the clock that its power leaves and, in equal part, waits:
+// 32768 x 10240 x 5120 on random codes 793-850 us (3.9-4.3 PFLOP/s), matrix cores
+// busy 62 % of the cycles at 1.58 GHz; on constant codes, which switch less, 688 us,
+// 55 % at 2.15 GHz.  LDS reads take 31 % of the cycles, waits for loads and the
+// barrier 28 % of the waves' time.  A loop of the same products alone reaches
+// 6.3-6.5 PFLOP/s on random codes.  Rows that are no whole lines (K = 5152: 2576
+// bytes) cost a second line for each piece: 1003 x 17536 70 us at K = 5120, 89 at
+// 5152.
 constexpr int kBK = 256;
 constexpr int kRowBytes = kBK / 2;
 
@@ -236,7 +239,6 @@ template <int ROWS, int NW, bool RAGGED>
 struct Loads {
   static constexpr int kCodes = ROWS / 8 / NW;
   static constexpr int kPerWave = (ROWS + 64 * NW - 1) / (64 * NW);    // rows / 64 of scales
-  static constexpr int kScales = kPerWave * (RAGGED ? 2 : 1);
   static constexpr int kRows = kPerWave * NW * 64;                     // places in LDS
   static constexpr int kScaleBytes = kRows * (RAGGED ? 20 : 16);
   static_assert(ROWS % (16 * NW) == 0, "rows split evenly over the waves");

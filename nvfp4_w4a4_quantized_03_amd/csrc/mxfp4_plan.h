@@ -17,11 +17,13 @@ struct Mxfp4Plan {
 // Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two).  Times of a round
 // of 256 CUs at K = 5120, full and partly filled: 42 and 30 us for the large
 // tile, 27 and, for at most one workgroup a CU, 16.5 for the small one; the
-// sums over a call's rounds choose.  (1003 x 17536 76 us with large, 69 with
-// small tiles; 300 x 5120 28 and 16; 1024 x 10240 32 and 41; 4096 x 12288 122
-// and 160.  Large tiles for the whole rounds and small ones for the rest in a
-// second launch: 1003 x 17536 66 us against 62, 8192 x 8448 184 against 181, 1500 x
-// 12288 59 against 63.)
+// sums over a call's rounds choose.  (1003 x 17536 72 us with large, 68 with
+// small tiles; 300 x 5120 28 and 17; 1024 x 10240 35 and 44; 4096 x 12288 125
+// and 163; 1500 x 12288 69 and 68.  Only the times' ratio counts, which other K, ragged
+// rows and float32 outputs keep near enough: 1003 x 17536 at K = 1024 22.6 and 20.0, at
+// 5152 to float32 104 and 89; K = 1024: 4096 x 12288 41 and 48, 1024 x 10240 11.0 and
+// 13.2.  Large tiles for the whole rounds and small ones for the rest in a second
+// launch: 1003 x 17536 6 % longer, 8192 x 8448 2 %, 1500 x 12288 7 % less.)
 inline bool large_tiles(int64_t m, int64_t n) {
   const double large = static_cast<double>((m + 255) / 256) * ((n + 255) / 256);
   const double small = static_cast<double>((m + 127) / 128) * ((n + 127) / 128);
