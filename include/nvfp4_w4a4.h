@@ -552,8 +552,8 @@ int mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
  * The state, its sums and the gates' products are binary32.  Requests of few
  * tokens are computed in binary32 throughout, with one rounding of out; longer
  * ones in chunks, whose matrix products take binary32 operands as sums of two or
- * three bf16 numbers (state: a relative error of some 2^-20), with one rounding of
- * out as well.
+ * three bf16 numbers (state: a relative error of some 2^-20, 2^-19 at worst), with
+ * one rounding of out as well.
  * Inputs should be finite.  Of a request that is computed in chunks (of 64 tokens
  * each from its first), an infinity or NaN in a token's k, v or gates may make
  * rows before it NaN, back to the start of its chunk; token after token, only rows
